@@ -78,14 +78,19 @@ typedef enum {
     GNQ_ERR_MODE = 4,  /* unknown quantization mode, or k out of range      */
     GNQ_ERR_ALIAS = 5, /* x == residual, or y aliases x or residual         */
     GNQ_ERR_ALIGN = 6, /* a pointer or the partial stride is misaligned     */
-    GNQ_ERR_CUDA = 7   /* the CUDA runtime reported an error at launch (the
+    GNQ_ERR_CUDA = 7,  /* the CUDA runtime reported an error at launch (the
                           runtime's last-error state is cleared, so the
                           caller's own later checks do not see it)         */
+    GNQ_ERR_MEMORY = 8 /* a buffer that must be device memory is not       */
 } gnq_status;
 
-typedef enum { GNQ_BF16 = 0, GNQ_FP16 = 1 } gnq_dtype;
+/* Activations are GNQ_BF16 or GNQ_FP16; GNQ_FP32 and GNQ_E4M3 are further
+ * output types of nvfp4_linear and gnq_nvfp4_dequantize. */
+typedef enum { GNQ_BF16 = 0, GNQ_FP16 = 1, GNQ_FP32 = 2, GNQ_E4M3 = 3 } gnq_dtype;
 
 typedef enum { GNQ_FP8 = 0, GNQ_NVFP4 = 1, GNQ_MXFP8 = 2 } gnq_mode;
+
+typedef enum { GNQ_SILU = 1, GNQ_GELU_TANH = 2 } gnq_act;
 
 /*
  * Residual add + Gemma RMSNorm, no quantization
@@ -163,6 +168,101 @@ int add_rms_norm_quant(const void *x_parts, int k, int64_t part_stride,
                        const float *scale, int mode, int write_y, void *q,
                        void *block_scale, void *y, int64_t M, int64_t H,
                        int dtype, void *stream);
+
+/*
+ * Sandwich norm: the norm after a block, its gate and residual scale, the
+ * residual add, and the norm before the next block with the quantization for
+ * that block's first linear, in one pass:
+ *
+ *     u = x * rsqrt(mean(x^2) + eps) * (1 + w_post)    (u = x if w_post is NULL)
+ *     h = dtype(residual + residual_scale * gate * u)  (one rounding; gate 1 if NULL)
+ *     y = dtype(h * rsqrt(mean(h^2) + eps) * (1 + w))
+ *     q = quant(y)
+ *
+ *   x            (M, H) the block's output, read only.
+ *   residual     (M, H), required.
+ *   residual_out (M, H) receives h; NULL or `residual` itself: updated in
+ *                place.  Must not overlap x, the gate or (in part) residual.
+ *   w_post, w    (H,) Gemma weights; w_post may be NULL.
+ *   gate         NULL, (H,) with gate_stride 0 (one gate per channel), or
+ *                (M, H) with rows gate_stride elements apart (>= H, a multiple
+ *                of 8); of the activation type, 16-byte aligned.
+ *   mode, write_y, scale, q, block_scale, y   as for
+ *                gemma_add_rms_norm_quant_parts (mode -1: y only).
+ * A row of more than 8192 elements (NVFP4: 16384) is split evenly over 2, 4 or
+ * 8 CTAs, in multiples of 8 elements (MXFP8: 32, NVFP4: 64); an H that does
+ * not divide so is GNQ_ERR_SHAPE.
+ */
+int gemma_sandwich_norm_quant(const void *x, void *residual,
+                              void *residual_out, const void *w_post,
+                              const void *w, const void *gate,
+                              int64_t gate_stride, float residual_scale,
+                              float eps, const float *scale, int mode,
+                              int write_y, void *q, void *block_scale, void *y,
+                              int64_t M, int64_t H, int dtype, void *stream);
+
+/*
+ * Quantization of a 16-bit matrix: q = quant(x), the codes and scales that
+ * the norm entry points give for a y equal to x.
+ *   x          (M, H), rows row_stride elements apart (>= H, a multiple of 8).
+ *   scale, mode, q, block_scale   as for gemma_add_rms_norm_quant.
+ */
+int gnq_quantize(const void *x, int64_t row_stride, const float *scale,
+                 int mode, void *q, void *block_scale, int64_t M, int64_t H,
+                 int dtype, void *stream);
+
+/*
+ * The gated activation between the products of an MLP, and the quantization
+ * for the second: y = dtype(act(gate) * up) in fp32, rounded once; q = quant(y).
+ *   x          (M, 2H): gate in the first H columns, up in the last; rows
+ *              row_stride elements apart (>= 2H, a multiple of 8).
+ *   act        GNQ_SILU: g / (1 + exp(-g)); GNQ_GELU_TANH: g/2 (1 + tanh(
+ *              sqrt(2/pi) (g + 0.044715 g^3))).
+ *   mode, write_y, scale, q, block_scale, y   as for
+ *              gemma_add_rms_norm_quant_parts (mode -1: y only).
+ */
+int gated_act_quant(const void *x, int64_t row_stride, int act,
+                    const float *scale, int mode, int write_y, void *q,
+                    void *block_scale, void *y, int64_t M, int64_t H,
+                    int dtype, void *stream);
+
+/*
+ * NVFP4 codes and swizzled block scales back to plain values:
+ * out = type(code * (block scale / g)), the quotient and the product each
+ * rounded to fp32.
+ *   scale      device pointer to the global scale g, or NULL for 1.
+ *   out        (M, K) of out_type GNQ_BF16, GNQ_FP16, GNQ_FP32, or GNQ_E4M3
+ *              (saturating).
+ */
+int gnq_nvfp4_dequantize(const void *q, const void *block_scale,
+                         const float *scale, void *out, int64_t M, int64_t K,
+                         int out_type, void *stream);
+
+/*
+ * Product of an NVFP4 activation with an NVFP4 weight:
+ *
+ *     y[m, n] = type(alpha * sum_k a[m, k] w[n, k] + bias[n])
+ *
+ * a and w being the codes times their block scales (products exact, sums in
+ * fp32), alpha usually 1 / (global scale of a * global scale of w).
+ *   q, block_scale      (M, K/2) packed codes and the swizzled scales of the
+ *                       activation, as the NVFP4 mode of the other entry
+ *                       points writes them; scale rows m >= M are read but
+ *                       affect nothing.
+ *   w_q, w_block_scale  (N, K/2) and the swizzled (round_up(N,128), K/16)
+ *                       scales of the weight, one row per output.
+ *   alpha               device pointer to ONE fp32.
+ *   bias                (N,) or NULL; of bias_type GNQ_BF16 or GNQ_FP16,
+ *                       which must be out_type unless that is GNQ_FP32.
+ *   y                   (M, N) of out_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
+ * K is a multiple of 64, at most 65536; M and N are any sizes.  The codes and
+ * block scales must be in device memory (GNQ_ERR_MEMORY) and 16-byte aligned,
+ * as must y.
+ */
+int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
+                 const void *w_block_scale, const float *alpha,
+                 const void *bias, void *y, int64_t M, int64_t N, int64_t K,
+                 int out_type, int bias_type, void *stream);
 
 /* Human-readable text of a gnq_status (static storage, never NULL). */
 const char *gnq_status_string(int status);
@@ -246,10 +346,10 @@ int gnq_set_constant_weights(int enable);
 
 /*
  * Test hook for the failure path of the bounded waits (off by default).
- * With enable = 1, later launches of the persistent streaming kernel in this
- * process announce 16 bytes more per row than their copies deliver and give
+ * With enable = 1, later launches of the persistent streaming kernel and of
+ * nvfp4_linear in this process announce 16 bytes more per row than their copies deliver and give
  * a wait at most ~2^20 clock cycles, so each CTA's wait for its first row
- * gives up: the kernel sets bit 1 of the device error word, completes each
+ * (its first stage of K) gives up: the kernel sets bit 1 of the device error word, completes each
  * outstanding barrier with one more valid 16-byte copy (from w into its own
  * shared memory, so every copy has landed before it returns), and returns
  * without writing any output.  Nothing outside the call's own buffers is

@@ -8,11 +8,16 @@ from ._binding import (  # noqa: F401
     add_rms_norm_quant,
     alloc_outputs,
     encode_e4m3_e2m1,
+    gated_act_quant,
     gemma_add_rms_norm,
     gemma_add_rms_norm_quant,
     gemma_add_rms_norm_quant_parts,
+    gemma_sandwich_norm_quant,
     inject_wait_timeout,
     library_path,
+    nvfp4_dequantize,
+    nvfp4_linear,
+    quantize,
     quantize_fp8_values,
     read_device_error,
     load,

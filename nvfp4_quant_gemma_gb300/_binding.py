@@ -48,6 +48,11 @@ def load() -> ctypes.CDLL:
             "gemma_add_rms_norm_quant": [P, P, P, F, P, I, I, P, P, P, i64, i64, I, P],
             "gemma_add_rms_norm_quant_parts": [P, I, i64, P, P, F, P, I, I, P, P, P, i64, i64, I, P],
             "add_rms_norm_quant": [P, I, i64, P, P, F, P, I, I, P, P, P, i64, i64, I, P],
+            "gemma_sandwich_norm_quant": [P, P, P, P, P, P, i64, F, F, P, I, I, P, P, P, i64, i64, I, P],
+            "gnq_quantize": [P, i64, P, I, P, P, i64, i64, I, P],
+            "gated_act_quant": [P, i64, I, P, I, I, P, P, P, i64, i64, I, P],
+            "gnq_nvfp4_dequantize": [P, P, P, P, i64, i64, I, P],
+            "nvfp4_linear": [P, P, P, P, P, P, P, i64, i64, i64, I, I, P],
             "gnq_set_launch_policy": [I, I, I, I],
             "gnq_query_launch": [i64, i64, I, I, I, I, I, F, P, P, P, P],
             "gnq_read_device_error": [P, I],
@@ -73,7 +78,8 @@ EXPORTS = ("gemma_add_rms_norm", "gemma_add_rms_norm_quant", "gemma_add_rms_norm
            "add_rms_norm_quant", "gnq_status_string", "gnq_set_launch_policy",
            "gnq_read_device_error", "gnq_set_pdl", "gnq_encode_e4m3_e2m1",
            "gnq_quantize_fp8_values", "gnq_query_launch", "gnq_set_constant_weights",
-           "gnq_inject_wait_timeout", "gnq_pdl_consumer")
+           "gnq_inject_wait_timeout", "gnq_pdl_consumer", "gemma_sandwich_norm_quant",
+           "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear")
 
 
 def status_string(status: int) -> str:
@@ -247,6 +253,215 @@ def add_rms_norm_quant(x_parts, residual, weight, eps, scale, mode, write_y=Fals
     """Plain RMSNorm variant (y = h * rsqrt(mean(h^2) + eps) * w)."""
     return _parts_call("add_rms_norm_quant", x_parts, residual, weight, eps, scale, mode,
                        write_y, out, stream)
+
+
+_OUT_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+_ACTS = {"silu": 1, "gelu_tanh": 2}
+
+
+def _need(t, name: str, nbytes: int, dtypes, contiguous: bool = True) -> None:
+    """A buffer of one of `dtypes`, at least `nbytes` long."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a tensor of {' / '.join(str(d) for d in dtypes)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes; the call needs {nbytes}")
+
+
+def _place(tensors, pinned: bool = True) -> int:
+    """The device of a call: every tensor on the current CUDA device (or, where
+    the operator takes it, in pinned host memory)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.is_cuda:
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
+                raise ValueError(f"a tensor is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+        elif not pinned or not t.is_pinned():
+            raise ValueError("tensors must be in CUDA" + (" or pinned host memory" if pinned else " memory"))
+    return torch.cuda.current_device() if dev is None else dev
+
+
+def _on(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _rows(x, name: str, width: int | None = None):
+    """(rows, columns, row stride) of a 2-D 16-bit matrix with dense rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be a 2-D bf16/fp16 tensor")
+    M, W = x.shape
+    sm, sn = x.stride()
+    if W > 1 and sn != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return M, W, (sm if M > 1 else W)
+
+
+def _need_outputs(M: int, H: int, m: int, dt, write_y: bool, out) -> None:
+    q, bs, y = out
+    if m in (0, 2):
+        _need(q, "q", M * H, (torch.float8_e4m3fn, torch.uint8))
+    elif m == 1:
+        _need(q, "q", M * H // 2, (torch.uint8,))
+        _need(bs, "block_scale", round_up(M, 128) * (H // 16), (torch.float8_e4m3fn, torch.uint8))
+    if m == 2:
+        _need(bs, "block_scale", M * (H // 32), (torch.uint8,))
+    if write_y:
+        _need(y, "y", M * H * 2, (dt,))
+
+
+def _need_scale(scale, name: str, required: bool) -> None:
+    if scale is None and not required:
+        return
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.numel() != 1:
+        raise ValueError(f"{name} must be a 1-element fp32 tensor")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None, mode="nvfp4", gate=None,
+                              residual_scale=1.0, residual_out=None, write_y=False, out=None, stream=None):
+    """The norm after a block, its gate and residual scale, the residual add,
+    and the norm before the next block quantized for its first linear:
+
+        u = x * rsqrt(mean(x^2) + eps) * (1 + post_weight)   (u = x without one)
+        h = residual + residual_scale * gate * u             (rounded once)
+        q = quant(y), y = h * rsqrt(mean(h^2) + eps) * (1 + weight)
+
+    ``gate`` is None, (H,) or (M, H) with dense rows.  h goes to
+    ``residual_out``, or in place to ``residual``.  ``mode`` is "none" (y
+    only), "fp8", "nvfp4" or "mxfp8"; ``out`` may supply (q, block_scale, y).
+    Returns (q, block_scale, y) as gemma_add_rms_norm_quant does."""
+    m = _mode(mode)
+    M, H, _ = _rows(x, "x")
+    dt = x.dtype
+    _need(x, "x", 0, (dt,))
+    write_y = bool(write_y) or m == -1
+    gate_stride = 0
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 2 and gate.shape == (M, H) and gate.dtype == dt:
+            gate_stride = _rows(gate, "gate")[2]
+        elif not isinstance(gate, torch.Tensor) or gate.shape != (H,) or gate.dtype != dt or not gate.is_contiguous():
+            raise ValueError(f"gate must be a ({H},) or ({M}, {H}) tensor of {dt}")
+    _need(residual, "residual", M * H * 2, (dt,))
+    if residual_out is not None:
+        _need(residual_out, "residual_out", M * H * 2, (dt,))
+    if post_weight is not None:
+        _need(post_weight, "post_weight", H * 2, (dt,))
+    _need(weight, "weight", H * 2, (dt,))
+    _need_scale(scale, "scale", m in (0, 1))
+    q, bs, y = out if out is not None else alloc_outputs(M, H, m, write_y, x)
+    _need_outputs(M, H, m, dt, write_y, (q, bs, y))
+    dev = _place((x, residual, residual_out, post_weight, weight, gate, scale, q if m >= 0 else None,
+                  bs if m > 0 else None, y if write_y else None))
+    st = load().gemma_sandwich_norm_quant(
+        x.data_ptr(), residual.data_ptr(), _at(residual_out), _at(post_weight), weight.data_ptr(),
+        _at(gate), gate_stride, float(residual_scale), float(eps), _at(scale), m, 1 if write_y else 0,
+        _at(q), _at(bs), _at(y), M, H, _DTYPE[dt], _on(stream, dev))
+    _check(st, "gemma_sandwich_norm_quant")
+    return q, (scale if m == 0 else bs), (y if write_y else None)
+
+
+def quantize(x, scale=None, mode="nvfp4", out=None, stream=None):
+    """Codes and scales of a 16-bit matrix (dense rows, any row stride that is
+    a multiple of 8): ``mode`` "fp8", "nvfp4" or "mxfp8".  ``out`` may supply
+    (q, block_scale).  Returns (q, block_scale); for FP8 block_scale is
+    ``scale`` itself."""
+    m = _mode(mode)
+    M, H, stride = _rows(x, "x")
+    _need_scale(scale, "scale", m in (0, 1))
+    q, bs = out if out is not None else alloc_outputs(M, H, m, False, x)[:2]
+    _need_outputs(M, H, m, x.dtype, False, (q, bs, None))
+    dev = _place((x, scale, q, bs if m > 0 else None))
+    st = load().gnq_quantize(x.data_ptr(), stride, _at(scale), m, _at(q), _at(bs) if m > 0 else None, M, H,
+                             _DTYPE[x.dtype], _on(stream, dev))
+    _check(st, "quantize")
+    return q, (scale if m == 0 else bs)
+
+
+def gated_act_quant(x, scale=None, mode="nvfp4", act="gelu_tanh", write_y=False, out=None, stream=None):
+    """y = act(gate) * up for x = [gate | up] (M, 2H), quantized: the step
+    between the two products of a gated MLP.  ``act`` is "silu" or
+    "gelu_tanh"; ``mode`` "none" (y only), "fp8", "nvfp4" or "mxfp8"; ``out``
+    may supply (q, block_scale, y).  Returns (q, block_scale, y)."""
+    m = _mode(mode)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    M, W, stride = _rows(x, "x")
+    if W % 2:
+        raise ValueError("x must hold gate and up side by side: an even number of columns")
+    H = W // 2
+    write_y = bool(write_y) or m == -1
+    _need_scale(scale, "scale", m in (0, 1))
+    q, bs, y = out if out is not None else alloc_outputs(M, H, m, write_y, x)
+    _need_outputs(M, H, m, x.dtype, write_y, (q, bs, y))
+    dev = _place((x, scale, q if m >= 0 else None, bs if m > 0 else None, y if write_y else None))
+    st = load().gated_act_quant(x.data_ptr(), stride, _ACTS[act], _at(scale), m, 1 if write_y else 0, _at(q),
+                                _at(bs), _at(y), M, H, _DTYPE[x.dtype], _on(stream, dev))
+    _check(st, "gated_act_quant")
+    return q, (scale if m == 0 else bs), (y if write_y else None)
+
+
+def _packed(q, block_scale, name: str):
+    """(rows, K) of packed NVFP4 codes with their swizzled block scales."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor of packed codes")
+    M, half = q.shape
+    _need(q, name, 0, (torch.uint8,))
+    _need(block_scale, name + "'s block scales", round_up(M, 128) * (half // 8), (torch.float8_e4m3fn, torch.uint8))
+    return M, 2 * half
+
+
+def nvfp4_dequantize(q, block_scale, scale=None, dtype=None, out=None, stream=None):
+    """NVFP4 codes (M, K/2) and swizzled block scales back to values,
+    code * (block scale / scale), as bf16 (default), fp16, fp32 or E4M3."""
+    M, K = _packed(q, block_scale, "q")
+    _need_scale(scale, "scale", False)
+    if out is None:
+        kw = {"device": q.device} if q.is_cuda else {"pin_memory": True}
+        out = torch.empty((M, K), dtype=dtype or torch.bfloat16, **kw)
+    if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
+        raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
+    _need(out, "out", M * K * out.element_size(), (out.dtype,))
+    dev = _place((q, block_scale, scale, out))
+    st = load().gnq_nvfp4_dequantize(q.data_ptr(), block_scale.data_ptr(), _at(scale), out.data_ptr(), M, K,
+                                     _OUT_TYPE[out.dtype], _on(stream, dev))
+    _check(st, "nvfp4_dequantize")
+    return out
+
+
+def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None, dtype=None, out=None,
+                 stream=None):
+    """alpha * (activation @ weight^T) + bias of NVFP4 operands: packed codes
+    (M, K/2) and (N, K/2) with their swizzled block scales, as ``quantize``
+    and the norm entry points return them.  ``alpha`` is a 1-element fp32
+    tensor, usually 1 / (scale of the activation * scale of the weight).
+    The output (M, N) is bf16 (default), fp16 or fp32."""
+    M, K = _packed(q, block_scale, "q")
+    N, Kw = _packed(weight_q, weight_block_scale, "weight_q")
+    if K != Kw:
+        raise ValueError(f"the activation has K = {K}, the weight {Kw}")
+    _need_scale(alpha, "alpha", True)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
+    ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
+    if ot == 3 or (dtype is not None and out.dtype != dtype):
+        raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
+    _need(out, "out", M * N * out.element_size(), (out.dtype,))
+    if bias is not None:
+        _need(bias, "bias", N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
+    dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, bias, out), pinned=False)
+    st = load().nvfp4_linear(q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(),
+                             weight_block_scale.data_ptr(), alpha.data_ptr(), _at(bias), out.data_ptr(), M, N, K,
+                             ot, 0 if bias is None else _DTYPE[bias.dtype], _on(stream, dev))
+    _check(st, "nvfp4_linear")
+    return out
 
 
 def set_launch_policy(kernel: int = 0, cluster: int = 0, vpt: int = 0, form: int = 0) -> None:

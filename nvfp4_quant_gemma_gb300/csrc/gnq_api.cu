@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "gemma_nq.h"
+#include "gnq_host.cuh"
 #include "gnq_launch.cuh"
 
 namespace gnq {
@@ -25,14 +26,7 @@ extern template int stream_blocks_per_sm<MODE_MXFP8>(int, bool, int, bool, bool,
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxH = 65536;
 constexpr int kMaxParts = 8;
-
-struct DevInfo {
-    int sms;
-    int smem_optin;     // largest dynamic shared memory a CTA may opt in to
-    unsigned int *err;  // device address of the error word
-};
 
 // Error word written by kernels whose bounded waits gave up (bit
 // DEVERR_WAIT_TIMEOUT); one per device, read and cleared by
@@ -51,6 +45,8 @@ std::atomic<int> g_inject_timeout{0};  // test hook: streaming waits give up (se
 
 constexpr long long kWaitLimit = 1LL << 31;      // cycles: about a second
 constexpr long long kTestWaitLimit = 1LL << 20;  // cycles: under a millisecond
+
+}  // namespace
 
 // Device properties and the error word's address, queried once per device
 // with that device current.
@@ -71,7 +67,22 @@ const DevInfo *dev_info() {
     return &g_info[dev];
 }
 
-}  // namespace
+bool pdl_on() { return g_pdl.load() != 0; }
+bool constant_weights_on() { return g_const_w.load() != 0; }
+bool inject_timeout_on() { return g_inject_timeout.load() != 0; }
+long long wait_limit_cycles() { return inject_timeout_on() ? kTestWaitLimit : kWaitLimit; }
+
+// True if `ptr` is plain device memory: the only memory the streaming
+// kernel's bulk copies are given.  Pinned host memory, managed memory and
+// anything the runtime does not know (or fails to classify) give false.
+bool in_device_memory(const void *ptr) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
+        cudaGetLastError();  // clear the error, so it is not reported by the launch
+        return false;
+    }
+    return a.type == cudaMemoryTypeDevice;
+}
 
 cudaError_t opt_in_dynamic_smem(const void *fn) {
     struct Done {
@@ -129,8 +140,6 @@ int one_wave_ctas(const void *fn, int threads) {
 }
 
 namespace {
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Elements per NVFP4 scale group (4 blocks), MXFP8 block, or vector chunk: a
 // cluster may only split a row at multiples of this.
@@ -193,18 +202,6 @@ int stream_occupancy(int mode, int dtype, bool parts, int vpt, bool lean, bool f
         cache[n_cached++] =
             Entry{dev, mode, dtype, (int)parts, vpt, (int)lean, (int)full, threads, smem, blocks};
     return blocks;
-}
-
-// True if `ptr` is plain device memory: the only memory the streaming
-// kernel's bulk copies are given.  Pinned host memory, managed memory and
-// anything the runtime does not know (or fails to classify) give false.
-bool in_device_memory(const void *ptr) {
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-        cudaGetLastError();  // clear the error, so it is not reported by the launch
-        return false;
-    }
-    return a.type == cudaMemoryTypeDevice;
 }
 
 // Streaming kernel shape.  For each ring depth S (rows in flight per CTA,
@@ -521,6 +518,7 @@ const char *gnq_status_string(int status) {
         case GNQ_ERR_ALIAS: return "x, residual and y must be distinct buffers";
         case GNQ_ERR_ALIGN: return "misaligned pointer or partial stride";
         case GNQ_ERR_CUDA: return "CUDA launch error";
+        case GNQ_ERR_MEMORY: return "a buffer must be in device memory";
         default: return "unknown status";
     }
 }
