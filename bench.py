@@ -47,7 +47,8 @@ FALLBACK_HBM_GBS = 6800.0
 KERNEL_SOURCES = ["nvfp4_quant_gemma_gb300/csrc/" + f for f in (
     "gnq_device.cuh", "gnq_kernels.cuh", "gnq_launch.cuh", "gnq_api.cu", "gnq_mode_none.cu",
     "gnq_mode_fp8.cu", "gnq_mode_nvfp4.cu", "gnq_mode_mxfp8.cu", "gnq_host.cuh", "gnq_tcgen05.cuh",
-    "gnq_sandwich.cu", "gnq_elementwise.cu", "gnq_linear.cu")]
+    "gnq_sandwich.cu", "gnq_elementwise.cu", "gnq_linear.cu",
+    "gnq_linear.cuh", "gnq_linear_pair.cu")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "dram_traffic.txt")
 
 

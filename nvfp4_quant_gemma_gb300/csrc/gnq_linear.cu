@@ -17,45 +17,10 @@
 #include <atomic>
 
 #include "gemma_nq.h"
-#include "gnq_host.cuh"
-#include "gnq_launch.cuh"
-#include "gnq_tcgen05.cuh"
+#include "gnq_linear.cuh"
 
 namespace gnq {
 namespace {
-
-constexpr int kTileN = 128;      // weight rows per CTA
-constexpr int kStageK = 256;     // elements of K per stage
-constexpr int kMaxStages = 8;
-constexpr uint32_t kBytesW = kTileN * kStageK / 2;
-constexpr uint32_t kBytesSf = 4 * 512;
-
-struct LinearParams {
-    const uint8_t *w_sf, *x_sf;
-    const float *alpha;
-    const uint16_t *bias;
-    void *y;
-    int64_t M;
-    int N, K64;       // K64: K / 64
-    int T;            // tokens per tile: the N of the tensor core's product
-    int n_tiles;      // weight tiles
-    int split;        // CTAs (a cluster) that share a tile's K
-    int stages;
-    uint32_t tmem_cols;
-    unsigned int *err;
-    long long wait_limit;
-    uint32_t tx_extra;  // test hook: bytes announced per stage beyond the copies
-};
-
-template <typename O> struct OutType;
-template <> struct OutType<__nv_bfloat16> {
-    static __device__ __forceinline__ float bias(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-    static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
-};
-template <> struct OutType<__half> {
-    static __device__ __forceinline__ float bias(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-    static __device__ __forceinline__ __half round(float v) { return __float2half_rn(v); }
-};
 
 // O: output type; B: type of the bias (bf16 or fp16).
 template <typename O, typename B>
@@ -80,10 +45,8 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const int64_t tt = tile / p.n_tiles, t0 = tt * p.T;
     const int KT = (p.K64 + 3) / 4;
     const int k_begin = KT * ks / S, n_k = KT * (ks + 1) / S - k_begin;
-    const int x_blocks = p.T > 128 && t0 + 128 < p.M ? 2 : 1;  // 128-token scale blocks of the tile
-    const int sf_blocks = p.T > 128 ? 2 : 1;
     const uint32_t bytes_x = (uint32_t)p.T * 128;
-    const uint32_t stage_bytes = kBytesW + bytes_x + kBytesSf * (1 + sf_blocks);
+    const uint32_t stage_bytes = kBytesW + bytes_x + 2 * kBytesSf;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -112,8 +75,9 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         *(volatile int *)&failed = 1;
     };
 
-    if (warp == 0 && lane == 0) {
-        // ---- producer ----
+    auto gave_up = [&] { return *(volatile int *)&failed != 0; };
+    if (warp == 0) {
+        // ---- copies ----
         int i = 0;
         for (; i < n_k; ++i) {
             const int s = i % p.stages;
@@ -122,50 +86,59 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
                 break;
             }
             const int kt = k_begin + i, nk = min(4, p.K64 - 4 * kt);
-            const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * nk;
-            mbar_expect_tx(full(s), kBytesW + bytes_x + sf_bytes * (1 + x_blocks) + p.tx_extra);
-            tma_load_2d(at, &map_w, kt * 128, n0, full(s));
-            tma_load_2d(at + kBytesW, &map_x, kt * 128, (int)t0, full(s));
-            const uint32_t sf = at + kBytesW + bytes_x;
-            bulk_g2s(sf, p.w_sf + ((int64_t)nt * p.K64 + 4 * kt) * 512, sf_bytes, full(s));
-            for (int b = 0; b < x_blocks; ++b)
-                bulk_g2s(sf + kBytesSf * (1 + b), p.x_sf + ((t0 / 128 + b) * p.K64 + 4 * kt) * 512,
-                         sf_bytes, full(s));
+            if (elect_one()) {
+                const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * nk;
+                mbar_expect_tx(full(s), kBytesW + bytes_x + 2 * sf_bytes + p.tx_extra);
+                tma_load_2d(at, &map_w, kt * 128, n0, full(s));
+                tma_load_2d(at + kBytesW, &map_x, kt * 128, (int)t0, full(s));
+                const uint32_t sf = at + kBytesW + bytes_x;
+                bulk_g2s(sf, p.w_sf + ((int64_t)nt * p.K64 + 4 * kt) * 512, sf_bytes, full(s));
+                bulk_g2s(sf + kBytesSf, p.x_sf + (t0 / 128 * p.K64 + 4 * kt) * 512, sf_bytes, full(s));
+            }
+            __syncwarp();
         }
         // Every copy has landed before the shared memory goes away or is
         // used again: the last use of each stage (test hook: with the bytes
         // that its announcement lacks).
-        for (int j = max(0, i - p.stages); j < i; ++j) {
-            const int s = j % p.stages;
-            if (mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit)) continue;
-            give_up();
-            if (p.tx_extra) bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, p.tx_extra, full(s));
-            mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit);
-        }
-    } else if (warp == 1 && lane == 0) {
-        // ---- tensor core ----
+        if (lane == 0)
+            for (int j = max(0, i - p.stages); j < i; ++j) {
+                const int s = j % p.stages;
+                if (mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit)) continue;
+                give_up();
+                if (p.tx_extra) bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, p.tx_extra, full(s));
+                mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit);
+            }
+    } else if (warp == 1) {
+        // ---- products ----
         const uint32_t idesc = idesc_nvfp4(kTileN, p.T);
         for (int i = 0; i < n_k; ++i) {
             const int s = i % p.stages;
-            if (!mbar_wait_bounded(full(s), (i / p.stages) & 1, p.wait_limit)) {
+            if (!mbar_wait_bounded(full(s), (i / p.stages) & 1, p.wait_limit) || gave_up()) {
                 give_up();
                 break;
             }
             tc_fence_after();
-            const int nk = min(4, p.K64 - 4 * (k_begin + i));
-            const uint32_t at = base + stage_bytes * s, sf = at + kBytesW + bytes_x;
-            for (int k = 0; k < nk; ++k) {
-                cp_scales<1>(sfw_col + 4 * k, desc_scales(sf + 512 * k));
-                for (int b = 0; b < sf_blocks; ++b)
-                    cp_scales<1>(sfx_col + 4 * (sf_blocks * k + b), desc_scales(sf + kBytesSf * (1 + b) + 512 * k));
+            const int nk = p.K64 - 4 * (k_begin + i);
+            if (elect_one()) {
+                const uint32_t at = base + stage_bytes * s, sf = at + kBytesW + bytes_x;
+                const uint64_t a = desc_sw128(at), b = desc_sw128(at + kBytesW);
+                const uint64_t sw = desc_scales(sf), sx = desc_scales(sf + kBytesSf);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < nk) {
+                        cp_scales<1>(sfw_col + 4 * k, sw + 32 * k);
+                        cp_scales<1>(sfx_col + 4 * k, sx + 32 * k);
+                    }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < nk)
+                        mma_nvfp4<1>(tmem, a + 2 * k, b + 2 * k, idesc, sfw_col + 4 * k, sfx_col + 4 * k,
+                                     i > 0 || k > 0);
+                tc_commit(empty(s));
             }
-            const uint64_t a = desc_sw128(at), b = desc_sw128(at + kBytesW);
-            for (int k = 0; k < nk; ++k)
-                mma_nvfp4<1>(tmem, a + 2 * k, b + 2 * k, idesc, sfw_col + 4 * k, sfx_col + 4 * sf_blocks * k,
-                             i > 0 || k > 0);
-            tc_commit(empty(s));
+            __syncwarp();
         }
-        tc_commit(acc_bar);
+        if (elect_one()) tc_commit(acc_bar);
     }
     __syncwarp();
 
@@ -188,12 +161,14 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     if (S == 1) {
         if (good)
             for (int c = 0; c < rows; c += 16) {
-                float v[16];
+                uint32_t v[16];
+                __syncwarp();
                 tmem_ld16(tmem + lane_base + c, v);
+                tmem_wait(v);
                 if (n < p.N)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (c + j < rows) store(t0 + c + j, v[j]);
+                        if (c + j < rows) store(t0 + c + j, __uint_as_float(v[j]));
             }
     } else {
         // The cluster's partial sums meet in shared memory, [token][weight row]
@@ -201,18 +176,24 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         float *part = reinterpret_cast<float *>(dyn + (base - (uint32_t)__cvta_generic_to_shared(dyn)));
         if (good)
             for (int c = 0; c < rows; c += 16) {
-                float v[16];
+                uint32_t v[16];
                 tmem_ld16(tmem + lane_base + c, v);
+                tmem_wait(v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + row] = v[j];
+                for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + row] = __uint_as_float(v[j]);
             }
         cluster_arrive_release();
         cluster_wait();
         if (good && n < p.N)
-            for (int c = ks; c < rows; c += S) {
-                float v = 0.f;
-                for (int r = 0; r < S; ++r) v += ld_peer_f32(part + c * kTileN + row, r);
-                store(t0 + c, v);
+            for (int c0 = ks; c0 < rows; c0 += 8 * S) {  // 8 tokens at a time: their reads overlap
+                float v[8] = {};
+                for (int r = 0; r < S; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] += ld_peer_f32(part + min(c0 + j * S, rows - 1) * kTileN + row, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c0 + j * S < rows) store(t0 + c0 + j * S, v[j]);
             }
         cluster_arrive_release();
         cluster_wait();  // peers may still be reading this CTA's sums
@@ -242,35 +223,44 @@ EncodeFn encode_fn() {
     return f;
 }
 
-// Map of a row-major (rows, K) matrix of packed codes, loaded in tiles of
-// `box` rows x 128 bytes; what lies outside reads as 0.
-bool encode(CUtensorMap *map, const void *codes, int64_t rows, int64_t K, int box) {
+bool encode_tiles(CUtensorMap *map, CUtensorMapDataType type, const void *base, const cuuint64_t (&dims)[2],
+                  cuuint64_t stride, const cuuint32_t (&box)[2], CUtensorMapSwizzle swizzle) {
     const EncodeFn f = encode_fn();
-    if (!f) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t tile[2] = {128, (cuuint32_t)box}, step[2] = {1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, tile, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t step[2] = {1, 1};
+    return f && f(map, type, 2, const_cast<void *>(base), dims, &stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+bool encode_codes(CUtensorMap *map, const void *codes, int64_t rows, int64_t K, int box) {
+    return encode_tiles(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, {(cuuint64_t)(K / 2), (cuuint64_t)rows},
+                        (cuuint64_t)(K / 2), {128, (cuuint32_t)box}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool encode_scales(CUtensorMap *map, const void *scales, int64_t rows) {
+    return encode_tiles(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, {128, (cuuint64_t)rows}, 512, {128, 4},
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+namespace {
 
 // Tile and split of a call.  The smallest tile that holds the tokens (above
 // 128, tiles of 256); K is split over a cluster while the grid is smaller
 // than the SMs and every CTA keeps a stage of it.
 bool shape_of(const DevInfo &d, int64_t M, int64_t N, int64_t K, LinearParams &p, int64_t &grid, size_t &smem) {
-    p.T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    p.T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
     const int KT = (p.K64 + 3) / 4;
     const int64_t tiles = p.n_tiles * ((M + p.T - 1) / p.T);
-    p.split = 1;
-    while (p.split < 8 && tiles * p.split < d.sms && 2 * p.split <= KT) p.split *= 2;
+    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, d.sms / tiles, KT}));
     grid = tiles * p.split;
     if (grid > 0x7FFFFFFF) return false;
-    const int64_t stage = kBytesW + p.T * 128 + kBytesSf * (p.T > 128 ? 3 : 2);
-    p.tmem_cols = p.T <= 32 ? 64 : p.T == 64 ? 128 : p.T == 128 ? 256 : 512;
+    const int64_t stage = kBytesW + p.T * 128 + 2 * kBytesSf;
+    p.tmem_cols = p.T <= 32 ? 64 : p.T == 64 ? 128 : 256;
     // two CTAs per SM where the grid has them and half of each memory does
     const int64_t limit = d.smem_optin - 1024 - 512;
-    const int64_t room = grid > d.sms && p.tmem_cols <= 256 ? limit / 2 - 1024 : limit;
+    const int64_t room = grid > d.sms ? limit / 2 - 1024 : limit;
     p.stages = (int)std::min<int64_t>({kMaxStages, room / stage, (KT + p.split - 1) / p.split});
     p.stages = std::max(p.stages, 1);
     smem = (size_t)(1024 + std::max<int64_t>(p.stages * stage, p.split > 1 ? p.T * kTileN * 4 : 0));
@@ -320,13 +310,19 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     p.err = d->err;
     p.wait_limit = wait_limit_cycles();
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (M > 128) {
+        e = launch_linear_pair(p, q, w_q, out_type, bias_type, d->sms, s);
+        if (e == cudaSuccess) return GNQ_OK;
+        cudaGetLastError();
+        return GNQ_ERR_CUDA;
+    }
     int64_t grid = 0;
     size_t smem = 0;
     if (!shape_of(*d, M, N, K, p, grid, smem)) return GNQ_ERR_SHAPE;
     CUtensorMap mw, mx;
-    if (!encode(&mw, w_q, N, K, kTileN) || !encode(&mx, q, M, K, p.T)) return GNQ_ERR_CUDA;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
+    if (!encode_codes(&mw, w_q, N, K, kTileN) || !encode_codes(&mx, q, M, K, p.T)) return GNQ_ERR_CUDA;
     if (out_type == GNQ_BF16) e = launch_linear<__nv_bfloat16, __nv_bfloat16>(mw, mx, p, grid, smem, s);
     else if (out_type == GNQ_FP16) e = launch_linear<__half, __half>(mw, mx, p, grid, smem, s);
     else if (bias_type == GNQ_FP16) e = launch_linear<float, __half>(mw, mx, p, grid, smem, s);
