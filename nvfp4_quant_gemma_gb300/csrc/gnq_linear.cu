@@ -243,6 +243,12 @@ bool encode_scales(CUtensorMap *map, const void *scales, int64_t rows) {
                         CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size) {
+    return encode_tiles(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, y,
+                        {(cuuint64_t)N, (cuuint64_t)M}, (cuuint64_t)N * size, {(cuuint32_t)(128 / size), 32},
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 namespace {
 
 // Tile and split of a call.  The smallest tile that holds the tokens (above

@@ -48,6 +48,10 @@ bool encode_codes(CUtensorMap *map, const void *codes, int64_t rows, int64_t K, 
 // of K), `rows` of them, loaded four at a time.
 bool encode_scales(CUtensorMap *map, const void *scales, int64_t rows);
 
+// Map of a row-major (M, N) output of 2- or 4-byte values, stored in tiles of
+// 32 rows x 128 bytes.
+bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size);
+
 // The kernel of large batches (gnq_linear_pair.cu): out_type as in the ABI.
 cudaError_t launch_linear_pair(const LinearParams &p, const void *q, const void *w_q, int out_type,
                                int bias_type, int sms, cudaStream_t s);

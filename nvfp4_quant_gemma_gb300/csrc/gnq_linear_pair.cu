@@ -12,6 +12,12 @@
 // not fit, so neighbours share 64 columns: the epilogue takes those first and
 // the next tile starts as soon as they are out, long before the rest is.
 //
+// A row of the output tile is 128 bytes at a time: each of the four epilogue
+// warps packs 32 rows of a chunk into shared memory and a tile store writes
+// it as whole lines (stores straight from the registers touch 32 rows per
+// instruction: 4864 x 8192 x 512 took 58 us with them).  An output whose rows
+// are not 16-byte aligned is stored value by value.
+//
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA),
 // 2-5 take sums out (32 rows each).
 #include <algorithm>
@@ -26,12 +32,15 @@ constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
 constexpr uint32_t kHalf = 128 * kStageK / 2;                       // 128 rows of codes of one stage
 constexpr uint32_t kPairStage = 2 * kHalf + 3 * kBytesSf;           // per CTA
+constexpr uint32_t kChunk = 32 * 128;                               // 32 rows x 128 bytes of output
+constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + 4 * 2 * kChunk;
 constexpr uint32_t kAccCols = 192, kSfxCol = 448, kSfwCol = 464;    // second tile, scales
 
 struct PairParams {
     LinearParams p;
     int m_tiles, n_tiles;
-    int vec;  // bytes of an output row's widest aligned store: 32, 16 or 0 (single values)
+    bool tiled;     // rows of y are 16-byte aligned: tile stores
+    bool bias16;    // the bias is 16-byte aligned
 };
 
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
@@ -58,53 +67,84 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// 32 sums of one row to y[n .. n + 32): alpha, bias, one rounding.
-template <typename O, typename B>
-__device__ __forceinline__ void store_row32(const PairParams &pp, int64_t m, int n, const uint32_t (&acc)[32],
-                                            float alpha) {
+// Tile store of this warp's chunk; clipped at the edges of y.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most the last `N` of this thread's committed groups still read shared memory.
+template <int N> __device__ __forceinline__ void tma_store_wait() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// Result of 32 sums of one row at columns n .. n + 31: alpha and bias.
+template <typename B>
+__device__ __forceinline__ void scale_bias32(const PairParams &pp, int n, const uint32_t (&acc)[32], float alpha,
+                                             float *v) {
     const LinearParams &p = pp.p;
-    if (m >= p.M || n >= p.N) return;
-    float v[32];
+    if (!p.bias) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float b = p.bias && n + i < p.N ? OutType<B>::bias(__ldg(p.bias + n + i)) : 0.f;
-        v[i] = fmaf(__uint_as_float(acc[i]), alpha, b);
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * alpha;
+        return;
     }
-    constexpr int PER = 4 / sizeof(O);  // values per 32-bit word
-    uint32_t w[32 / PER];
+    float b[32];
+    if (pp.bias16 && n + 32 <= p.N) {
 #pragma unroll
-    for (int i = 0; i < 32 / PER; ++i) {
-        if constexpr (PER == 1) w[i] = __float_as_uint(v[i]);
-        else w[i] = Act<O>::pack2(v[2 * i], v[2 * i + 1]);
-    }
-    O *o = static_cast<O *>(p.y) + m * p.N + n;
-    if (pp.vec && n + 32 <= p.N) {
-#pragma unroll
-        for (int i = 0; i < 32 / PER; i += 8) {
-            const uint4 a = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-            const uint4 b = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
-            if (pp.vec == 32) {
-                st_v8(reinterpret_cast<uint32_t *>(o) + i, a, b);
-            } else {
-                st_v4(reinterpret_cast<uint32_t *>(o) + i, a);
-                st_v4(reinterpret_cast<uint32_t *>(o) + i + 4, b);
-            }
-        }
+        for (int i = 0; i < 32; i += 8) Act<B>::unpack(ld_weight(p.bias + n + i), &b[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 32; ++i) b[i] = n + i < p.N ? OutType<B>::bias(__ldg(p.bias + n + i)) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(acc[i]), alpha, b[i]);
+}
+
+// One chunk: 32 rows (one per lane) x 128 bytes of y from column n, of the
+// sums in `acc` (32 or 64 columns).  buf: this warp's shared memory chunk.
+template <typename O, typename B, int COLS>
+__device__ __forceinline__ void store_chunk(const PairParams &pp, const CUtensorMap *map_y, uint32_t buf, int64_t m0,
+                                            int n, const uint32_t (*acc)[32], float alpha, int lane) {
+    const LinearParams &p = pp.p;
+    float v[COLS];
+#pragma unroll
+    for (int h = 0; h < COLS / 32; ++h) scale_bias32<B>(pp, n + 32 * h, acc[h], alpha, v + 32 * h);
+    if (pp.tiled) {
+        constexpr int PER = COLS / 8;  // values per 16 bytes
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint4 w;
+            if constexpr (PER == 8) w = pack8<O>(&v[8 * i]);
+            else w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + 128u * lane + 16u * (i ^ (lane & 7))),
+                         "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                         : "memory");
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (m0 < p.M && n < p.N) tma_store_2d(map_y, n, (int)m0, buf);
+            tma_store_commit();  // a group per chunk, empty or not: the buffers take turns by count
+        }
+    } else if (m0 + lane < p.M) {
+        O *o = static_cast<O *>(p.y) + (m0 + lane) * p.N + n;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i)
             if (n + i < p.N) {
-                if constexpr (PER == 1) o[i] = v[i];
+                if constexpr (sizeof(O) == 4) o[i] = v[i];
                 else o[i] = OutType<O>::round(v[i]);
             }
     }
+    __syncwarp();
 }
 
 template <typename O, typename B>
 __global__ void __launch_bounds__(192) linear_pair_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
     const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ CUtensorMap map_ws,
-    const __grid_constant__ PairParams pp) {
+    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ PairParams pp) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kPairStages + 3];
     __shared__ __align__(16) uint4 topup[kPairStages];
@@ -229,13 +269,10 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
                             cp_scales<2>(tmem + kSfxCol + 4 * k, sx + 32 * k);
                             cp_scales<2>(tmem + kSfwCol + 8 * k, sw0 + 32 * k);
                             cp_scales<2>(tmem + kSfwCol + 8 * k + 4, sw1 + 32 * k);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nk)
                             mma_nvfp4<2>(acc, a + 2 * k, b + 2 * k, idesc, tmem + kSfxCol + 4 * k,
                                          tmem + kSfwCol + 8 * k, kt > 0 || k > 0);
+                        }
+                    }
                     tc_commit_pair(empty(s));
                     if (kt == KT - 1) tc_commit_pair(acc_full);
                 }
@@ -254,6 +291,15 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
         const int quad = warp & 3;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
         const uint32_t free_bar = map_to_cta(shared_free, 0);
+        // two chunks of shared memory in turn: one is filled while the other is stored
+        const uint32_t bufs = base + kPairStages * kPairStage + 2 * kChunk * quad;
+        int turn = 0;
+        auto out_chunk = [&](int64_t m0, int n, const uint32_t (*acc)[32], auto cols) {
+            if (lane == 0) tma_store_wait<1>();
+            __syncwarp();
+            store_chunk<O, B, decltype(cols)::value>(pp, &map_y, bufs + kChunk * turn, m0, n, acc, alpha, lane);
+            turn ^= 1;
+        };
         int j = 0;
         for (int i = blockIdx.x / 2; i < tiles; i += G, ++j) {
             int mt, nt;
@@ -264,28 +310,36 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
                 break;
             }
             tc_fence_after();
-            const int64_t m = (int64_t)mt * kPairTile + 128 * rank + 32 * quad + lane;
+            const int64_t m0 = (int64_t)mt * kPairTile + 128 * rank + 32 * quad;
             const int n0 = nt * kPairTile;
             const uint32_t acc = tmem + kAccCols * (j & 1) + lanes;
-            const int first = j & 1 ? 0 : 192;  // the tile's columns that it shares
-            uint32_t v[32], u[32];
-            tmem_ld32(acc + first, v);
-            tmem_ld32(acc + first + 32, u);
-            tmem_wait(v);
-            tmem_wait(u);
+            // the 64 columns that the next tile shares, then the other 192
+            const int first = j & 1 ? 0 : 192, rest = j & 1 ? 64 : 0;
+            uint32_t v[2][32];
+            tmem_ld32(acc + first, v[0]);
+            tmem_ld32(acc + first + 32, v[1]);
+            tmem_wait(v[0]);
+            tmem_wait(v[1]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(free_bar);
-            store_row32<O, B>(pp, m, n0 + first, v, alpha);
-            store_row32<O, B>(pp, m, n0 + first + 32, u, alpha);
-            const int rest = j & 1 ? 64 : 0;
-            for (int c = rest; c < rest + 192; c += 32) {
-                __syncwarp();
-                tmem_ld32(acc + c, v);
-                tmem_wait(v);
-                store_row32<O, B>(pp, m, n0 + c, v, alpha);
+            for (int c = first;; c = c == first ? rest : c + 64) {
+                if (c != first) {
+                    tmem_ld32(acc + c, v[0]);
+                    tmem_ld32(acc + c + 32, v[1]);
+                    tmem_wait(v[0]);
+                    tmem_wait(v[1]);
+                }
+                if constexpr (sizeof(O) == 2) {
+                    out_chunk(m0, n0 + c, v, std::integral_constant<int, 64>{});
+                } else {
+                    out_chunk(m0, n0 + c, v, std::integral_constant<int, 32>{});
+                    out_chunk(m0, n0 + c + 32, v + 1, std::integral_constant<int, 32>{});
+                }
+                if (c == rest + 128) break;
             }
         }
+        tma_store_wait<0>();  // shared memory is read before it goes away
     }
     __syncwarp();
     tc_fence_before();
@@ -296,29 +350,31 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
 }
 
 template <typename O, typename B>
-cudaError_t launch_pair(const CUtensorMap (&m)[4], const PairParams &pp, int64_t grid, cudaStream_t s) {
+cudaError_t launch_pair(const CUtensorMap (&m)[5], const PairParams &pp, int64_t grid, cudaStream_t s) {
     auto fn = linear_pair_kernel<O, B>;
     const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
-    return launch(fn, grid, 192, 1024 + kPairStages * kPairStage, 2, s, m[0], m[1], m[2], m[3], pp);
+    return launch(fn, grid, 192, kPairSmem, 2, s, m[0], m[1], m[2], m[3], m[4], pp);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_pair(const LinearParams &p, const void *q, const void *w_q, int out_type, int bias_type,
                                int sms, cudaStream_t s) {
-    PairParams pp = {p, 0, 0, 0};
+    PairParams pp = {p, 0, 0, false, false};
     const int64_t K = (int64_t)p.K64 * 64;
     const int64_t mt = (p.M + kPairTile - 1) / kPairTile, nt = (p.N + kPairTile - 1) / kPairTile;
     const int64_t x_rows = (p.M + 127) / 128 * p.K64, w_rows = (p.N + 127) / 128 * (int64_t)p.K64;
     if (mt * nt > 0x3FFFFFFF || x_rows > 0x7FFFFFFF || w_rows > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     pp.m_tiles = (int)mt;
     pp.n_tiles = (int)nt;
-    const int64_t row_bytes = (int64_t)p.N * (out_type == GNQ_FP32 ? 4 : 2);
-    pp.vec = row_bytes % 32 == 0 && aligned(p.y, 32) ? 32 : row_bytes % 16 == 0 ? 16 : 0;
-    CUtensorMap m[4];
+    const int size = out_type == GNQ_FP32 ? 4 : 2;
+    pp.tiled = (int64_t)p.N * size % 16 == 0;
+    pp.bias16 = p.bias && aligned(p.bias, 16);
+    CUtensorMap m[5] = {};
     if (!encode_codes(&m[0], q, p.M, K, 128) || !encode_codes(&m[1], w_q, p.N, K, 128) ||
-        !encode_scales(&m[2], p.x_sf, x_rows) || !encode_scales(&m[3], p.w_sf, w_rows))
+        !encode_scales(&m[2], p.x_sf, x_rows) || !encode_scales(&m[3], p.w_sf, w_rows) ||
+        (pp.tiled && !encode_output(&m[4], p.y, p.M, p.N, size)))
         return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(mt * nt, sms / 2);
     if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, pp, grid, s);
