@@ -113,27 +113,26 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         const uint32_t idesc = idesc_nvfp4(kTileN, p.T);
         for (int i = 0; i < n_k; ++i) {
             const int s = i % p.stages;
-            if (!mbar_wait_bounded(full(s), (i / p.stages) & 1, p.wait_limit) || gave_up()) {
+            if (!mbar_wait_bounded(full(s), (i / p.stages) & 1, p.wait_limit) || (p.tx_extra && gave_up())) {
                 give_up();
                 break;
             }
             tc_fence_after();
             const int nk = p.K64 - 4 * (k_begin + i);
             if (elect_one()) {
-                const uint32_t at = base + stage_bytes * s, sf = at + kBytesW + bytes_x;
-                const uint64_t a = desc_sw128(at), b = desc_sw128(at + kBytesW);
-                const uint64_t sw = desc_scales(sf), sx = desc_scales(sf + kBytesSf);
+                const uint32_t at = (base + stage_bytes * s) >> 4, sf = at + ((kBytesW + bytes_x) >> 4);
+                auto step = [&](int k) {
+                    cp_scales<1>(sfw_col + 4 * k, desc_scales(sf + 32 * k));
+                    cp_scales<1>(sfx_col + 4 * k, desc_scales(sf + kBytesSf / 16 + 32 * k));
+                    mma_nvfp4<1>(tmem, desc_sw128(at + 2 * k), desc_sw128(at + kBytesW / 16 + 2 * k), idesc,
+                                 sfw_col + 4 * k, sfx_col + 4 * k, i > 0 || k > 0);
+                };
+                if (nk >= 4) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < nk) {
-                        cp_scales<1>(sfw_col + 4 * k, sw + 32 * k);
-                        cp_scales<1>(sfx_col + 4 * k, sx + 32 * k);
-                    }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < nk)
-                        mma_nvfp4<1>(tmem, a + 2 * k, b + 2 * k, idesc, sfw_col + 4 * k, sfx_col + 4 * k,
-                                     i > 0 || k > 0);
+                    for (int k = 0; k < 4; ++k) step(k);
+                } else {
+                    for (int k = 0; k < nk; ++k) step(k);
+                }
                 tc_commit(empty(s));
             }
             __syncwarp();

@@ -205,26 +205,30 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
 
     if (warp == 0) {
         // ---- copies ----
-        int it = 0;
+        int it = 0, s = 0;
+        uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
+        const uint32_t x_row = 128 * rank;
         for (int i = blockIdx.x / 2; i < tiles && !gave_up(); i += G) {
             int mt, nt;
             tile_at(i, mt, nt);
+            const int x0 = mt * kPairTile + x_row, w0 = nt * kPairTile + x_row;
+            const int xs = (2 * mt + rank) * p.K64, ws = 2 * nt * p.K64;
             for (int kt = 0; kt < KT; ++kt, ++it) {
-                const int s = it % kPairStages;
-                if (it >= kPairStages && !mbar_wait_bounded(empty(s), (it / kPairStages - 1) & 1, p.wait_limit)) {
+                if (!mbar_wait_bounded(empty(s), parity, p.wait_limit)) {
                     give_up();
                     break;
                 }
                 if (elect_one()) {
                     const uint32_t at = base + kPairStage * s, bar = map_to_cta(full(s), 0);
                     if (rank == 0) mbar_expect_tx(full(s), 2 * kPairStage + p.tx_extra);
-                    tma_load_pair(at, &map_x, kt * 128, mt * kPairTile + 128 * rank, bar);
-                    tma_load_pair(at + kHalf, &map_w, kt * 128, nt * kPairTile + 128 * rank, bar);
-                    tma_load_pair(at + 2 * kHalf, &map_xs, 0, (2 * mt + rank) * p.K64 + 4 * kt, bar);
-                    tma_load_pair(at + 2 * kHalf + kBytesSf, &map_ws, 0, 2 * nt * p.K64 + 4 * kt, bar);
-                    tma_load_pair(at + 2 * kHalf + 2 * kBytesSf, &map_ws, 0, (2 * nt + 1) * p.K64 + 4 * kt, bar);
+                    tma_load_pair(at, &map_x, kt * 128, x0, bar);
+                    tma_load_pair(at + kHalf, &map_w, kt * 128, w0, bar);
+                    tma_load_pair(at + 2 * kHalf, &map_xs, 0, xs + 4 * kt, bar);
+                    tma_load_pair(at + 2 * kHalf + kBytesSf, &map_ws, 0, ws + 4 * kt, bar);
+                    tma_load_pair(at + 2 * kHalf + 2 * kBytesSf, &map_ws, 0, ws + p.K64 + 4 * kt, bar);
                 }
                 __syncwarp();
+                if (++s == kPairStages) s = 0, parity ^= 1;
             }
         }
         // Every copy has landed before the shared memory goes away (test
@@ -240,7 +244,8 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
     } else if (warp == 1 && rank == 0) {
         // ---- products ----
         constexpr uint32_t idesc = idesc_nvfp4(256, 256);
-        int it = 0, j = 0;
+        int j = 0, s = 0;
+        uint32_t parity = 0;
         bool good = true;
         for (int i = blockIdx.x / 2; good && i < tiles; i += G, ++j) {
             if (j > 0 && !mbar_wait_bounded(shared_free, (j - 1) & 1, p.wait_limit)) {
@@ -249,9 +254,10 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
             }
             tc_fence_after();
             const uint32_t acc = tmem + kAccCols * (j & 1);
-            for (int kt = 0; kt < KT; ++kt, ++it) {
-                const int s = it % kPairStages;
-                if (!mbar_wait_bounded(full(s), (it / kPairStages) & 1, p.wait_limit) || gave_up()) {
+            for (int kt = 0; kt < KT; ++kt) {
+                // (under the test hook a stage may complete late, by the copy
+                // that makes up for the announcement)
+                if (!mbar_wait_bounded(full(s), parity, p.wait_limit) || (p.tx_extra && gave_up())) {
                     give_up();
                     good = false;
                     break;
@@ -259,24 +265,26 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
                 tc_fence_after();
                 const int nk = p.K64 - 4 * kt;
                 if (elect_one()) {
-                    const uint32_t at = base + kPairStage * s, sf = at + 2 * kHalf;
-                    const uint64_t a = desc_sw128(at), b = desc_sw128(at + kHalf);
-                    const uint64_t sx = desc_scales(sf), sw0 = desc_scales(sf + kBytesSf),
-                                   sw1 = desc_scales(sf + 2 * kBytesSf);
+                    const uint32_t at = (base >> 4) + (kPairStage >> 4) * s;
+                    auto step = [&](int k) {
+                        cp_scales<2>(tmem + kSfxCol + 4 * k, desc_scales(at + (2 * kHalf + 512 * k) / 16));
+                        cp_scales<2>(tmem + kSfwCol + 8 * k, desc_scales(at + (2 * kHalf + kBytesSf + 512 * k) / 16));
+                        cp_scales<2>(tmem + kSfwCol + 8 * k + 4,
+                                     desc_scales(at + (2 * kHalf + 2 * kBytesSf + 512 * k) / 16));
+                        mma_nvfp4<2>(acc, desc_sw128(at + 2 * k), desc_sw128(at + kHalf / 16 + 2 * k), idesc,
+                                     tmem + kSfxCol + 4 * k, tmem + kSfwCol + 8 * k, kt > 0 || k > 0);
+                    };
+                    if (nk >= 4) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < nk) {
-                            cp_scales<2>(tmem + kSfxCol + 4 * k, sx + 32 * k);
-                            cp_scales<2>(tmem + kSfwCol + 8 * k, sw0 + 32 * k);
-                            cp_scales<2>(tmem + kSfwCol + 8 * k + 4, sw1 + 32 * k);
-                            mma_nvfp4<2>(acc, a + 2 * k, b + 2 * k, idesc, tmem + kSfxCol + 4 * k,
-                                         tmem + kSfwCol + 8 * k, kt > 0 || k > 0);
-                        }
+                        for (int k = 0; k < 4; ++k) step(k);
+                    } else {
+                        for (int k = 0; k < nk; ++k) step(k);
                     }
                     tc_commit_pair(empty(s));
                     if (kt == KT - 1) tc_commit_pair(acc_full);
                 }
                 __syncwarp();
+                if (++s == kPairStages) s = 0, parity ^= 1;
             }
         }
         // every product is done before tensor memory goes away

@@ -80,16 +80,22 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
 }
 
 // ---- descriptors ----
-// Shared-memory matrix descriptor of a K-major tile whose rows are 128 bytes
-// in the 128-byte swizzle (8-row groups 1024 bytes apart).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// A shared-memory descriptor is (address / 16) in the low bits of its low
+// word plus constants, so the descriptors of one stage are one value plus
+// compile-time offsets, which is what keeps the issue loops short.
+// desc_sw128: a K-major tile whose rows are 128 bytes in the 128-byte swizzle
+// (8-row groups 1024 bytes apart).  desc_scales: a 512-byte scale tile (32
+// rows of 16 bytes, no swizzle).  `a16`: address / 16.
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
 }
-// Of a 512-byte scale tile (32 rows of 16 bytes, no swizzle).
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 |
-           (uint64_t)1 << 46;
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t a16) {
+    return desc64(a16 + (1u << 16), 1024 >> 4 | 1u << 14 | 2u << 29);
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t a16) {
+    return desc64(a16 + (8u << 16), 128 >> 4 | 1u << 14);
 }
 // Instruction descriptor of a block-scaled product: E2M1 x E2M1 with one
 // E4M3 scale per 16 elements of K, both operands K-major, M x N tile.
