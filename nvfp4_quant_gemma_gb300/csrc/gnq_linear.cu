@@ -22,6 +22,9 @@
 namespace gnq {
 namespace {
 
+// Tokens of a tile that one CTA of a split adds: whole groups of four.
+__host__ __device__ constexpr int join_block(int T, int split) { return ((T + split - 1) / split + 3) / 4 * 4; }
+
 // O: output type; B: type of the bias (bf16 or fp16).
 template <typename O, typename B>
 __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUtensorMap map_w,
@@ -67,6 +70,33 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const uint32_t tmem = tmem_slot;
     const uint32_t sfw_col = tmem + p.T, sfx_col = sfw_col + 16;
 
+    if (S > 1) cluster_arrive_relaxed();  // the join's stores may go to CTAs that have started
+
+    // Copies of the k-th 256 elements into stage s: the weight's tile and
+    // scales, then the tokens'.  (The stage and its phase are counted, not
+    // divided out: one warp issues every copy, and its loop is what limits a
+    // CTA at these sizes.)
+    const uint8_t *const w_sf = p.w_sf + ((int64_t)nt * p.K64 + 4 * k_begin) * 512;
+    const uint8_t *const x_sf = p.x_sf + (t0 / 128 * p.K64 + 4 * k_begin) * 512;
+    const int k64 = p.K64 - 4 * k_begin;  // 64-element steps from this CTA's first
+    auto copy_w = [&](int k, int s) {
+        const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * min(4, k64 - 4 * k);
+        mbar_expect_tx(full(s), kBytesW + bytes_x + 2 * sf_bytes + p.tx_extra);
+        tma_load_2d(at, &map_w, (k_begin + k) * 128, n0, full(s));
+        bulk_g2s(at + kBytesW + bytes_x, w_sf + k * 2048, sf_bytes, full(s));
+    };
+    auto copy_x = [&](int k, int s) {
+        const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * min(4, k64 - 4 * k);
+        tma_load_2d(at + kBytesW, &map_x, (k_begin + k) * 128, (int)t0, full(s));
+        bulk_g2s(at + kBytesW + bytes_x + kBytesSf, x_sf + k * 2048, sf_bytes, full(s));
+    };
+    // Constant weights (gnq_set_constant_weights): the first stages' come in
+    // while the preceding grid drains.
+    const int early = p.early_w ? min(n_k, p.stages) : 0;
+    if (warp == 0 && elect_one())
+        for (int i = 0; i < early; ++i) copy_w(i, i);
+    __syncwarp();
+
     pdl_wait();  // inputs may come from the preceding grid, outputs may still be read by it
     pdl_trigger();
 
@@ -78,30 +108,25 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     auto gave_up = [&] { return *(volatile int *)&failed != 0; };
     if (warp == 0) {
         // ---- copies ----
-        int i = 0;
+        int i = 0, s = 0;
+        uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         for (; i < n_k; ++i) {
-            const int s = i % p.stages;
-            if (i >= p.stages && !mbar_wait_bounded(empty(s), (i / p.stages - 1) & 1, p.wait_limit)) {
+            if (!mbar_wait_bounded(empty(s), parity, p.wait_limit)) {
                 give_up();
                 break;
             }
-            const int kt = k_begin + i, nk = min(4, p.K64 - 4 * kt);
             if (elect_one()) {
-                const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * nk;
-                mbar_expect_tx(full(s), kBytesW + bytes_x + 2 * sf_bytes + p.tx_extra);
-                tma_load_2d(at, &map_w, kt * 128, n0, full(s));
-                tma_load_2d(at + kBytesW, &map_x, kt * 128, (int)t0, full(s));
-                const uint32_t sf = at + kBytesW + bytes_x;
-                bulk_g2s(sf, p.w_sf + ((int64_t)nt * p.K64 + 4 * kt) * 512, sf_bytes, full(s));
-                bulk_g2s(sf + kBytesSf, p.x_sf + (t0 / 128 * p.K64 + 4 * kt) * 512, sf_bytes, full(s));
+                if (i >= early) copy_w(i, s);
+                copy_x(i, s);
             }
             __syncwarp();
+            if (++s == p.stages) s = 0, parity ^= 1;
         }
-        // Every copy has landed before the shared memory goes away or is
-        // used again: the last use of each stage (test hook: with the bytes
-        // that its announcement lacks).
+        // Every copy has landed before the shared memory goes away: the last
+        // use of each stage (test hook: with the bytes that its announcement
+        // lacks).
         if (lane == 0)
-            for (int j = max(0, i - p.stages); j < i; ++j) {
+            for (int j = max(0, i - p.stages); j < max(i, early); ++j) {
                 const int s = j % p.stages;
                 if (mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit)) continue;
                 give_up();
@@ -111,31 +136,38 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     } else if (warp == 1) {
         // ---- products ----
         const uint32_t idesc = idesc_nvfp4(kTileN, p.T);
+        int s = 0;
+        uint32_t parity = 0;
         for (int i = 0; i < n_k; ++i) {
-            const int s = i % p.stages;
-            if (!mbar_wait_bounded(full(s), (i / p.stages) & 1, p.wait_limit) || (p.tx_extra && gave_up())) {
+            if (!mbar_wait_bounded(full(s), parity, p.wait_limit) || (p.tx_extra && gave_up())) {
                 give_up();
                 break;
             }
             tc_fence_after();
-            const int nk = p.K64 - 4 * (k_begin + i);
+            const int nk = k64 - 4 * i;
             if (elect_one()) {
                 const uint32_t at = (base + stage_bytes * s) >> 4, sf = at + ((kBytesW + bytes_x) >> 4);
-                auto step = [&](int k) {
+                auto scales = [&](int k) {
                     cp_scales<1>(sfw_col + 4 * k, desc_scales(sf + 32 * k));
                     cp_scales<1>(sfx_col + 4 * k, desc_scales(sf + kBytesSf / 16 + 32 * k));
+                };
+                auto product = [&](int k) {
                     mma_nvfp4<1>(tmem, desc_sw128(at + 2 * k), desc_sw128(at + kBytesW / 16 + 2 * k), idesc,
                                  sfw_col + 4 * k, sfx_col + 4 * k, i > 0 || k > 0);
                 };
                 if (nk >= 4) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) step(k);
+                    for (int k = 0; k < 4; ++k) scales(k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) product(k);
                 } else {
-                    for (int k = 0; k < nk; ++k) step(k);
+                    for (int k = 0; k < nk; ++k) scales(k);
+                    for (int k = 0; k < nk; ++k) product(k);
                 }
                 tc_commit(empty(s));
             }
             __syncwarp();
+            if (++s == p.stages) s = 0, parity ^= 1;
         }
         if (elect_one()) tc_commit(acc_bar);
     }
@@ -150,52 +182,93 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const int row = warp * 32 + lane, n = n0 + row;
     const int rows = (int)min((int64_t)p.T, p.M - t0);  // tokens in the tile
     const float bias = p.bias && n < p.N ? OutType<B>::bias(__ldg(p.bias + n)) : 0.f;
+    auto result = [&](float v) { return fmaf(v, alpha, bias); };
     auto store = [&](int64_t m, float v) {
-        const float r = fmaf(v, alpha, bias);
-        const int64_t at = m * p.N + n;
-        if constexpr (std::is_same<O, float>::value) static_cast<float *>(p.y)[at] = r;
-        else static_cast<O *>(p.y)[at] = OutType<O>::round(r);
+        O *const o = static_cast<O *>(p.y) + m * p.N + n;
+        if constexpr (std::is_same<O, float>::value) *o = result(v);
+        else *o = OutType<O>::round(result(v));
     };
     const uint32_t lane_base = (uint32_t)warp << 21;  // 32 lanes per warp, lane number in bits 16-31
     if (S == 1) {
+        // Two 16-bit columns per lane: neighbouring lanes exchange, the even
+        // one stores token c + j, the odd one c + j + 1.
+        const bool pairs = sizeof(O) == 2 && p.N % 2 == 0;
         if (good)
             for (int c = 0; c < rows; c += 16) {
                 uint32_t v[16];
                 __syncwarp();
                 tmem_ld16(tmem + lane_base + c, v);
                 tmem_wait(v);
+                if constexpr (sizeof(O) == 2) {
+                    if (pairs && c + 16 <= rows) {
+                        const int odd = lane & 1;
+                        O *o = static_cast<O *>(p.y) + (t0 + c + odd) * p.N + (n - odd);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const uint32_t own = Act<O>::pack2(result(__uint_as_float(v[j])), result(__uint_as_float(v[j + 1])));
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                            if (n < p.N)
+                                *reinterpret_cast<uint32_t *>(o) =
+                                    odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                            o += 2 * (int64_t)p.N;
+                        }
+                        continue;
+                    }
+                }
                 if (n < p.N)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         if (c + j < rows) store(t0 + c + j, __uint_as_float(v[j]));
             }
     } else {
-        // The cluster's partial sums meet in shared memory, [token][weight row]
-        // in fp32, and each CTA adds every S-th token's in rank order.
-        float *part = reinterpret_cast<float *>(dyn + (base - (uint32_t)__cvta_generic_to_shared(dyn)));
-        if (good)
+        // Join: CTA r adds the r-th block of tokens.  Every CTA stores its
+        // partial sums of a block into the shared memory of the CTA that adds
+        // it, [source][token / 4][weight row][token % 4], then each adds in
+        // source order: one way across the cluster and one barrier, and the
+        // order of the sum is fixed.
+        const int blk = join_block(p.T, S);
+        const uint32_t part = base + stage_bytes * p.stages + 16u * row;
+        const uint32_t src = 16u * kTileN * (blk / 4);  // bytes of one source
+        cluster_wait();
+        if (good) {
+            int dst = -1, left = 0;
+            uint32_t to = 0;
             for (int c = 0; c < rows; c += 16) {
                 uint32_t v[16];
+                __syncwarp();
                 tmem_ld16(tmem + lane_base + c, v);
                 tmem_wait(v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + row] = __uint_as_float(v[j]);
+                for (int j = 0; j < 16; j += 4) {
+                    if (left == 0) {
+                        left = blk;
+                        to = map_to_cta(part + src * ks, ++dst);
+                    }
+                    if (c + j < rows) st_cluster_v4(to, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    to += 16u * kTileN;
+                    left -= 4;
+                }
             }
+        }
         cluster_arrive_release();
         cluster_wait();
         if (good && n < p.N)
-            for (int c0 = ks; c0 < rows; c0 += 8 * S) {  // 8 tokens at a time: their reads overlap
-                float v[8] = {};
-                for (int r = 0; r < S; ++r)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] += ld_peer_f32(part + min(c0 + j * S, rows - 1) * kTileN + row, r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j * S < rows) store(t0 + c0 + j * S, v[j]);
+            for (int i = 0; i < blk; i += 4) {
+                const int c = ks * blk + i;
+                if (c >= rows) break;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int r = 0; r < S; ++r) {
+                    const uint4 u = lds_v4(part + src * r + 16u * kTileN * (i / 4));
+                    v.x += __uint_as_float(u.x);
+                    v.y += __uint_as_float(u.y);
+                    v.z += __uint_as_float(u.z);
+                    v.w += __uint_as_float(u.w);
+                }
+                store(t0 + c, v.x);
+                if (c + 1 < rows) store(t0 + c + 1, v.y);
+                if (c + 2 < rows) store(t0 + c + 2, v.z);
+                if (c + 3 < rows) store(t0 + c + 3, v.w);
             }
-        cluster_arrive_release();
-        cluster_wait();  // peers may still be reading this CTA's sums
     }
     tc_fence_before();
     __syncthreads();
@@ -250,26 +323,88 @@ bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size) {
 
 namespace {
 
-// Tile and split of a call.  The smallest tile that holds the tokens (above
-// 128, tiles of 256); K is split over a cluster while the grid is smaller
-// than the SMs and every CTA keeps a stage of it.
-bool shape_of(const DevInfo &d, int64_t M, int64_t N, int64_t K, LinearParams &p, int64_t &grid, size_t &smem) {
+// Shared memory of a split: half of an SM's where two stages fit it (two CTAs
+// of one grid run there, or the next grid's start up beside the last ones of
+// this one), else all.
+struct SplitShape {
+    int stages;
+    size_t smem;
+};
+SplitShape split_shape(const DevInfo &d, int T, int split, int KT) {
+    const int64_t stage = kBytesW + T * 128 + 2 * kBytesSf;
+    const int64_t join = split > 1 ? (int64_t)join_block(T, split) * split * kTileN * 4 : 0;
+    const int64_t whole = d.smem_optin - 1024 - 512 - join, half = (d.smem_optin - 1024 - 512) / 2 - 1024 - join;
+    const int64_t room = half >= 2 * stage ? half : whole;
+    const int stages =
+        std::max(1, (int)std::min<int64_t>({kMaxStages, room / stage, (KT + split - 1) / split}));
+    return {stages, (size_t)(1024 + stages * stage + join)};
+}
+
+// Clusters of `split` CTAs with tiles of T tokens that the device runs at a
+// time (0 on error), asked once per device, T and split.
+int resident_clusters(const DevInfo &d, int T, int split) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> cached[kDevices][4][9];  // clusters + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+    std::atomic<int> &c = cached[dev][T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3][split];
+    int n = c.load() - 1;
+    if (n < 0) {
+        auto fn = linear_kernel<__nv_bfloat16, __nv_bfloat16>;
+        if (opt_in_dynamic_smem(reinterpret_cast<const void *>(fn)) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)split, 1, 1);
+        cfg.blockDim = dim3(128, 1, 1);
+        cfg.dynamicSmemBytes = split_shape(d, T, split, 1 << 20).smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)split;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+        cfg.attrs = &attr;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        c.store(n + 1);
+    }
+    return n;
+}
+
+// Tile and split of a call: the smallest tile that holds the tokens (128 at
+// most), and K split over the largest cluster of which the device runs all at
+// a time, each CTA keeping two stages or more.  One round of CTAs is what
+// counts: with one stage of K more per round a split pays until its clusters
+// no longer fit (M = 16, N = 8192, K = 5120: 8.4, 6.4, 6.1, 5.6 us for 1 to
+// 4, then 9.6 us for 6, in two rounds).
+void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &grid, size_t &smem) {
     p.T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
     const int KT = (p.K64 + 3) / 4;
     const int64_t tiles = p.n_tiles * ((M + p.T - 1) / p.T);
-    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, d.sms / tiles, KT}));
+    p.split = 1;
+    for (int c = std::min(8, KT / 2); c > 1 && p.split == 1; --c)
+        if (tiles <= d.sms && resident_clusters(d, p.T, c) >= tiles) p.split = c;
     grid = tiles * p.split;
-    if (grid > 0x7FFFFFFF) return false;
-    const int64_t stage = kBytesW + p.T * 128 + 2 * kBytesSf;
+    const SplitShape ss = split_shape(d, p.T, p.split, KT);
+    p.stages = ss.stages;
+    smem = ss.smem;
     p.tmem_cols = p.T <= 32 ? 64 : p.T == 64 ? 128 : 256;
-    // two CTAs per SM where the grid has them and half of each memory does
-    const int64_t limit = d.smem_optin - 1024 - 512;
-    const int64_t room = grid > d.sms ? limit / 2 - 1024 : limit;
-    p.stages = (int)std::min<int64_t>({kMaxStages, room / stage, (KT + p.split - 1) / p.split});
-    p.stages = std::max(p.stages, 1);
-    smem = (size_t)(1024 + std::max<int64_t>(p.stages * stage, p.split > 1 ? p.T * kTileN * 4 : 0));
-    return true;
+}
+
+// Whether CTA pairs on 256 x 256 tiles take the call (more than 64 tokens).
+// Both times follow the rounds of CTAs and the depth of K; the constants, in
+// microseconds, are fits to calls of 128 to 512 tokens (M = 128, N = 2048,
+// K = 5120: 7.8 against 10.4 us for pairs; 300 x 5000 x 4096: 11.4 against
+// 10.2; 512 x 4096 x 4096: 13 against 9.6).
+bool pairs_take(const DevInfo &d, int64_t M, int64_t N, const LinearParams &p, int64_t grid) {
+    if (M <= 64) return false;
+    const int KT = (p.K64 + 3) / 4;
+    const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), pairs = d.sms / 2;
+    const double pair = 4.2 + (double)((tiles + pairs - 1) / pairs) * (0.31 * KT + 0.4);
+    const double single = 3.0 + (double)((grid + d.sms - 1) / d.sms) * 0.47 * ((KT + p.split - 1) / p.split) +
+                          (p.split > 1 ? 2.5 : 0.0);
+    return pair < single;
 }
 
 template <typename O, typename B>
@@ -315,17 +450,18 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     p.err = d->err;
     p.wait_limit = wait_limit_cycles();
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
+    p.early_w = constant_weights_on();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (M > 128) {
+    int64_t grid = 0;
+    size_t smem = 0;
+    shape_of(*d, M, N, p, grid, smem);
+    if (grid > 0x7FFFFFFF || pairs_take(*d, M, N, p, grid)) {
         e = launch_linear_pair(p, q, w_q, out_type, bias_type, d->sms, s);
         if (e == cudaSuccess) return GNQ_OK;
         cudaGetLastError();
         return GNQ_ERR_CUDA;
     }
-    int64_t grid = 0;
-    size_t smem = 0;
-    if (!shape_of(*d, M, N, K, p, grid, smem)) return GNQ_ERR_SHAPE;
     CUtensorMap mw, mx;
     if (!encode_codes(&mw, w_q, N, K, kTileN) || !encode_codes(&mx, q, M, K, p.T)) return GNQ_ERR_CUDA;
     if (out_type == GNQ_BF16) e = launch_linear<__nv_bfloat16, __nv_bfloat16>(mw, mx, p, grid, smem, s);

@@ -28,6 +28,7 @@ struct LinearParams {
     uint32_t tmem_cols;
     unsigned int *err;
     long long wait_limit;
+    bool early_w;       // the weight's first stages are read before the wait on the preceding grid
     uint32_t tx_extra;  // test hook: bytes announced per stage beyond the copies
 };
 

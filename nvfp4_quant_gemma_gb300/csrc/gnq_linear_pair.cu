@@ -12,14 +12,14 @@
 // not fit, so neighbours share 64 columns: the epilogue takes those first and
 // the next tile starts as soon as they are out, long before the rest is.
 //
-// A row of the output tile is 128 bytes at a time: each of the four epilogue
+// A row of the output tile is 128 bytes at a time: each of the eight epilogue
 // warps packs 32 rows of a chunk into shared memory and a tile store writes
 // it as whole lines (stores straight from the registers touch 32 rows per
 // instruction: 4864 x 8192 x 512 took 58 us with them).  An output whose rows
 // are not 16-byte aligned is stored value by value.
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA),
-// 2-5 take sums out (32 rows each).
+// 2-9 take sums out: two warps for each 32 rows, chunks in turn.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -33,7 +33,7 @@ constexpr int kPairStages = 5;
 constexpr uint32_t kHalf = 128 * kStageK / 2;                       // 128 rows of codes of one stage
 constexpr uint32_t kPairStage = 2 * kHalf + 3 * kBytesSf;           // per CTA
 constexpr uint32_t kChunk = 32 * 128;                               // 32 rows x 128 bytes of output
-constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + 4 * 2 * kChunk;
+constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + 8 * kChunk;
 constexpr uint32_t kAccCols = 192, kSfxCol = 448, kSfwCol = 464;    // second tile, scales
 
 struct PairParams {
@@ -43,11 +43,6 @@ struct PairParams {
     bool bias16;    // the bias is 16-byte aligned
 };
 
-__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 // Tile load into this CTA, completing on a barrier of the pair's first CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -141,7 +136,7 @@ __device__ __forceinline__ void store_chunk(const PairParams &pp, const CUtensor
 }
 
 template <typename O, typename B>
-__global__ void __launch_bounds__(192) linear_pair_kernel(
+__global__ void __launch_bounds__(320) linear_pair_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
     const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ CUtensorMap map_ws,
     const __grid_constant__ CUtensorMap map_y, const __grid_constant__ PairParams pp) {
@@ -168,7 +163,7 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
             mbar_init(empty(s), 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(shared_free, 8);
+        mbar_init(shared_free, 16);
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         failed = 0;
@@ -295,24 +290,23 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
         if (!mbar_wait_bounded(done, 0, 4 * p.wait_limit)) give_up();  // the first CTA's last arrival here
     } else if (warp >= 2) {
         // ---- sums out ----
+        // Warps 2-5 take the shared columns of a tile first and then the
+        // third chunk of 64, warps 6-9 the second and the fourth.
         const float alpha = __ldg(p.alpha);
-        const int quad = warp & 3;
+        const int quad = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
         const uint32_t free_bar = map_to_cta(shared_free, 0);
-        // two chunks of shared memory in turn: one is filled while the other is stored
-        const uint32_t bufs = base + kPairStages * kPairStage + 2 * kChunk * quad;
-        int turn = 0;
+        const uint32_t buf = base + kPairStages * kPairStage + kChunk * (warp - 2);
         auto out_chunk = [&](int64_t m0, int n, const uint32_t (*acc)[32], auto cols) {
-            if (lane == 0) tma_store_wait<1>();
+            if (lane == 0) tma_store_wait<0>();
             __syncwarp();
-            store_chunk<O, B, decltype(cols)::value>(pp, &map_y, bufs + kChunk * turn, m0, n, acc, alpha, lane);
-            turn ^= 1;
+            store_chunk<O, B, decltype(cols)::value>(pp, &map_y, buf, m0, n, acc, alpha, lane);
         };
         int j = 0;
         for (int i = blockIdx.x / 2; i < tiles; i += G, ++j) {
             int mt, nt;
             tile_at(i, mt, nt);
-            const bool ok = mbar_wait_bounded(acc_full, j & 1, 2 * p.wait_limit) && !gave_up();
+            const bool ok = mbar_wait_bounded(acc_full, j & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
             if (!__all_sync(0xffffffffu, ok)) {
                 give_up();
                 break;
@@ -321,22 +315,23 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
             const int64_t m0 = (int64_t)mt * kPairTile + 128 * rank + 32 * quad;
             const int n0 = nt * kPairTile;
             const uint32_t acc = tmem + kAccCols * (j & 1) + lanes;
-            // the 64 columns that the next tile shares, then the other 192
-            const int first = j & 1 ? 0 : 192, rest = j & 1 ? 64 : 0;
-            uint32_t v[2][32];
-            tmem_ld32(acc + first, v[0]);
-            tmem_ld32(acc + first + 32, v[1]);
-            tmem_wait(v[0]);
-            tmem_wait(v[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_remote(free_bar);
-            for (int c = first;; c = c == first ? rest : c + 64) {
-                if (c != first) {
-                    tmem_ld32(acc + c, v[0]);
-                    tmem_ld32(acc + c + 32, v[1]);
-                    tmem_wait(v[0]);
-                    tmem_wait(v[1]);
+            // the next tile may start once the shared columns of this one are
+            // out (first set) and all of the one before, whose place it takes
+            // (second set: it has come here)
+            if (set == 1 && lane == 0) arrive_remote(free_bar);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int turn = 2 * h + set;  // chunk in the order of taking: the shared one is the first
+                const int c = j & 1 ? 64 * turn : 64 * ((turn + 3) & 3);
+                uint32_t v[2][32];
+                tmem_ld32(acc + c, v[0]);
+                tmem_ld32(acc + c + 32, v[1]);
+                tmem_wait(v[0]);
+                tmem_wait(v[1]);
+                if (turn == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(free_bar);
                 }
                 if constexpr (sizeof(O) == 2) {
                     out_chunk(m0, n0 + c, v, std::integral_constant<int, 64>{});
@@ -344,8 +339,9 @@ __global__ void __launch_bounds__(192) linear_pair_kernel(
                     out_chunk(m0, n0 + c, v, std::integral_constant<int, 32>{});
                     out_chunk(m0, n0 + c + 32, v + 1, std::integral_constant<int, 32>{});
                 }
-                if (c == rest + 128) break;
             }
+            tc_fence_before();  // this tile's reads are done before the arrival at the next
+            __syncwarp();
         }
         tma_store_wait<0>();  // shared memory is read before it goes away
     }
@@ -362,7 +358,7 @@ cudaError_t launch_pair(const CUtensorMap (&m)[5], const PairParams &pp, int64_t
     auto fn = linear_pair_kernel<O, B>;
     const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
-    return launch(fn, grid, 192, kPairSmem, 2, s, m[0], m[1], m[2], m[3], m[4], pp);
+    return launch(fn, grid, 320, kPairSmem, 2, s, m[0], m[1], m[2], m[3], m[4], pp);
 }
 
 }  // namespace

@@ -18,6 +18,16 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Address of the same shared memory in another CTA of the cluster.
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // ---- tensor memory ----
 template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
     if constexpr (CG == 1)
