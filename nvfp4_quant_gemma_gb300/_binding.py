@@ -290,7 +290,7 @@ def _on(stream, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _rows(x, name: str, width: int | None = None):
+def _rows(x, name: str):
     """(rows, columns, row stride) of a 2-D 16-bit matrix with dense rows."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
         raise ValueError(f"{name} must be a 2-D bf16/fp16 tensor")
@@ -325,6 +325,46 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+# Each call below first tries its whole argument check as one expression (all
+# tensors on the current CUDA device, the common case: a call of a decode step
+# takes microseconds, most of them here); what that does not pass goes through
+# the step-by-step check, which names the fault or admits pinned host memory.
+_U8, _F32, _E4M3 = torch.uint8, torch.float32, torch.float8_e4m3fn
+
+
+def _here(dev: int) -> bool:
+    return dev >= 0 and dev == torch._C._cuda_getDevice()
+
+
+def _outputs_ok(dev: int, M: int, H: int, m: int, dt, write_y: bool, q, bs, y) -> bool:
+    if write_y and not (y.dtype is dt and y.is_contiguous() and y.nbytes >= 2 * M * H and y.get_device() == dev):
+        return False
+    if m == 1:
+        return (q.dtype is _U8 and q.is_contiguous() and q.nbytes >= M * H // 2 and q.get_device() == dev
+                and bs.dtype in (_E4M3, _U8) and bs.is_contiguous()
+                and bs.nbytes >= (M + 127) // 128 * 8 * H and bs.get_device() == dev)
+    if m == -1:
+        return True
+    return (q.dtype in (_E4M3, _U8) and q.is_contiguous() and q.nbytes >= M * H and q.get_device() == dev
+            and (m == 0 or (bs.dtype is _U8 and bs.is_contiguous() and bs.nbytes >= M * (H // 32)
+                            and bs.get_device() == dev)))
+
+
+def _scale_ok(dev: int, m: int, scale) -> bool:
+    if scale is None:
+        return m in (-1, 2)
+    return scale.dtype is _F32 and scale.numel() == 1 and scale.get_device() == dev
+
+
+def _gate_stride(gate, M: int, H: int, dt) -> int:
+    if isinstance(gate, torch.Tensor) and gate.dtype == dt:
+        if gate.dim() == 2 and gate.shape == (M, H):
+            return _rows(gate, "gate")[2]
+        if gate.shape == (H,) and gate.is_contiguous():
+            return 0
+    raise ValueError(f"gate must be a ({H},) or ({M}, {H}) tensor of {dt}")
+
+
 def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None, mode="nvfp4", gate=None,
                               residual_scale=1.0, residual_out=None, write_y=False, out=None, stream=None):
     """The norm after a block, its gate and residual scale, the residual add,
@@ -341,30 +381,43 @@ def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None,
     m = _mode(mode)
     M, H, _ = _rows(x, "x")
     dt = x.dtype
-    _need(x, "x", 0, (dt,))
     write_y = bool(write_y) or m == -1
-    gate_stride = 0
-    if gate is not None:
-        if isinstance(gate, torch.Tensor) and gate.dim() == 2 and gate.shape == (M, H) and gate.dtype == dt:
-            gate_stride = _rows(gate, "gate")[2]
-        elif not isinstance(gate, torch.Tensor) or gate.shape != (H,) or gate.dtype != dt or not gate.is_contiguous():
-            raise ValueError(f"gate must be a ({H},) or ({M}, {H}) tensor of {dt}")
-    _need(residual, "residual", M * H * 2, (dt,))
-    if residual_out is not None:
-        _need(residual_out, "residual_out", M * H * 2, (dt,))
-    if post_weight is not None:
-        _need(post_weight, "post_weight", H * 2, (dt,))
-    _need(weight, "weight", H * 2, (dt,))
-    _need_scale(scale, "scale", m in (0, 1))
+    gate_stride = 0 if gate is None else _gate_stride(gate, M, H, dt)
     q, bs, y = out if out is not None else alloc_outputs(M, H, m, write_y, x)
-    _need_outputs(M, H, m, dt, write_y, (q, bs, y))
-    dev = _place((x, residual, residual_out, post_weight, weight, gate, scale, q if m >= 0 else None,
-                  bs if m > 0 else None, y if write_y else None))
-    st = load().gemma_sandwich_norm_quant(
-        x.data_ptr(), residual.data_ptr(), _at(residual_out), _at(post_weight), weight.data_ptr(),
-        _at(gate), gate_stride, float(residual_scale), float(eps), _at(scale), m, 1 if write_y else 0,
-        _at(q), _at(bs), _at(y), M, H, _DTYPE[dt], _on(stream, dev))
-    _check(st, "gemma_sandwich_norm_quant")
+    dev = x.get_device()
+    n, w = 2 * M * H, 2 * H
+    try:
+        ok = (_here(dev) and x.is_contiguous()
+              and residual.dtype is dt and residual.is_contiguous() and residual.nbytes >= n
+              and residual.get_device() == dev
+              and weight.dtype is dt and weight.is_contiguous() and weight.nbytes >= w and weight.get_device() == dev
+              and (post_weight is None or (post_weight.dtype is dt and post_weight.is_contiguous()
+                                           and post_weight.nbytes >= w and post_weight.get_device() == dev))
+              and (residual_out is None or (residual_out.dtype is dt and residual_out.is_contiguous()
+                                            and residual_out.nbytes >= n and residual_out.get_device() == dev))
+              and (gate is None or gate.get_device() == dev)
+              and _scale_ok(dev, m, scale) and _outputs_ok(dev, M, H, m, dt, write_y, q, bs, y))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need(x, "x", 0, (dt,))
+        _need(residual, "residual", n, (dt,))
+        if residual_out is not None:
+            _need(residual_out, "residual_out", n, (dt,))
+        if post_weight is not None:
+            _need(post_weight, "post_weight", w, (dt,))
+        _need(weight, "weight", w, (dt,))
+        _need_scale(scale, "scale", m in (0, 1))
+        _need_outputs(M, H, m, dt, write_y, (q, bs, y))
+        dev = _place((x, residual, residual_out, post_weight, weight, gate, scale, q if m >= 0 else None,
+                      bs if m > 0 else None, y if write_y else None))
+    st = (_lib or load()).gemma_sandwich_norm_quant(
+        x.data_ptr(), residual.data_ptr(), None if residual_out is None else residual_out.data_ptr(),
+        None if post_weight is None else post_weight.data_ptr(), weight.data_ptr(),
+        None if gate is None else gate.data_ptr(), gate_stride, residual_scale, eps, _at(scale), m,
+        1 if write_y else 0, _at(q), _at(bs), _at(y), M, H, _DTYPE[dt], _on(stream, dev))
+    if st:
+        _check(st, "gemma_sandwich_norm_quant")
     return q, (scale if m == 0 else bs), (y if write_y else None)
 
 
@@ -375,13 +428,20 @@ def quantize(x, scale=None, mode="nvfp4", out=None, stream=None):
     ``scale`` itself."""
     m = _mode(mode)
     M, H, stride = _rows(x, "x")
-    _need_scale(scale, "scale", m in (0, 1))
     q, bs = out if out is not None else alloc_outputs(M, H, m, False, x)[:2]
-    _need_outputs(M, H, m, x.dtype, False, (q, bs, None))
-    dev = _place((x, scale, q, bs if m > 0 else None))
-    st = load().gnq_quantize(x.data_ptr(), stride, _at(scale), m, _at(q), _at(bs) if m > 0 else None, M, H,
-                             _DTYPE[x.dtype], _on(stream, dev))
-    _check(st, "quantize")
+    dev = x.get_device()
+    try:
+        ok = _here(dev) and _scale_ok(dev, m, scale) and _outputs_ok(dev, M, H, m, None, False, q, bs, None)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_scale(scale, "scale", m in (0, 1))
+        _need_outputs(M, H, m, x.dtype, False, (q, bs, None))
+        dev = _place((x, scale, q, bs if m > 0 else None))
+    st = (_lib or load()).gnq_quantize(x.data_ptr(), stride, _at(scale), m, _at(q), _at(bs) if m > 0 else None, M,
+                                       H, _DTYPE[x.dtype], _on(stream, dev))
+    if st:
+        _check(st, "quantize")
     return q, (scale if m == 0 else bs)
 
 
@@ -398,13 +458,20 @@ def gated_act_quant(x, scale=None, mode="nvfp4", act="gelu_tanh", write_y=False,
         raise ValueError("x must hold gate and up side by side: an even number of columns")
     H = W // 2
     write_y = bool(write_y) or m == -1
-    _need_scale(scale, "scale", m in (0, 1))
     q, bs, y = out if out is not None else alloc_outputs(M, H, m, write_y, x)
-    _need_outputs(M, H, m, x.dtype, write_y, (q, bs, y))
-    dev = _place((x, scale, q if m >= 0 else None, bs if m > 0 else None, y if write_y else None))
-    st = load().gated_act_quant(x.data_ptr(), stride, _ACTS[act], _at(scale), m, 1 if write_y else 0, _at(q),
-                                _at(bs), _at(y), M, H, _DTYPE[x.dtype], _on(stream, dev))
-    _check(st, "gated_act_quant")
+    dev = x.get_device()
+    try:
+        ok = _here(dev) and _scale_ok(dev, m, scale) and _outputs_ok(dev, M, H, m, x.dtype, write_y, q, bs, y)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_scale(scale, "scale", m in (0, 1))
+        _need_outputs(M, H, m, x.dtype, write_y, (q, bs, y))
+        dev = _place((x, scale, q if m >= 0 else None, bs if m > 0 else None, y if write_y else None))
+    st = (_lib or load()).gated_act_quant(x.data_ptr(), stride, _ACTS[act], _at(scale), m, 1 if write_y else 0,
+                                          _at(q), _at(bs), _at(y), M, H, _DTYPE[x.dtype], _on(stream, dev))
+    if st:
+        _check(st, "gated_act_quant")
     return q, (scale if m == 0 else bs), (y if write_y else None)
 
 
@@ -413,26 +480,45 @@ def _packed(q, block_scale, name: str):
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor of packed codes")
     M, half = q.shape
-    _need(q, name, 0, (torch.uint8,))
-    _need(block_scale, name + "'s block scales", round_up(M, 128) * (half // 8), (torch.float8_e4m3fn, torch.uint8))
+    _need(q, name, 0, (_U8,))
+    _need(block_scale, name + "'s block scales", round_up(M, 128) * (half // 8), (_E4M3, _U8))
     return M, 2 * half
+
+
+def _packed_ok(dev: int, q, sf) -> bool:
+    M, half = q.shape
+    return (q.dtype is _U8 and q.is_contiguous() and q.get_device() == dev and sf.dtype in (_E4M3, _U8)
+            and sf.is_contiguous() and sf.nbytes >= (M + 127) // 128 * 16 * half and sf.get_device() == dev)
 
 
 def nvfp4_dequantize(q, block_scale, scale=None, dtype=None, out=None, stream=None):
     """NVFP4 codes (M, K/2) and swizzled block scales back to values,
     code * (block scale / scale), as bf16 (default), fp16, fp32 or E4M3."""
-    M, K = _packed(q, block_scale, "q")
-    _need_scale(scale, "scale", False)
-    if out is None:
-        kw = {"device": q.device} if q.is_cuda else {"pin_memory": True}
-        out = torch.empty((M, K), dtype=dtype or torch.bfloat16, **kw)
-    if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
-        raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
-    _need(out, "out", M * K * out.element_size(), (out.dtype,))
-    dev = _place((q, block_scale, scale, out))
-    st = load().gnq_nvfp4_dequantize(q.data_ptr(), block_scale.data_ptr(), _at(scale), out.data_ptr(), M, K,
-                                     _OUT_TYPE[out.dtype], _on(stream, dev))
-    _check(st, "nvfp4_dequantize")
+    try:
+        dev = q.get_device()
+        M, half = q.shape
+        K = 2 * half
+        if out is None and dev >= 0:
+            out = torch.empty((M, K), dtype=dtype or torch.bfloat16, device=q.device)
+        ok = (_here(dev) and _packed_ok(dev, q, block_scale)
+              and (scale is None or (scale.dtype is _F32 and scale.numel() == 1 and scale.get_device() == dev))
+              and out.dtype in _OUT_TYPE and (dtype is None or out.dtype is dtype) and out.is_contiguous()
+              and out.numel() >= M * K and out.get_device() == dev)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        M, K = _packed(q, block_scale, "q")
+        _need_scale(scale, "scale", False)
+        if out is None:
+            out = torch.empty((M, K), dtype=dtype or torch.bfloat16, pin_memory=True)
+        if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
+            raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
+        _need(out, "out", M * K * out.element_size(), (out.dtype,))
+        dev = _place((q, block_scale, scale, out))
+    st = (_lib or load()).gnq_nvfp4_dequantize(q.data_ptr(), block_scale.data_ptr(), _at(scale), out.data_ptr(), M,
+                                               K, _OUT_TYPE[out.dtype], _on(stream, dev))
+    if st:
+        _check(st, "nvfp4_dequantize")
     return out
 
 
@@ -443,24 +529,41 @@ def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None,
     and the norm entry points return them.  ``alpha`` is a 1-element fp32
     tensor, usually 1 / (scale of the activation * scale of the weight).
     The output (M, N) is bf16 (default), fp16 or fp32."""
-    M, K = _packed(q, block_scale, "q")
-    N, Kw = _packed(weight_q, weight_block_scale, "weight_q")
-    if K != Kw:
-        raise ValueError(f"the activation has K = {K}, the weight {Kw}")
-    _need_scale(alpha, "alpha", True)
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
-    ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
-    if ot == 3 or (dtype is not None and out.dtype != dtype):
-        raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
-    _need(out, "out", M * N * out.element_size(), (out.dtype,))
-    if bias is not None:
-        _need(bias, "bias", N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
-    dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, bias, out), pinned=False)
-    st = load().nvfp4_linear(q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(),
-                             weight_block_scale.data_ptr(), alpha.data_ptr(), _at(bias), out.data_ptr(), M, N, K,
-                             ot, 0 if bias is None else _DTYPE[bias.dtype], _on(stream, dev))
-    _check(st, "nvfp4_linear")
+    try:
+        dev = q.get_device()
+        M, half = q.shape
+        N, wide = weight_q.shape
+        K = 2 * half
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
+        ot = _OUT_TYPE.get(out.dtype, 3)
+        ok = (ot < 3 and wide == half and _here(dev) and (dtype is None or out.dtype is dtype)
+              and _packed_ok(dev, q, block_scale) and _packed_ok(dev, weight_q, weight_block_scale)
+              and alpha.dtype is _F32 and alpha.numel() == 1 and alpha.get_device() == dev
+              and out.is_contiguous() and out.numel() >= M * N and out.get_device() == dev
+              and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous() and bias.numel() >= N
+                                    and bias.get_device() == dev)))
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        M, K = _packed(q, block_scale, "q")
+        N, Kw = _packed(weight_q, weight_block_scale, "weight_q")
+        if K != Kw:
+            raise ValueError(f"the activation has K = {K}, the weight {Kw}")
+        _need_scale(alpha, "alpha", True)
+        ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
+        if ot == 3 or (dtype is not None and out.dtype != dtype):
+            raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
+        _need(out, "out", M * N * out.element_size(), (out.dtype,))
+        if bias is not None:
+            _need(bias, "bias", N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
+        dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, bias, out), pinned=False)
+    st = (_lib or load()).nvfp4_linear(
+        q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(), weight_block_scale.data_ptr(), alpha.data_ptr(),
+        None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K, ot,
+        0 if bias is None else _DTYPE.get(bias.dtype, 2), _on(stream, dev))
+    if st:
+        _check(st, "nvfp4_linear")
     return out
 
 
