@@ -15,7 +15,7 @@
 // them.
 #include "gemma_nq.h"
 #include "gnq_host.cuh"
-#include "gnq_kernels.cuh"
+#include "gnq_launch.cuh"
 
 namespace gnq {
 namespace {
@@ -29,16 +29,36 @@ struct QuantParams {
     int upr;             // units per row
 };
 
-// act(g) * u in fp32.  silu(g) = g / (1 + e^-g); gelu_tanh(g) =
-// g / 2 * (1 + tanh t) = g / (1 + e^-2t), t = sqrt(2/pi) (g + 0.044715 g^3).
-// The fast exponential and quotient are good to about 1e-6, far inside the
-// one rounding to 16 bits that follows; both forms go to -0 and g as g goes
-// to -inf and +inf.
-template <int ACT> __device__ __forceinline__ float act_mul(float g, float u) {
-    float t;
-    if (ACT == ACT_SILU) t = -g;
-    else t = g * fmaf(g * g, -0.0713548162726009f, -1.5957691216057308f);
-    return __fdividef(g, 1.f + __expf(t)) * u;
+// act(g) * u of two elements in fp32.  silu(g) = g / (1 + e^-g); gelu_tanh(g)
+// = g / 2 * (1 + tanh t) = g / (1 + e^-2t), t = sqrt(2/pi) (g + 0.044715 g^3).
+// The powers of two and reciprocals are the fast ones, good to about 1e-6 of
+// the result, far inside the one rounding to 16 bits that follows; both forms
+// go to -0 and to g as g goes to -inf and +inf.  The rest is paired fp32
+// arithmetic: with one operation per instruction a 16384 x 7168 batch into
+// FP8 was bound by instruction issue.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int ACT> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint64_t u) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    uint64_t t;  // the exponent of two
+    if (ACT == ACT_SILU) {
+        t = mul2(g, pk2(-kLog2e, -kLog2e));
+    } else {
+        constexpr float c1 = -1.5957691216057308f * kLog2e, c3 = -0.0713548162726009f * kLog2e;
+        t = mul2(g, fma2(mul2(g, g), pk2(c3, c3), pk2(c1, c1)));
+    }
+    float t0, t1, d0, d1;
+    upk2(t, t0, t1);
+    upk2(add2(pk2(exp2_fast(t0), exp2_fast(t1)), pk2(1.f, 1.f)), d0, d1);
+    return mul2(mul2(g, pk2(rcp_fast(d0), rcp_fast(d1))), u);
 }
 
 template <typename T, bool V8, int U>
@@ -72,6 +92,17 @@ __global__ void __launch_bounds__(256) quant_kernel(const __grid_constant__ Quan
         m[v] = m0 + r;
         col[v] = (int)(i - r * qp.upr) * E;
     }
+    // The first wave's units into L2 while the preceding grid drains: a hint
+    // (the values are read after the wait).
+    if ((int)blockIdx.x < p.pf_ctas) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (ok[v]) {
+                const uint16_t *src = p.x + m[v] * qp.row_stride + col[v];
+                prefetch_l2_line(src, false);
+                if (ACT != ACT_NONE) prefetch_l2_line(src + p.H, false);
+            }
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -94,7 +125,10 @@ __global__ void __launch_bounds__(256) quant_kernel(const __grid_constant__ Quan
                     float f[8];
                     Act<T>::unpack(u[v][c], f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[8 * c + i] = act_mul<ACT>(y[8 * c + i], f[i]);
+                    for (int i = 0; i < 8; i += 2) {
+                        float *o = &y[8 * c + i];
+                        upk2(act_mul2<ACT>(pk2(o[0], o[1]), pk2(f[i], f[i + 1])), o[0], o[1]);
+                    }
                 }
             }
             const RowOut o = row_out<MODE>(p, m[v]);
@@ -106,36 +140,54 @@ __global__ void __launch_bounds__(256) quant_kernel(const __grid_constant__ Quan
     else finish(std::integral_constant<int, FP8_PAIR>{});
 }
 
-template <typename T, int MODE, int ACT>
-cudaError_t launch_quant(QuantParams &qp, bool v8, cudaStream_t s) {
-    constexpr int E = Unit<MODE>::E, VPT = 1, NT = 256;
-    qp.upr = qp.p.H / E;
-    qp.units = qp.p.M * qp.upr;
+// Units per thread.  Several keep enough bytes in flight per SM in a large
+// batch (fp16 16384 x 8192 to NVFP4: 66.6, 61.6, 57.6 us with 1, 2, 4); the
+// gated form reads twice as much per unit (NVFP4 16384 x 7168: 87, 89, 109 us;
+// no quantization 107, 103, 107).  Small batches take one, for latency.
+template <int MODE, int ACT>
+constexpr int kUnitsPerThread = ACT == ACT_NONE ? 4 : MODE == MODE_NVFP4 ? 1 : 2;
+
+template <typename T, int MODE, int ACT, int VPT>
+cudaError_t launch_quant_vpt(QuantParams &qp, bool v8, cudaStream_t s) {
+    constexpr int NT = 256;
     const int64_t grid = (qp.units + NT * VPT - 1) / (NT * VPT);
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    auto start = [&](auto fn) {
+        qp.p.pf_ctas = one_wave_ctas(reinterpret_cast<const void *>(fn), NT);
+        return launch(fn, grid, NT, 0, 1, s, qp);
+    };
     if constexpr (MODE == MODE_NVFP4) {
-        if (v8) return launch(quant_kernel<T, MODE, ACT, VPT, true>, grid, NT, 0, 1, s, qp);
+        if (v8) return start(quant_kernel<T, MODE, ACT, VPT, true>);
     }
-    return launch(quant_kernel<T, MODE, ACT, VPT, false>, grid, NT, 0, 1, s, qp);
+    return start(quant_kernel<T, MODE, ACT, VPT, false>);
+}
+
+template <typename T, int MODE, int ACT>
+cudaError_t launch_quant(QuantParams &qp, bool v8, int sms, cudaStream_t s) {
+    constexpr int VPT = kUnitsPerThread<MODE, ACT>;
+    qp.upr = qp.p.H / Unit<MODE>::E;
+    qp.units = qp.p.M * qp.upr;
+    if (qp.units >= (int64_t)sms * 2048 * VPT) return launch_quant_vpt<T, MODE, ACT, VPT>(qp, v8, s);
+    return launch_quant_vpt<T, MODE, ACT, 1>(qp, v8, s);
 }
 
 template <typename T, int ACT>
-cudaError_t launch_quant_mode(QuantParams &qp, int mode, bool v8, cudaStream_t s) {
+cudaError_t launch_quant_mode(QuantParams &qp, int mode, bool v8, int sms, cudaStream_t s) {
     switch (mode) {
         case MODE_NONE:
-            if constexpr (ACT != ACT_NONE) return launch_quant<T, MODE_NONE, ACT>(qp, v8, s);
+            if constexpr (ACT != ACT_NONE) return launch_quant<T, MODE_NONE, ACT>(qp, v8, sms, s);
             return cudaErrorInvalidConfiguration;
-        case MODE_FP8: return launch_quant<T, MODE_FP8, ACT>(qp, v8, s);
-        case MODE_NVFP4: return launch_quant<T, MODE_NVFP4, ACT>(qp, v8, s);
-        default: return launch_quant<T, MODE_MXFP8, ACT>(qp, v8, s);
+        case MODE_FP8: return launch_quant<T, MODE_FP8, ACT>(qp, v8, sms, s);
+        case MODE_NVFP4: return launch_quant<T, MODE_NVFP4, ACT>(qp, v8, sms, s);
+        default: return launch_quant<T, MODE_MXFP8, ACT>(qp, v8, sms, s);
     }
 }
 
 template <typename T>
-cudaError_t launch_quant_act(QuantParams &qp, int mode, int act, bool v8, cudaStream_t s) {
-    if (act == ACT_SILU) return launch_quant_mode<T, ACT_SILU>(qp, mode, v8, s);
-    if (act == ACT_GELU_TANH) return launch_quant_mode<T, ACT_GELU_TANH>(qp, mode, v8, s);
-    return launch_quant_mode<T, ACT_NONE>(qp, mode, v8, s);
+cudaError_t launch_quant_act(QuantParams &qp, int mode, int act, bool v8, int sms, cudaStream_t s) {
+    if (act == ACT_SILU) return launch_quant_mode<T, ACT_SILU>(qp, mode, v8, sms, s);
+    if (act == ACT_GELU_TANH) return launch_quant_mode<T, ACT_GELU_TANH>(qp, mode, v8, sms, s);
+    return launch_quant_mode<T, ACT_NONE>(qp, mode, v8, sms, s);
 }
 
 int status_of(cudaError_t e) {
@@ -161,6 +213,8 @@ int run_quant(const void *x, int64_t row_stride, int act, const float *scale, in
     if (!aligned(x, 16) || (write_y && !aligned(y, 16)) || (mode != MODE_NONE && !aligned(q, 16)) ||
         (scale && !aligned(scale, 4)) || (block_scale && mode >= MODE_NVFP4 && !aligned(block_scale, 4)))
         return GNQ_ERR_ALIGN;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
     QuantParams qp = {};
     qp.p.x = static_cast<const uint16_t *>(x);
     qp.p.scale = scale;
@@ -174,8 +228,8 @@ int run_quant(const void *x, int64_t row_stride, int act, const float *scale, in
     qp.row_stride = row_stride;
     const bool v8 = aligned(x, 32) && row_stride % 16 == 0 && (!write_y || aligned(y, 32));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(dtype == GNQ_BF16 ? launch_quant_act<__nv_bfloat16>(qp, mode, act, v8, s)
-                                       : launch_quant_act<__half>(qp, mode, act, v8, s));
+    return status_of(dtype == GNQ_BF16 ? launch_quant_act<__nv_bfloat16>(qp, mode, act, v8, d->sms, s)
+                                       : launch_quant_act<__half>(qp, mode, act, v8, d->sms, s));
 }
 
 // ---------------------------------------------------------------------------
@@ -188,8 +242,8 @@ struct DequantParams {
     const uint8_t *block_scale;
     const float *scale;  // global scale, or nullptr for 1
     void *out;
-    int64_t blocks;      // 16-element blocks in the whole matrix
-    int bpr;             // blocks per row
+    int64_t pairs;       // pairs of 16-element blocks in the whole matrix
+    int ppr;             // pairs per row
     int Kp4;
 };
 
@@ -208,63 +262,85 @@ __device__ __forceinline__ void e2m1_values8(uint32_t w, float *f) {
     for (int i = 0; i < 4; ++i) Act<__half>::unpack2(h[i], f[2 * i], f[2 * i + 1]);
 }
 
-// A thread per 16-element block.  The block's factor is one IEEE quotient of
-// its scale and the global one; value = RN(code * factor), then one rounding
-// to the output type.
-template <int OUT, int VPT>
+// A thread takes pairs of neighbouring blocks: 16 bytes of codes, two of
+// scales, 32 values out in whole 32-byte sectors (V8) or 16-byte stores.  A
+// block's factor is one IEEE quotient of its scale and the global one; value
+// = RN(code * factor), then one rounding to the output type.
+template <int OUT, int VPT, bool V8>
 __global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ DequantParams p) {
     const int t = threadIdx.x, NT = blockDim.x;
     const int64_t base = (int64_t)blockIdx.x * (NT * VPT);
-    const int64_t m0 = base / p.bpr;
-    const uint32_t b0 = (uint32_t)(base - m0 * p.bpr);
+    const int64_t m0 = base / p.ppr;
+    const uint32_t b0 = (uint32_t)(base - m0 * p.ppr);
     pdl_wait();
     pdl_trigger();
-    uint2 code[VPT];
+    uint4 code[VPT];
     uint32_t sf[VPT];
     bool ok[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const uint32_t i = b0 + v * NT + t;
-        const uint32_t r = i / (uint32_t)p.bpr;
-        const int b = (int)(i - r * p.bpr);
+        const uint32_t r = i / (uint32_t)p.ppr;
+        const int b = 2 * (int)(i - r * p.ppr);
         const int64_t m = m0 + r, at = base + v * NT + t;
-        ok[v] = at < p.blocks;
-        code[v] = ok[v] ? __ldg(reinterpret_cast<const uint2 *>(p.q) + at) : make_uint2(0, 0);
-        sf[v] = ok[v] ? __ldg(p.block_scale + swizzled_group(m, b & ~3, p.Kp4) + (b & 3)) : 0;
+        ok[v] = at < p.pairs;
+        code[v] = make_uint4(0, 0, 0, 0);
+        sf[v] = 0;
+        if (ok[v]) {
+            code[v] = ld_stream(p.q + 16 * at);
+            sf[v] = __ldg(reinterpret_cast<const uint16_t *>(p.block_scale + swizzled_group(m, b & ~3, p.Kp4) + (b & 3)));
+        }
     }
     const float g = p.scale ? __ldg(p.scale) : 1.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        float f[16];
-        e2m1_values8(code[v].x, &f[0]);
-        e2m1_values8(code[v].y, &f[8]);
-        mul_arr_s<16>(f, __fdiv_rn(e4m3_value(sf[v]), g));
         if (!ok[v]) continue;
-        const int64_t at = (base + v * NT + t) * 16;
-        if constexpr (OUT == OUT_FP32) {
-            float *o = static_cast<float *>(p.out) + at;
+        const int64_t at = (base + v * NT + t) * 32;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                st_v4(o + 4 * c, make_uint4(__float_as_uint(f[4 * c]), __float_as_uint(f[4 * c + 1]),
-                                            __float_as_uint(f[4 * c + 2]), __float_as_uint(f[4 * c + 3])));
-        } else if constexpr (OUT == OUT_E4M3) {
-            uint8_t *o = static_cast<uint8_t *>(p.out) + at;
-            st_v4(o, make_uint4(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]),
-                                e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15])));
-        } else {
-            using T = typename std::conditional<OUT == OUT_BF16, __nv_bfloat16, __half>::type;
-            uint16_t *o = static_cast<uint16_t *>(p.out) + at;
-            st_v4(o, pack8<T>(&f[0]));
-            st_v4(o + 8, pack8<T>(&f[8]));
+        for (int h = 0; h < 2; ++h) {
+            float f[16];
+            e2m1_values8(h ? code[v].z : code[v].x, &f[0]);
+            e2m1_values8(h ? code[v].w : code[v].y, &f[8]);
+            mul_arr_s<16>(f, __fdiv_rn(e4m3_value(sf[v] >> (8 * h) & 0xFF), g));
+            uint4 w[4];
+            constexpr int N = OUT == OUT_FP32 ? 4 : OUT == OUT_E4M3 ? 1 : 2;  // 16-byte words of a block
+            if constexpr (OUT == OUT_FP32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    w[c] = make_uint4(__float_as_uint(f[4 * c]), __float_as_uint(f[4 * c + 1]),
+                                      __float_as_uint(f[4 * c + 2]), __float_as_uint(f[4 * c + 3]));
+            } else if constexpr (OUT == OUT_E4M3) {
+                w[0] = make_uint4(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]),
+                                  e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
+            } else {
+                using T = typename std::conditional<OUT == OUT_BF16, __nv_bfloat16, __half>::type;
+                w[0] = pack8<T>(&f[0]);
+                w[1] = pack8<T>(&f[8]);
+            }
+            uint8_t *o = static_cast<uint8_t *>(p.out) + (at + 16 * h) * N;
+            if constexpr (V8 && N > 1) {
+#pragma unroll
+                for (int c = 0; c < N; c += 2) st_v8(o + 16 * c, w[c], w[c + 1]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < N; ++c) st_v4(o + 16 * c, w[c]);
+            }
         }
     }
 }
 
-template <int OUT> cudaError_t launch_dequant(const DequantParams &p, cudaStream_t s) {
-    constexpr int VPT = 1, NT = 256;
-    const int64_t grid = (p.blocks + NT * VPT - 1) / (NT * VPT);
+template <int OUT, int VPT> cudaError_t launch_dequant_vpt(const DequantParams &p, cudaStream_t s) {
+    constexpr int NT = 256;
+    const int64_t grid = (p.pairs + NT * VPT - 1) / (NT * VPT);
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch(dequant_kernel<OUT, VPT>, grid, NT, 0, 1, s, p);
+    if (aligned(p.out, 32)) return launch(dequant_kernel<OUT, VPT, true>, grid, NT, 0, 1, s, p);
+    return launch(dequant_kernel<OUT, VPT, false>, grid, NT, 0, 1, s, p);
+}
+
+template <int OUT> cudaError_t launch_dequant(const DequantParams &p, int sms, cudaStream_t s) {
+    constexpr int VPT = 2;
+    if (p.pairs >= (int64_t)sms * 2048 * VPT) return launch_dequant_vpt<OUT, VPT>(p, s);
+    return launch_dequant_vpt<OUT, 1>(p, s);
 }
 
 }  // namespace
@@ -298,20 +374,22 @@ int gnq_nvfp4_dequantize(const void *q, const void *block_scale, const float *sc
     if (!gnq::aligned(q, 16) || !gnq::aligned(out, 16) || !gnq::aligned(block_scale, 4) ||
         (scale && !gnq::aligned(scale, 4)))
         return GNQ_ERR_ALIGN;
+    const gnq::DevInfo *d = gnq::dev_info();
+    if (!d) return GNQ_ERR_CUDA;
     gnq::DequantParams p;
     p.q = static_cast<const uint8_t *>(q);
     p.block_scale = static_cast<const uint8_t *>(block_scale);
     p.scale = scale;
     p.out = out;
-    p.blocks = M * (K / 16);
-    p.bpr = (int)(K / 16);
+    p.pairs = M * (K / 32);
+    p.ppr = (int)(K / 32);
     p.Kp4 = (int)(K / 64);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (out_type) {
-        case GNQ_BF16: return gnq::status_of(gnq::launch_dequant<gnq::OUT_BF16>(p, s));
-        case GNQ_FP16: return gnq::status_of(gnq::launch_dequant<gnq::OUT_FP16>(p, s));
-        case GNQ_FP32: return gnq::status_of(gnq::launch_dequant<gnq::OUT_FP32>(p, s));
-        default: return gnq::status_of(gnq::launch_dequant<gnq::OUT_E4M3>(p, s));
+        case GNQ_BF16: return gnq::status_of(gnq::launch_dequant<gnq::OUT_BF16>(p, d->sms, s));
+        case GNQ_FP16: return gnq::status_of(gnq::launch_dequant<gnq::OUT_FP16>(p, d->sms, s));
+        case GNQ_FP32: return gnq::status_of(gnq::launch_dequant<gnq::OUT_FP32>(p, d->sms, s));
+        default: return gnq::status_of(gnq::launch_dequant<gnq::OUT_E4M3>(p, d->sms, s));
     }
 }
 

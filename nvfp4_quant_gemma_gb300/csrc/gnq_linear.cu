@@ -51,6 +51,10 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const uint32_t bytes_x = (uint32_t)p.T * 128;
     const uint32_t stage_bytes = kBytesW + bytes_x + 2 * kBytesSf;
 
+    // No CTA waits for another between taking tensor memory and giving it
+    // back, so CTAs of several grids that share SMs cannot block each other:
+    // the arrival that lets peers store here comes before, the join after.
+    if (S > 1) cluster_arrive_relaxed();
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
@@ -69,8 +73,6 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t sfw_col = tmem + p.T, sfx_col = sfw_col + 16;
-
-    if (S > 1) cluster_arrive_relaxed();  // the join's stores may go to CTAs that have started
 
     // Copies of the k-th 256 elements into stage s: the weight's tile and
     // scales, then the tokens'.  (The stage and its phase are counted, not
@@ -188,6 +190,12 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         if constexpr (std::is_same<O, float>::value) *o = result(v);
         else *o = OutType<O>::round(result(v));
     };
+    auto free_tmem = [&] {
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 1) tmem_dealloc<1>(tmem, p.tmem_cols);
+        __syncwarp();
+    };
     const uint32_t lane_base = (uint32_t)warp << 21;  // 32 lanes per warp, lane number in bits 16-31
     if (S == 1) {
         // Two 16-bit columns per lane: neighbouring lanes exchange, the even
@@ -220,6 +228,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
                     for (int j = 0; j < 16; ++j)
                         if (c + j < rows) store(t0 + c + j, __uint_as_float(v[j]));
             }
+        free_tmem();
     } else {
         // Join: CTA r adds the r-th block of tokens.  Every CTA stores its
         // partial sums of a block into the shared memory of the CTA that adds
@@ -250,6 +259,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
                 }
             }
         }
+        free_tmem();
         cluster_arrive_release();
         cluster_wait();
         if (good && n < p.N)
@@ -270,9 +280,6 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
                 if (c + 3 < rows) store(t0 + c + 3, v.w);
             }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_dealloc<1>(tmem, p.tmem_cols);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -15,7 +15,7 @@
 // meets twice; both meetings are a warp shuffle tree and one barrier.
 #include "gemma_nq.h"
 #include "gnq_host.cuh"
-#include "gnq_kernels.cuh"
+#include "gnq_launch.cuh"
 
 namespace gnq {
 namespace {
@@ -45,8 +45,23 @@ __device__ __forceinline__ void load_unit(const uint16_t *src, uint4 (&d)[U]) {
     }
 }
 
-template <typename T, int MODE, int VPT, bool V8>
-__global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_constant__ SandwichParams sp) {
+// Register budget of an instance.  At four 16-byte chunks per thread and
+// operand (256 threads a row for H = 8192), 64 registers keep four rows per
+// SM: fp16 16384 x 8192 into FP8 138.2 us (6.80 TB/s) and into NVFP4 129.7 us
+// (6.79 TB/s), against 146 and 145 us with 72, 150 and 144 with 80, 187 and
+// 177 with 96, and 147 and 149 with 56, which spills.
+template <int MODE, int VPT> struct SandwichForm {
+    static constexpr int chunks = VPT * Unit<MODE>::U;  // of 16 bytes, per thread and operand
+    static constexpr int cap = 65536 / (1024 / VPT) < 255 ? 65536 / (1024 / VPT) : 255;
+    static constexpr int maxnreg = chunks == 4 ? 64 : chunks == 8 ? 128 : cap;
+};
+
+// GROWS: a gate of its own for every row, read with x and the residual (the
+// weights and a gate per channel are the same lines for every row and come
+// from L1 where they are used).  V8: 256-bit accesses.
+template <typename T, int MODE, int VPT, bool GROWS, bool V8>
+__global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VPT>::maxnreg))
+    sandwich_kernel(const __grid_constant__ SandwichParams sp) {
     constexpr int U = Unit<MODE>::U, E = Unit<MODE>::E;
     constexpr bool ESDIV = MODE == MODE_NVFP4;
     __shared__ __align__(16) float warp_ss[2][32];
@@ -68,18 +83,33 @@ __global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_const
         col[v] = (int)rank * p.seg + u * E;
         lc[v] = ok[v] ? col[v] : (int)rank * p.seg;
     }
+    // The first wave's rows into L2 while the preceding grid drains: a hint
+    // (the values are read after the wait), as in the single norm.
+    if ((int)blockIdx.x < p.pf_ctas) {
+        const int64_t seg0 = row + (int64_t)rank * p.seg;
+        for (int l = t; l < (p.seg * 2 + 127) >> 7; l += NT) {
+            prefetch_l2_line(reinterpret_cast<const char *>(p.x + seg0) + 128 * l, false);
+            prefetch_l2_line(reinterpret_cast<const char *>(p.residual + seg0) + 128 * l, false);
+        }
+    }
     pdl_wait();  // inputs may come from the preceding grid
     pdl_trigger();
 
-    uint4 xv[VPT][U], rv[VPT][U], pv[VPT][U];
+    uint4 xv[VPT][U], rv[VPT][U], gv[GROWS ? VPT : 1][U];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         load_unit<LD_STREAM, V8>(p.x + row + lc[v], xv[v]);
         load_unit<LD_INOUT, V8>(p.residual + row + lc[v], rv[v]);
+        if constexpr (GROWS) load_unit<LD_STREAM, V8>(sp.gate + m * sp.gate_stride + lc[v], gv[v]);
     }
-    if (sp.w_post) {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[v], pv[v]);
+    // One unit per thread (few rows, bound by latency): the weights come in
+    // with the activations.
+    constexpr bool W_FIRST = VPT == 1;
+    uint4 pv[U], wv[U];
+    if constexpr (W_FIRST) {
+        if (sp.w_post) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[0], pv);
+        load_unit<LD_WEIGHT, V8>(p.w + lc[0], wv);
+        if (!GROWS && sp.gate) load_unit<LD_WEIGHT, V8>(sp.gate + lc[0], gv[0]);
     }
     const QuantCtx qc = make_quant_ctx<!ESDIV>(p, MODE, nullptr, t, NT);
 
@@ -118,20 +148,22 @@ __global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_const
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        uint4 gv[U];
-        if (sp.gate) load_unit<LD_WEIGHT, false>(sp.gate + m * sp.gate_stride + lc[v], gv);
+        if constexpr (!W_FIRST) {
+            if (sp.w_post) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[v], pv);
+            if (!GROWS && sp.gate) load_unit<LD_WEIGHT, V8>(sp.gate + lc[v], gv[0]);
+        }
         float sv = 0.f;
 #pragma unroll
         for (int c = 0; c < U; ++c) {
             float x[8], f[8];
             Act<T>::unpack(xv[v][c], x);
             if (sp.w_post) {
-                Act<T>::unpack(pv[v][c], f);
+                Act<T>::unpack(pv[c], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], f[i], x[i]);  // x (1 + w_post)
             }
-            if (sp.gate) {
-                Act<T>::unpack(gv[c], f);
+            if (GROWS || sp.gate) {
+                Act<T>::unpack(gv[GROWS ? v : 0][c], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= f[i];
             }
@@ -150,9 +182,6 @@ __global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_const
             for (int c = 0; c < U; ++c) st_v4_if(o + 8 * c, hb[v][c], ok[v]);
         }
     }
-    uint4 wv[VPT][U];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) load_unit<LD_WEIGHT, V8>(p.w + lc[v], wv[v]);
     const float inv = row_inv(ss, 1);
     if (C > 1) cluster_arrive_relaxed();  // this CTA's reads of its peers are done
 
@@ -161,12 +190,13 @@ __global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_const
     auto finish = [&](auto path) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
+            if constexpr (!W_FIRST) load_unit<LD_WEIGHT, V8>(p.w + lc[v], wv);
             float y[E];
 #pragma unroll
             for (int c = 0; c < U; ++c) {
                 float w[8];
                 Act<T>::unpack(hb[v][c], &y[8 * c]);
-                Act<T>::unpack(wv[v][c], w);
+                Act<T>::unpack(wv[c], w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[8 * c + i] = fmaf(y[8 * c + i], w[i], y[8 * c + i]) * inv;
             }
@@ -179,15 +209,25 @@ __global__ void __launch_bounds__(1024 / VPT) sandwich_kernel(const __grid_const
     if (C > 1) cluster_wait();  // peers may still be reading this CTA's partials
 }
 
-template <typename T, int MODE, int VPT>
-cudaError_t launch_vpt(const SandwichParams &sp, bool v8, int cluster, cudaStream_t s) {
+template <typename T, int MODE, int VPT, bool GROWS, bool V8>
+cudaError_t launch_instance(SandwichParams &sp, int cluster, cudaStream_t s) {
+    auto fn = sandwich_kernel<T, MODE, VPT, GROWS, V8>;
     const int units = sp.p.seg / Unit<MODE>::E;
     const int threads = ((units + VPT - 1) / VPT + 31) / 32 * 32;
-    const int64_t grid = sp.p.M * cluster;
+    sp.p.pf_ctas = one_wave_ctas(reinterpret_cast<const void *>(fn), threads);
+    return launch(fn, sp.p.M * cluster, threads, 0, cluster, s, sp);
+}
+
+template <typename T, int MODE, int VPT>
+cudaError_t launch_vpt(SandwichParams &sp, bool v8, int cluster, cudaStream_t s) {
+    const bool rows = sp.gate && sp.gate_stride;
     if constexpr (MODE == MODE_NVFP4) {
-        if (v8) return launch(sandwich_kernel<T, MODE, VPT, true>, grid, threads, 0, cluster, s, sp);
+        if (v8)
+            return rows ? launch_instance<T, MODE, VPT, true, true>(sp, cluster, s)
+                        : launch_instance<T, MODE, VPT, false, true>(sp, cluster, s);
     }
-    return launch(sandwich_kernel<T, MODE, VPT, false>, grid, threads, 0, cluster, s, sp);
+    return rows ? launch_instance<T, MODE, VPT, true, false>(sp, cluster, s)
+                : launch_instance<T, MODE, VPT, false, false>(sp, cluster, s);
 }
 
 // CTAs per row: a CTA holds at most 1024 units.  0 if the row does not split.
@@ -281,6 +321,7 @@ extern "C" int gemma_sandwich_norm_quant(const void *x, void *residual, void *re
     sp.res_scale = residual_scale;
     const bool v8 = mode == MODE_NVFP4 && aligned(x, 32) && aligned(residual, 32) &&
                     aligned(residual_out, 32) && aligned(w, 32) && (!w_post || aligned(w_post, 32)) &&
+                    (!gate || (aligned(gate, 32) && gate_stride % 16 == 0)) &&
                     (!write_y || aligned(y, 32));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == GNQ_BF16

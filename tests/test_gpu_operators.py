@@ -445,3 +445,70 @@ def test_empty_batches(gnq):
     assert gnq.gated_act_quant(e, s, "fp8")[0].shape == (0, 64)
     wq, wsf = gnq.quantize(torch.zeros(32, 128, dtype=T, device="cuda"), s, "nvfp4")
     assert gnq.nvfp4_linear(q, bs, wq, wsf, s).shape == (0, 32)
+
+
+def test_linear_with_constant_weights(gnq):
+    """The weight read before the wait on the preceding grid: the same bits,
+    in a chain whose activation the preceding call writes."""
+    H, T = 1024, torch.bfloat16
+    gw, gx = _gpu_scale(12000.0), _gpu_scale(60.0)
+    gen = torch.Generator().manual_seed(7)
+    w = gnq.quantize((torch.randn(H, H, generator=gen) * 0.04).to(T).cuda(), gw, "nvfp4")
+    alpha = 1.0 / (gx * gw)
+    x0 = (torch.randn(24, H, generator=gen) * 2).to(T).cuda()
+
+    def chain():
+        x = x0
+        for _ in range(4):
+            q, bs = gnq.quantize(x, gx, "nvfp4")
+            x = gnq.nvfp4_linear(q, bs, *w, alpha)
+        torch.cuda.synchronize()
+        return x
+
+    want = chain()
+    gnq.set_constant_weights(True)
+    try:
+        for _ in range(5):
+            assert torch.equal(chain(), want)
+    finally:
+        gnq.set_constant_weights(False)
+
+
+@pytest.mark.parametrize("M,N,K", [(30, 2049, 2048), (100, 1030, 512), (300, 1001, 512), (1500, 2500, 320),
+                                   (700, 8200, 192)])
+def test_linear_many_tiles(gnq, M, N, K):
+    """More tiles than fit at a time, edges inside tiles, rows of y that tile stores cannot take."""
+    for T in (torch.bfloat16, torch.float32):
+        _run_linear(gnq, M, N, K, T, bias=torch.bfloat16, seed=M)
+
+
+def test_linear_two_streams_at_a_time(gnq):
+    """Calls of several shapes in flight on two streams give what they give alone."""
+    shapes = [(3, 2048, 2048), (60, 1024, 4096), (120, 640, 1024), (400, 1024, 1024)]
+    calls = [_run_linear(gnq, M, N, K, torch.bfloat16, seed=M) for M, N, K in shapes]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(24):
+        (args, a, y) = calls[(i * 3) % len(calls)]
+        with torch.cuda.stream(streams[i % 2]):
+            o = torch.empty_like(y)
+            gnq.nvfp4_linear(*args, a, out=o)
+            outs.append((o, y))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for o, y in outs)
+    assert gnq.read_device_error() == 0
+
+
+def test_infinities_and_nan_stay_in_their_rows(gnq):
+    """A row that overflows, and NaN scale bytes of one row, reach no other row."""
+    q, sf = random_nvfp4(70, 512, 1)
+    wq, wsf = random_nvfp4(260, 512, 2)
+    clean = gnq.nvfp4_linear(q.cuda(), sf.cuda(), wq.cuda(), wsf.cuda(), _gpu_scale(1.0), dtype=torch.float16)
+    bad = sf.view(torch.uint8).clone().reshape(-1)
+    from operators_ref import swizzle_index
+    bad[swizzle_index(70, 32)[13]] = 0x7F
+    bad = bad.reshape(sf.shape).view(torch.float8_e4m3fn)
+    y = gnq.nvfp4_linear(q.cuda(), bad.cuda(), wq.cuda(), wsf.cuda(), _gpu_scale(1.0), dtype=torch.float16)
+    keep = torch.arange(70, device="cuda") != 13
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[13]).all())
