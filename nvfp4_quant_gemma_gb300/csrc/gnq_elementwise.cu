@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ De
     for (int v = 0; v < VPT; ++v) {
         if (!ok[v]) continue;
         const int64_t at = (base + v * NT + t) * 32;
+        uint4 e4m3[2];  // E4M3: both blocks leave together
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float f[16];
@@ -310,8 +311,9 @@ __global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ De
                     w[c] = make_uint4(__float_as_uint(f[4 * c]), __float_as_uint(f[4 * c + 1]),
                                       __float_as_uint(f[4 * c + 2]), __float_as_uint(f[4 * c + 3]));
             } else if constexpr (OUT == OUT_E4M3) {
-                w[0] = make_uint4(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]),
-                                  e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
+                e4m3[h] = make_uint4(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]),
+                                     e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
+                continue;
             } else {
                 using T = typename std::conditional<OUT == OUT_BF16, __nv_bfloat16, __half>::type;
                 w[0] = pack8<T>(&f[0]);
@@ -324,6 +326,15 @@ __global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ De
             } else {
 #pragma unroll
                 for (int c = 0; c < N; ++c) st_v4(o + 16 * c, w[c]);
+            }
+        }
+        if constexpr (OUT == OUT_E4M3) {
+            uint8_t *o = static_cast<uint8_t *>(p.out) + at;
+            if constexpr (V8) {
+                st_v8(o, e4m3[0], e4m3[1]);
+            } else {
+                st_v4(o, e4m3[0]);
+                st_v4(o + 16, e4m3[1]);
             }
         }
     }
