@@ -81,7 +81,8 @@ typedef enum {
     GNQ_ERR_CUDA = 7,  /* the CUDA runtime reported an error at launch (the
                           runtime's last-error state is cleared, so the
                           caller's own later checks do not see it)         */
-    GNQ_ERR_MEMORY = 8 /* a buffer that must be device memory is not       */
+    GNQ_ERR_MEMORY = 8 /* a buffer that must be in the current device's
+                          memory is not                                    */
 } gnq_status;
 
 /* Activations are GNQ_BF16 or GNQ_FP16; GNQ_FP32 and GNQ_E4M3 are further
@@ -255,9 +256,9 @@ int gnq_nvfp4_dequantize(const void *q, const void *block_scale,
  *   bias                (N,) or NULL; of bias_type GNQ_BF16 or GNQ_FP16,
  *                       which must be out_type unless that is GNQ_FP32.
  *   y                   (M, N) of out_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
- * K is a multiple of 64, at most 65536; M and N are any sizes.  The codes and
- * block scales must be in device memory (GNQ_ERR_MEMORY) and 16-byte aligned,
- * as must y.
+ * K is a multiple of 64, at most 65536; M and N are any sizes.  The codes,
+ * block scales and y must be in the current device's memory (GNQ_ERR_MEMORY)
+ * and 16-byte aligned.
  */
 int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
                  const void *w_block_scale, const float *alpha,
@@ -334,12 +335,15 @@ int gnq_set_pdl(int enable);
  * one row per SM, with one activation rather than partials) read the norm
  * weight w and the quantization scale, and build their quantizer constants,
  * before they wait for the preceding kernel on their stream (programmatic
- * dependent launch), so that work overlaps its tail; other calls ignore the
- * flag.  The caller guarantees that no kernel that precedes a call on its
- * stream, and may still be running, writes w or scale (true when they are
- * model constants).  x, the partials and the residual are always read after
- * the wait.  Results are identical either way.  enable = 0 restores the
- * default.  Not synchronised with calls in flight on other host threads.
+ * dependent launch), so that work overlaps its tail; so do nvfp4_linear calls
+ * that run on tiles of at most 128 tokens with the first part of the weight's
+ * codes and block scales.  Other calls ignore the flag.  The caller
+ * guarantees that no kernel that precedes a call on its stream, and may still
+ * be running, writes w, the scale, or the linear's weight (true when they are
+ * model constants).  x, the partials, the residual and the linear's
+ * activation are always read after the wait.  Results are identical either
+ * way.  enable = 0 restores the default.  Not synchronised with calls in
+ * flight on other host threads.
  * Returns GNQ_ERR_SHAPE for other values.
  */
 int gnq_set_constant_weights(int enable);
@@ -347,13 +351,14 @@ int gnq_set_constant_weights(int enable);
 /*
  * Test hook for the failure path of the bounded waits (off by default).
  * With enable = 1, later launches of the persistent streaming kernel and of
- * nvfp4_linear in this process announce 16 bytes more per row than their copies deliver and give
- * a wait at most ~2^20 clock cycles, so each CTA's wait for its first row
- * (its first stage of K) gives up: the kernel sets bit 1 of the device error word, completes each
- * outstanding barrier with one more valid 16-byte copy (from w into its own
+ * nvfp4_linear in this process announce 16 bytes more per row (per stage of
+ * K) than their copies deliver and give a wait at most ~2^20 clock cycles, so
+ * each CTA's wait for its first row (stage) gives up: the kernel sets bit 1
+ * of the device error word, completes each outstanding barrier with one more
+ * valid 16-byte copy (from w, or the weight's block scales, into its own
  * shared memory, so every copy has landed before it returns), and returns
  * without writing any output.  Nothing outside the call's own buffers is
- * touched; the row kernel is unaffected.  enable = 0 restores normal
+ * touched; the other kernels are unaffected.  enable = 0 restores normal
  * launches.  Not synchronised with calls in flight on other host threads.
  * Returns GNQ_ERR_SHAPE for other values.
  */

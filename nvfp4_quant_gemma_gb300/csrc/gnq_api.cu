@@ -25,7 +25,6 @@ extern template int stream_blocks_per_sm<MODE_MXFP8>(int, bool, int, bool, bool,
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxParts = 8;
 
 // Error word written by kernels whose bounded waits gave up (bit
@@ -55,6 +54,7 @@ const DevInfo *dev_info() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
     if (g_ready[dev].load(std::memory_order_acquire) == 0) {
         DevInfo d{};
+        d.dev = dev;
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin,
                                    dev) != cudaSuccess ||
@@ -82,6 +82,15 @@ bool in_device_memory(const void *ptr) {
         return false;
     }
     return a.type == cudaMemoryTypeDevice;
+}
+
+bool on_device(const void *ptr, int dev) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeDevice && a.device == dev;
 }
 
 cudaError_t opt_in_dynamic_smem(const void *fn) {

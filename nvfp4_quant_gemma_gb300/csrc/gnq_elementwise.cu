@@ -16,6 +16,7 @@
 #include "gemma_nq.h"
 #include "gnq_host.cuh"
 #include "gnq_launch.cuh"
+#include "gnq_tcgen05.cuh"
 
 namespace gnq {
 namespace {
@@ -288,10 +289,10 @@ __global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ De
         sf[v] = 0;
         if (ok[v]) {
             code[v] = ld_stream(p.q + 16 * at);
-            sf[v] = __ldg(reinterpret_cast<const uint16_t *>(p.block_scale + swizzled_group(m, b & ~3, p.Kp4) + (b & 3)));
+            sf[v] = ld_u16(p.block_scale + swizzled_group(m, b & ~3, p.Kp4) + (b & 3));
         }
     }
-    const float g = p.scale ? __ldg(p.scale) : 1.f;
+    const float g = p.scale ? ld_f32(p.scale) : 1.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if (!ok[v]) continue;

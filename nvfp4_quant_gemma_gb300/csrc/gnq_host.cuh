@@ -11,7 +11,10 @@ namespace gnq {
 constexpr int64_t kMaxH = 65536;
 constexpr int64_t kMaxM = (int64_t)0x7FFFFFFF / 8;
 
+constexpr int kMaxDevices = 64;
+
 struct DevInfo {
+    int dev;
     int sms;
     int smem_optin;     // largest dynamic shared memory a CTA may opt in to
     unsigned int *err;  // device address of the error word
@@ -31,6 +34,8 @@ long long wait_limit_cycles();
 
 // True if `ptr` is plain device memory (not pinned host, managed or unknown).
 bool in_device_memory(const void *ptr);
+// ... of this device.
+bool on_device(const void *ptr, int dev);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

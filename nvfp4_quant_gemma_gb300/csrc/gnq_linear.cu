@@ -9,7 +9,7 @@
 // once to the output type.
 //
 // The weight takes the tensor core's M side (128 rows), the tokens its N
-// side (16 to 256), so a decode batch wastes no rows.  A scale tile of the
+// side (16 to 128), so a decode batch wastes no rows.  A scale tile of the
 // 128x4 layout is 512 contiguous bytes for 128 rows x 64 elements, exactly
 // what one copy into tensor memory takes, so scales are fetched by plain bulk
 // copies.  K advances by 256 elements (128 bytes, one swizzle row) a stage.
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         int i = 0, s = 0;
         uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         for (; i < n_k; ++i) {
-            if (!mbar_wait_bounded(empty(s), parity, p.wait_limit)) {
+            if (!warp_wait_bounded(empty(s), parity, p.wait_limit)) {
                 give_up();
                 break;
             }
@@ -141,7 +141,10 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         int s = 0;
         uint32_t parity = 0;
         for (int i = 0; i < n_k; ++i) {
-            if (!mbar_wait_bounded(full(s), parity, p.wait_limit) || (p.tx_extra && gave_up())) {
+            // (under the test hook a stage may complete late, by the copy that
+            // makes up for the announcement)
+            if (!warp_wait_bounded(full(s), parity, p.wait_limit) ||
+                (p.tx_extra && __any_sync(0xffffffffu, gave_up()))) {
                 give_up();
                 break;
             }
@@ -180,10 +183,10 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     tc_fence_after();
     __syncthreads();  // `failed` agreed on, every copy landed
     const bool good = !failed;
-    const float alpha = __ldg(p.alpha);
+    const float alpha = ld_f32(p.alpha);
     const int row = warp * 32 + lane, n = n0 + row;
     const int rows = (int)min((int64_t)p.T, p.M - t0);  // tokens in the tile
-    const float bias = p.bias && n < p.N ? OutType<B>::bias(__ldg(p.bias + n)) : 0.f;
+    const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + n)) : 0.f;
     auto result = [&](float v) { return fmaf(v, alpha, bias); };
     auto store = [&](int64_t m, float v) {
         O *const o = static_cast<O *>(p.y) + m * p.N + n;
@@ -350,11 +353,8 @@ SplitShape split_shape(const DevInfo &d, int T, int split, int KT) {
 // Clusters of `split` CTAs with tiles of T tokens that the device runs at a
 // time (0 on error), asked once per device, T and split.
 int resident_clusters(const DevInfo &d, int T, int split) {
-    constexpr int kDevices = 64;
-    static std::atomic<int> cached[kDevices][4][9];  // clusters + 1
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-    std::atomic<int> &c = cached[dev][T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3][split];
+    static std::atomic<int> cached[kMaxDevices][4][9];  // clusters + 1
+    std::atomic<int> &c = cached[d.dev][T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3][split];
     int n = c.load() - 1;
     if (n < 0) {
         auto fn = linear_kernel<__nv_bfloat16, __nv_bfloat16>;
@@ -442,9 +442,8 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
         return GNQ_ERR_ALIGN;
     const DevInfo *d = dev_info();
     if (!d) return GNQ_ERR_CUDA;
-    if (!in_device_memory(q) || !in_device_memory(block_scale) || !in_device_memory(w_q) ||
-        !in_device_memory(w_block_scale))
-        return GNQ_ERR_MEMORY;
+    for (const void *buf : {q, block_scale, w_q, w_block_scale, static_cast<const void *>(y)})
+        if (!on_device(buf, d->dev)) return GNQ_ERR_MEMORY;
     LinearParams p = {};
     p.w_sf = static_cast<const uint8_t *>(w_block_scale);
     p.x_sf = static_cast<const uint8_t *>(block_scale);

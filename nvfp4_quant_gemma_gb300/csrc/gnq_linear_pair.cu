@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
+constexpr int kBand = 4;                                            // tile rows of a band
 constexpr uint32_t kHalf = 128 * kStageK / 2;                       // 128 rows of codes of one stage
 constexpr uint32_t kPairStage = 2 * kHalf + 3 * kBytesSf;           // per CTA
 constexpr uint32_t kChunk = 32 * 128;                               // 32 rows x 128 bytes of output
@@ -90,7 +91,7 @@ __device__ __forceinline__ void scale_bias32(const PairParams &pp, int n, const 
         for (int i = 0; i < 32; i += 8) Act<B>::unpack(ld_weight(p.bias + n + i), &b[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) b[i] = n + i < p.N ? OutType<B>::bias(__ldg(p.bias + n + i)) : 0.f;
+        for (int i = 0; i < 32; ++i) b[i] = n + i < p.N ? OutType<B>::bias(ld_u16(p.bias + n + i)) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(acc[i]), alpha, b[i]);
@@ -184,13 +185,13 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
 
     const int KT = (p.K64 + 3) / 4;
     const int tiles = pp.m_tiles * pp.n_tiles, G = gridDim.x / 2;
-    // Bands of 8 tile rows, walked column by column: the tiles in flight at
-    // one time share few rows and columns.
+    // Bands of tile rows, walked column by column: the tiles in flight at one
+    // time share few rows and columns.
     auto tile_at = [&](int i, int &mt, int &nt) {
-        const int band = i / (8 * pp.n_tiles), in = i - band * 8 * pp.n_tiles;
-        const int rows = min(8, pp.m_tiles - 8 * band);
+        const int band = i / (kBand * pp.n_tiles), in = i - band * kBand * pp.n_tiles;
+        const int rows = min(kBand, pp.m_tiles - kBand * band);
         nt = in / rows;
-        mt = 8 * band + in - nt * rows;
+        mt = kBand * band + in - nt * rows;
     };
     auto gave_up = [&] { return *(volatile int *)&failed != 0; };
     auto give_up = [&] {
@@ -203,13 +204,13 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
         int it = 0, s = 0;
         uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         const uint32_t x_row = 128 * rank;
-        for (int i = blockIdx.x / 2; i < tiles && !gave_up(); i += G) {
+        for (int i = blockIdx.x / 2; i < tiles && !__any_sync(0xffffffffu, gave_up()); i += G) {
             int mt, nt;
             tile_at(i, mt, nt);
             const int x0 = mt * kPairTile + x_row, w0 = nt * kPairTile + x_row;
             const int xs = (2 * mt + rank) * p.K64, ws = 2 * nt * p.K64;
             for (int kt = 0; kt < KT; ++kt, ++it) {
-                if (!mbar_wait_bounded(empty(s), parity, p.wait_limit)) {
+                if (!warp_wait_bounded(empty(s), parity, p.wait_limit)) {
                     give_up();
                     break;
                 }
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
         uint32_t parity = 0;
         bool good = true;
         for (int i = blockIdx.x / 2; good && i < tiles; i += G, ++j) {
-            if (j > 0 && !mbar_wait_bounded(shared_free, (j - 1) & 1, p.wait_limit)) {
+            if (j > 0 && !warp_wait_bounded(shared_free, (j - 1) & 1, p.wait_limit)) {
                 give_up();
                 break;
             }
@@ -252,7 +253,8 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
             for (int kt = 0; kt < KT; ++kt) {
                 // (under the test hook a stage may complete late, by the copy
                 // that makes up for the announcement)
-                if (!mbar_wait_bounded(full(s), parity, p.wait_limit) || (p.tx_extra && gave_up())) {
+                if (!warp_wait_bounded(full(s), parity, p.wait_limit) ||
+                    (p.tx_extra && __any_sync(0xffffffffu, gave_up()))) {
                     give_up();
                     good = false;
                     break;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
         // ---- sums out ----
         // Warps 2-5 take the shared columns of a tile first and then the
         // third chunk of 64, warps 6-9 the second and the fourth.
-        const float alpha = __ldg(p.alpha);
+        const float alpha = ld_f32(p.alpha);
         const int quad = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
         const uint32_t free_bar = map_to_cta(shared_free, 0);

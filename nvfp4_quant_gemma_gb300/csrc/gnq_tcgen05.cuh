@@ -28,6 +28,25 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Bounded wait of a whole converged warp, with one answer for all its lanes:
+// a lane that gave up takes the others along, so the warp stays converged.
+__device__ __forceinline__ bool warp_wait_bounded(uint32_t bar, uint32_t parity, long long limit) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
+}
+
+// Reads of small operands that the preceding grid may have written: not to be
+// moved ahead of the wait for it.
+__device__ __forceinline__ float ld_f32(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_u16(const void *p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // ---- tensor memory ----
 template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
     if constexpr (CG == 1)
