@@ -286,10 +286,6 @@ def _place(tensors, pinned: bool = True) -> int:
     return torch.cuda.current_device() if dev is None else dev
 
 
-def _on(stream, dev: int):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
 def _rows(x, name: str):
     """(rows, columns, row stride) of a 2-D 16-bit matrix with dense rows."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
@@ -321,19 +317,14 @@ def _need_scale(scale, name: str, required: bool) -> None:
         raise ValueError(f"{name} must be a 1-element fp32 tensor")
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 # Each call below first tries its whole argument check as one expression (all
 # tensors on the current CUDA device, the common case: a call of a decode step
 # takes microseconds, most of them here); what that does not pass goes through
 # the step-by-step check, which names the fault or admits pinned host memory.
 _U8, _F32, _E4M3 = torch.uint8, torch.float32, torch.float8_e4m3fn
-
-
-def _here(dev: int) -> bool:
-    return dev >= 0 and dev == torch._C._cuda_getDevice()
+# the current device and its current stream, without torch.cuda's wrappers
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _outputs_ok(dev: int, M: int, H: int, m: int, dt, write_y: bool, q, bs, y) -> bool:
@@ -378,8 +369,10 @@ def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None,
     ``residual_out``, or in place to ``residual``.  ``mode`` is "none" (y
     only), "fp8", "nvfp4" or "mxfp8"; ``out`` may supply (q, block_scale, y).
     Returns (q, block_scale, y) as gemma_add_rms_norm_quant does."""
-    m = _mode(mode)
-    M, H, _ = _rows(x, "x")
+    m = _MODES[mode] if type(mode) is str else _mode(mode)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a 2-D bf16/fp16 tensor")
+    M, H = x.shape
     dt = x.dtype
     write_y = bool(write_y) or m == -1
     gate_stride = 0 if gate is None else _gate_stride(gate, M, H, dt)
@@ -387,7 +380,7 @@ def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None,
     dev = x.get_device()
     n, w = 2 * M * H, 2 * H
     try:
-        ok = (_here(dev) and x.is_contiguous()
+        ok = (dev >= 0 and dev == _current_device() and x.is_contiguous()
               and residual.dtype is dt and residual.is_contiguous() and residual.nbytes >= n
               and residual.get_device() == dev
               and weight.dtype is dt and weight.is_contiguous() and weight.nbytes >= w and weight.get_device() == dev
@@ -414,8 +407,10 @@ def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None,
     st = (_lib or load()).gemma_sandwich_norm_quant(
         x.data_ptr(), residual.data_ptr(), None if residual_out is None else residual_out.data_ptr(),
         None if post_weight is None else post_weight.data_ptr(), weight.data_ptr(),
-        None if gate is None else gate.data_ptr(), gate_stride, residual_scale, eps, _at(scale), m,
-        1 if write_y else 0, _at(q), _at(bs), _at(y), M, H, _DTYPE[dt], _on(stream, dev))
+        None if gate is None else gate.data_ptr(), gate_stride, residual_scale, eps,
+        None if scale is None else scale.data_ptr(), m, 1 if write_y else 0, None if q is None else q.data_ptr(),
+        None if bs is None else bs.data_ptr(), None if y is None else y.data_ptr(), M, H, _DTYPE[dt],
+        _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "gemma_sandwich_norm_quant")
     return q, (scale if m == 0 else bs), (y if write_y else None)
@@ -426,20 +421,25 @@ def quantize(x, scale=None, mode="nvfp4", out=None, stream=None):
     a multiple of 8): ``mode`` "fp8", "nvfp4" or "mxfp8".  ``out`` may supply
     (q, block_scale).  Returns (q, block_scale); for FP8 block_scale is
     ``scale`` itself."""
-    m = _mode(mode)
+    m = _MODES[mode] if type(mode) is str else _mode(mode)
+    if m < 0:
+        raise ValueError("quantize needs a quantization mode")
     M, H, stride = _rows(x, "x")
     q, bs = out if out is not None else alloc_outputs(M, H, m, False, x)[:2]
     dev = x.get_device()
     try:
-        ok = _here(dev) and _scale_ok(dev, m, scale) and _outputs_ok(dev, M, H, m, None, False, q, bs, None)
+        ok = (dev >= 0 and dev == _current_device() and _scale_ok(dev, m, scale)
+              and _outputs_ok(dev, M, H, m, None, False, q, bs, None))
     except AttributeError:
         ok = False
     if not ok:
         _need_scale(scale, "scale", m in (0, 1))
         _need_outputs(M, H, m, x.dtype, False, (q, bs, None))
         dev = _place((x, scale, q, bs if m > 0 else None))
-    st = (_lib or load()).gnq_quantize(x.data_ptr(), stride, _at(scale), m, _at(q), _at(bs) if m > 0 else None, M,
-                                       H, _DTYPE[x.dtype], _on(stream, dev))
+    st = (_lib or load()).gnq_quantize(
+        x.data_ptr(), stride, None if scale is None else scale.data_ptr(), m, q.data_ptr(),
+        bs.data_ptr() if m > 0 else None, M, H, _DTYPE[x.dtype],
+        _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "quantize")
     return q, (scale if m == 0 else bs)
@@ -450,7 +450,7 @@ def gated_act_quant(x, scale=None, mode="nvfp4", act="gelu_tanh", write_y=False,
     between the two products of a gated MLP.  ``act`` is "silu" or
     "gelu_tanh"; ``mode`` "none" (y only), "fp8", "nvfp4" or "mxfp8"; ``out``
     may supply (q, block_scale, y).  Returns (q, block_scale, y)."""
-    m = _mode(mode)
+    m = _MODES[mode] if type(mode) is str else _mode(mode)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     M, W, stride = _rows(x, "x")
@@ -461,15 +461,19 @@ def gated_act_quant(x, scale=None, mode="nvfp4", act="gelu_tanh", write_y=False,
     q, bs, y = out if out is not None else alloc_outputs(M, H, m, write_y, x)
     dev = x.get_device()
     try:
-        ok = _here(dev) and _scale_ok(dev, m, scale) and _outputs_ok(dev, M, H, m, x.dtype, write_y, q, bs, y)
+        ok = (dev >= 0 and dev == _current_device() and _scale_ok(dev, m, scale)
+              and _outputs_ok(dev, M, H, m, x.dtype, write_y, q, bs, y))
     except AttributeError:
         ok = False
     if not ok:
         _need_scale(scale, "scale", m in (0, 1))
         _need_outputs(M, H, m, x.dtype, write_y, (q, bs, y))
         dev = _place((x, scale, q if m >= 0 else None, bs if m > 0 else None, y if write_y else None))
-    st = (_lib or load()).gated_act_quant(x.data_ptr(), stride, _ACTS[act], _at(scale), m, 1 if write_y else 0,
-                                          _at(q), _at(bs), _at(y), M, H, _DTYPE[x.dtype], _on(stream, dev))
+    st = (_lib or load()).gated_act_quant(
+        x.data_ptr(), stride, _ACTS[act], None if scale is None else scale.data_ptr(), m, 1 if write_y else 0,
+        None if q is None else q.data_ptr(), None if bs is None else bs.data_ptr(),
+        None if y is None else y.data_ptr(), M, H, _DTYPE[x.dtype],
+        _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "gated_act_quant")
     return q, (scale if m == 0 else bs), (y if write_y else None)
@@ -500,7 +504,7 @@ def nvfp4_dequantize(q, block_scale, scale=None, dtype=None, out=None, stream=No
         K = 2 * half
         if out is None and dev >= 0:
             out = torch.empty((M, K), dtype=dtype or torch.bfloat16, device=q.device)
-        ok = (_here(dev) and _packed_ok(dev, q, block_scale)
+        ok = (dev >= 0 and dev == _current_device() and _packed_ok(dev, q, block_scale)
               and (scale is None or (scale.dtype is _F32 and scale.numel() == 1 and scale.get_device() == dev))
               and out.dtype in _OUT_TYPE and (dtype is None or out.dtype is dtype) and out.is_contiguous()
               and out.numel() >= M * K and out.get_device() == dev)
@@ -511,12 +515,14 @@ def nvfp4_dequantize(q, block_scale, scale=None, dtype=None, out=None, stream=No
         _need_scale(scale, "scale", False)
         if out is None:
             out = torch.empty((M, K), dtype=dtype or torch.bfloat16, pin_memory=True)
-        if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
+        if (not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE
+                or (dtype is not None and out.dtype != dtype)):
             raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
         _need(out, "out", M * K * out.element_size(), (out.dtype,))
         dev = _place((q, block_scale, scale, out))
-    st = (_lib or load()).gnq_nvfp4_dequantize(q.data_ptr(), block_scale.data_ptr(), _at(scale), out.data_ptr(), M,
-                                               K, _OUT_TYPE[out.dtype], _on(stream, dev))
+    st = (_lib or load()).gnq_nvfp4_dequantize(
+        q.data_ptr(), block_scale.data_ptr(), None if scale is None else scale.data_ptr(), out.data_ptr(), M, K,
+        _OUT_TYPE[out.dtype], _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "nvfp4_dequantize")
     return out
@@ -537,7 +543,8 @@ def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None,
         if out is None:
             out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
         ot = _OUT_TYPE.get(out.dtype, 3)
-        ok = (ot < 3 and wide == half and _here(dev) and (dtype is None or out.dtype is dtype)
+        ok = (ot < 3 and wide == half and dev >= 0 and dev == _current_device()
+              and (dtype is None or out.dtype is dtype)
               and _packed_ok(dev, q, block_scale) and _packed_ok(dev, weight_q, weight_block_scale)
               and alpha.dtype is _F32 and alpha.numel() == 1 and alpha.get_device() == dev
               and out.is_contiguous() and out.numel() >= M * N and out.get_device() == dev
@@ -561,7 +568,7 @@ def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None,
     st = (_lib or load()).nvfp4_linear(
         q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(), weight_block_scale.data_ptr(), alpha.data_ptr(),
         None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K, ot,
-        0 if bias is None else _DTYPE.get(bias.dtype, 2), _on(stream, dev))
+        0 if bias is None else _DTYPE.get(bias.dtype, 2), _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "nvfp4_linear")
     return out
