@@ -58,6 +58,8 @@ const DevInfo *dev_info() {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin,
                                    dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) !=
+                cudaSuccess ||
             cudaGetSymbolAddress(reinterpret_cast<void **>(&d.err), g_device_error) !=
                 cudaSuccess)
             return nullptr;

@@ -17,6 +17,7 @@ struct DevInfo {
     int dev;
     int sms;
     int smem_optin;     // largest dynamic shared memory a CTA may opt in to
+    int smem_sm;        // shared memory of an SM
     unsigned int *err;  // device address of the error word
 };
 

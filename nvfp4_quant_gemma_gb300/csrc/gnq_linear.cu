@@ -335,7 +335,8 @@ namespace {
 
 // Shared memory of a split: half of an SM's where two stages fit it (two CTAs
 // of one grid run there, or the next grid's start up beside the last ones of
-// this one), else all.
+// this one), else all.  Up to 64 tokens three stages are as many as help (M =
+// 16, N = 8192, K = 5120 in four parts: 5.5, 5.3, 5.6 us with 2, 3, 4).
 struct SplitShape {
     int stages;
     size_t smem;
@@ -345,24 +346,25 @@ SplitShape split_shape(const DevInfo &d, int T, int split, int KT) {
     const int64_t join = split > 1 ? (int64_t)join_block(T, split) * split * kTileN * 4 : 0;
     const int64_t whole = d.smem_optin - 1024 - 512 - join, half = (d.smem_optin - 1024 - 512) / 2 - 1024 - join;
     const int64_t room = half >= 2 * stage ? half : whole;
-    const int stages =
-        std::max(1, (int)std::min<int64_t>({kMaxStages, room / stage, (KT + split - 1) / split}));
+    const int stages = std::max(
+        1, (int)std::min<int64_t>({T <= 64 ? 3 : kMaxStages, room / stage, (KT + split - 1) / split}));
     return {stages, (size_t)(1024 + stages * stage + join)};
 }
 
-// Clusters of `split` CTAs with tiles of T tokens that the device runs at a
-// time (0 on error), asked once per device, T and split.
-int resident_clusters(const DevInfo &d, int T, int split) {
-    static std::atomic<int> cached[kMaxDevices][4][9];  // clusters + 1
-    std::atomic<int> &c = cached[d.dev][T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3][split];
+// Clusters of `split` CTAs that the device runs at a time with one CTA per SM
+// (0 on error), asked once per device: SMs of a processing cluster that do
+// not make a whole one stay idle (GB300: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
+int resident_clusters(const DevInfo &d, int split) {
+    static std::atomic<int> cached[kMaxDevices][9];  // clusters + 1
+    std::atomic<int> &c = cached[d.dev][split];
     int n = c.load() - 1;
     if (n < 0) {
         auto fn = linear_kernel<__nv_bfloat16, __nv_bfloat16>;
         if (opt_in_dynamic_smem(reinterpret_cast<const void *>(fn)) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)split, 1, 1);
+        cfg.gridDim = dim3((unsigned)(split * d.sms), 1, 1);
         cfg.blockDim = dim3(128, 1, 1);
-        cfg.dynamicSmemBytes = split_shape(d, T, split, 1 << 20).smem;
+        cfg.dynamicSmemBytes = (size_t)d.smem_optin / 2 + 4096;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = (unsigned)split;
@@ -379,19 +381,23 @@ int resident_clusters(const DevInfo &d, int T, int split) {
 }
 
 // Tile and split of a call: the smallest tile that holds the tokens (128 at
-// most), and K split over the largest cluster of which the device runs all at
-// a time, each CTA keeping two stages or more.  One round of CTAs is what
-// counts: with one stage of K more per round a split pays until its clusters
-// no longer fit (M = 16, N = 8192, K = 5120: 8.4, 6.4, 6.1, 5.6 us for 1 to
-// 4, then 9.6 us for 6, in two rounds).
+// most), and K split over the largest cluster of which all run at a time, each
+// CTA keeping two stages of K or more.  A further round of CTAs costs more
+// than a deeper split gives (M = 16, N = 8192, K = 5120: 7.8, 6.1, 5.8, 5.3 us
+// for 1 to 4 parts, then 8.8 us for 6, in two rounds; N = 5120: 4.9 us for 6,
+// 8.0 for 8).  At 64 tokens a join of more than six parts costs more too (N =
+// 2048: 5.45 us for 6, 6.0 for 8).
 void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &grid, size_t &smem) {
     p.T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
     const int KT = (p.K64 + 3) / 4;
     const int64_t tiles = p.n_tiles * ((M + p.T - 1) / p.T);
     p.split = 1;
-    for (int c = std::min(8, KT / 2); c > 1 && p.split == 1; --c)
-        if (tiles <= d.sms && resident_clusters(d, p.T, c) >= tiles) p.split = c;
+    if (tiles <= d.sms)
+        for (int c = std::min(p.T >= 64 ? 6 : 8, KT / 2); c > 1 && p.split == 1; --c) {
+            const int64_t per_sm = d.smem_sm / ((int64_t)split_shape(d, p.T, c, KT).smem + 1024 + 512);
+            if (resident_clusters(d, c) * per_sm >= tiles) p.split = c;
+        }
     grid = tiles * p.split;
     const SplitShape ss = split_shape(d, p.T, p.split, KT);
     p.stages = ss.stages;
