@@ -72,9 +72,13 @@ __device__ __forceinline__ void load_unit(const uint16_t *p, uint4 (&v)[U]) {
     }
 }
 
-// V8: 32-byte aligned 16-bit tensors move a unit's block in one access.
+// V8: 32-byte aligned 16-bit tensors move a unit's block in one access.  Six
+// CTAs per SM for four 8-element units a thread (bf16 16384 x 8192 to FP8:
+// 68.8, 67.9, 65.7, 64.1 us with the compiler's choice, 4, 5 and 6; NVFP4's
+// 16-element units spill there: 57.2 us with its choice, 69 and 77 with 5 and
+// 6).
 template <typename T, int MODE, int ACT, int VPT, bool V8>
-__global__ void __launch_bounds__(256) quant_kernel(const __grid_constant__ QuantParams qp) {
+__global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) quant_kernel(const __grid_constant__ QuantParams qp) {
     constexpr int U = Unit<MODE>::U, E = Unit<MODE>::E;
     const Params &p = qp.p;
     const int t = threadIdx.x, NT = blockDim.x;
