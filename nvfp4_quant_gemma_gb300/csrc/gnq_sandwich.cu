@@ -239,9 +239,11 @@ int row_cluster(int64_t H, int mode) {
     return units <= 1024 * c ? c : 0;
 }
 
-// One unit per thread while there are fewer rows than SMs (latency), else
-// about 256 threads per row; rows wider than 1024 units are split over a
-// cluster, as for the single norm.
+// One unit per thread while all rows run at a time so (1024 threads of that
+// form per SM; M = 256, H = 4096 without quantization: 2.9 us against 3.7 at
+// two units), else about 256 threads per row (512 or more: 16384 x 8192 into
+// FP8 309 us); rows wider than 1024 units are split over a cluster, as for the
+// single norm.
 template <typename T, int MODE>
 cudaError_t launch_sandwich(SandwichParams &sp, bool v8, int sms, cudaStream_t s) {
     constexpr int E = Unit<MODE>::E;
@@ -249,7 +251,8 @@ cudaError_t launch_sandwich(SandwichParams &sp, bool v8, int sms, cudaStream_t s
     sp.p.seg = sp.p.H / cluster;
     const int units = sp.p.seg / E;
     int vpt = 1;
-    while (vpt < 4 && sp.p.M >= sms && units > 256 * vpt) vpt *= 2;
+    const int per_sm = 1024 / ((units + 31) / 32 * 32);  // rows at one unit per thread
+    while (vpt < 4 && sp.p.M * cluster > (int64_t)sms * per_sm && units > 256 * vpt) vpt *= 2;
     switch (vpt) {
         case 1: return launch_vpt<T, MODE, 1>(sp, v8, cluster, s);
         case 2: return launch_vpt<T, MODE, 2>(sp, v8, cluster, s);

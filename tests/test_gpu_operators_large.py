@@ -65,11 +65,11 @@ def test_sandwich(gnq):
     q, sf, y = gnq.gemma_sandwich_norm_quant(x, r, wp, w, 1e-6, s, "nvfp4", gate=gate, write_y=True)
     for b in blocks:
         rows = slice(128 * b, 128 * b + 128)
-        # 256 rows, so that the small call is launched in the same shape
-        two = lambda t: torch.cat((t, t))
-        rr = two(r0[b])
-        q1, sf1, y1 = gnq.gemma_sandwich_norm_quant(two(x[rows]), rr, wp, w, 1e-6, s, "nvfp4", gate=two(gate[rows]),
-                                                    write_y=True)
+        # 512 rows, so that the small call is launched in the same shape
+        four = lambda t: torch.cat((t, t, t, t))
+        rr = four(r0[b])
+        q1, sf1, y1 = gnq.gemma_sandwich_norm_quant(four(x[rows]), rr, wp, w, 1e-6, s, "nvfp4",
+                                                    gate=four(gate[rows]), write_y=True)
         assert torch.equal(r[rows], rr[:128]) and torch.equal(y[rows], y1[:128]) and torch.equal(q[rows], q1[:128]), b
         assert torch.equal(sf.view(torch.uint8).view(-1, 128 * H // 16)[b], sf1.view(torch.uint8).view(-1)[:128 * H // 16]), b
 
