@@ -1,4 +1,5 @@
-"""GB300-native fused Gemma add-RMSNorm + FP8 / NVFP4 input quantization.
+"""GB300-native fused Gemma add-RMSNorm + FP8 / NVFP4 input quantization, and
+the operators around the NVFP4 linear that follows it.
 
 The compute path is the sm_103a library ``libgemma_nq.so`` (C ABI declared in
 ``include/gemma_nq.h``); the functions below are its thin Python binding.

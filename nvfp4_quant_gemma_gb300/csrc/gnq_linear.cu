@@ -13,6 +13,12 @@
 // 128x4 layout is 512 contiguous bytes for 128 rows x 64 elements, exactly
 // what one copy into tensor memory takes, so scales are fetched by plain bulk
 // copies.  K advances by 256 elements (128 bytes, one swizzle row) a stage.
+//
+// A decode batch is bound by the weight's bytes and, at these sizes, by
+// latency: launch, the first copy, the join and the stores are 3.5 us of the
+// 5.3 us of M = 16, N = 8192, K = 5120 (23.9 MB, 3.5 us at 6.8 TB/s; M = 1,
+// N = 4096, K = 2048: 3.5 us).  So K is split until one round of CTAs fills
+// the SMs, and the split is joined in shared memory across a cluster.
 #include <algorithm>
 #include <atomic>
 

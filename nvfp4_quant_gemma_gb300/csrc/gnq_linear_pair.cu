@@ -1,11 +1,17 @@
 // NVFP4 product for large batches: CTA pairs on 256 x 256 tiles.
 //
-// What bounds it is the FP4 rate of the tensor cores, so the design keeps
-// them fed: a pair of CTAs issues one 256 x 256 x 64 product over both SMs
-// (each reads half of the weight tile, which halves the traffic into shared
-// memory), five stages of 256 elements of K are in flight, CTAs are
-// persistent, and the sums of one tile leave tensor memory while the next
-// tile is computed.
+// A pair of CTAs issues one 256 x 256 x 64 product over both SMs, each with
+// half of the weight tile in its shared memory; five stages of 256 elements of
+// K are in flight, CTAs are persistent, and the sums of one tile leave tensor
+// memory while the next tile is computed.
+//
+// What bounds it: a stage is 512 cycles of the tensor cores but 38 912 bytes
+// into each SM, and 608 cycles at 64 bytes a cycle is what a stage takes with
+// the scale copies into tensor memory left out (650 with them; on 40 pairs as
+// on 76, so it is the SM's intake, not the L2).  A larger tile does not fit
+// tensor memory.  The rest is the hand-over between tiles, about 1300 cycles.
+// 4864 x 8192 x 16384: 188 us, 6.9 PFLOP/s; 8192 x 8192 x 5120 (14 rounds for
+// 13.5 of tiles): 113 us, 6.1 PFLOP/s.
 //
 // Tensor memory (512 columns): the sums of even tiles in columns 0-255, of
 // odd tiles in 192-447, the scales behind.  Two whole tiles and the scales do
@@ -28,7 +34,7 @@
 namespace gnq {
 namespace {
 
-constexpr int kPairTile = 256;
+constexpr int kPairTile = 256;   // tokens and weight rows of a tile
 constexpr int kPairStages = 5;
 constexpr int kBand = 4;                                            // tile rows of a band
 constexpr uint32_t kHalf = 128 * kStageK / 2;                       // 128 rows of codes of one stage
