@@ -512,3 +512,158 @@ def test_infinities_and_nan_stay_in_their_rows(gnq):
     y = gnq.nvfp4_linear(q.cuda(), bad.cuda(), wq.cuda(), wsf.cuda(), _gpu_scale(1.0), dtype=torch.float16)
     keep = torch.arange(70, device="cuda") != 13
     assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[13]).all())
+
+
+# ---------------------------------------------------------------------------
+# places, streams, threads, capture
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("mode", ["none", "fp8", "nvfp4", "mxfp8"])
+def test_pinned_host_buffers_give_the_bits_of_device_ones(gnq, mode):
+    M, H, T = 130, 1024, torch.bfloat16
+    x, r, wp, w, gate = _sandwich_inputs(M, H, T, 21, "rows")
+    xg = torch.randn(M, 2 * H, generator=torch.Generator().manual_seed(1)).to(T)
+    s = _gpu_scale(SCALE[mode])
+    pin = lambda t: None if t is None else t.cpu().pin_memory()
+
+    def same(a, b):
+        torch.cuda.synchronize()
+        for u, v in zip(a, b):
+            if u is not None and v is not None and u.dim() > 1:
+                n = min(u.numel(), v.numel())
+                u, v = u.cpu().view(torch.uint8), v.cpu().view(torch.uint8)
+                if mode == "nvfp4" and u.shape[1] == H // 16:  # padding rows of the scales are not written
+                    from operators_ref import swizzle_index
+                    i = swizzle_index(M, H // 16).reshape(-1)
+                    u, v = u.reshape(-1)[i], v.reshape(-1)[i]
+                assert torch.equal(u, v) and n > 0
+
+    for post in (wp, None):
+        h1, h2 = torch.empty_like(r), pin(r)
+        a = gnq.gemma_sandwich_norm_quant(x, r, post, w, 1e-6, s, mode, gate=gate, residual_out=h1, write_y=True)
+        b = gnq.gemma_sandwich_norm_quant(pin(x), pin(r), pin(post), pin(w), 1e-6, pin(s), mode, gate=pin(gate),
+                                          residual_out=h2, write_y=True)
+        assert not b[2].is_cuda
+        same((*a, h1), (*b, h2))
+    same(gnq.gated_act_quant(xg.cuda(), s, mode, write_y=True), gnq.gated_act_quant(pin(xg), pin(s), mode, write_y=True))
+    if mode != "none":
+        same(gnq.quantize(x, s, mode), gnq.quantize(pin(x), pin(s), mode))
+    if mode == "nvfp4":
+        q, bs = gnq.quantize(x, s, mode)
+        same((gnq.nvfp4_dequantize(q, bs, s),), (gnq.nvfp4_dequantize(pin(q), pin(bs), pin(s)),))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e30])
+def test_fp8_extreme_scales(gnq, scale):
+    """Scales outside the corrected quotient's range, on the division path."""
+    M, H, T = 33, 512, torch.bfloat16
+    x, r, wp, w, _ = _sandwich_inputs(M, H, T, 2, "none")
+    q, _, y = gnq.gemma_sandwich_norm_quant(x, r, wp, w, 1e-6, _gpu_scale(scale), "fp8", write_y=True)
+    check_codes(oracle, y, q, None, scale, "fp8", "bf16")
+    q, _, y = gnq.gated_act_quant(x, _gpu_scale(scale), "fp8", act="silu", write_y=True)
+    check_codes(oracle, y, q, None, scale, "fp8", "bf16")
+
+
+def test_gate_forms_agree(gnq):
+    """One gate per channel, the same expanded over the rows, and the same
+    written out per row; a single row's gate in two dimensions."""
+    M, H, T = 200, 2048, torch.bfloat16
+    x, r, wp, w, gate = _sandwich_inputs(M, H, T, 8, "channels")
+    outs = []
+    for g in (gate, gate.expand(M, H), gate.expand(M, H).contiguous()):
+        h = torch.empty_like(r)
+        y = gnq.gemma_sandwich_norm_quant(x, r, wp, w, 1e-6, None, "none", gate=g, residual_out=h)[2]
+        outs.append((h, y))
+    for h, y in outs[1:]:
+        assert torch.equal(h, outs[0][0]) and torch.equal(y, outs[0][1])
+    one = gnq.gemma_sandwich_norm_quant(x[:1], r[:1].clone(), wp, w, 1e-6, None, "none", gate=gate)[2]
+    two = gnq.gemma_sandwich_norm_quant(x[:1], r[:1].clone(), wp, w, 1e-6, None, "none", gate=gate[None])[2]
+    assert torch.equal(one, two)
+
+
+def test_linear_deepest_and_of_a_matrix_with_itself(gnq):
+    _run_linear(gnq, 5, 130, 65536, torch.bfloat16, seed=3)
+    _run_linear(gnq, 400, 300, 65536, torch.float32, seed=4)
+    q, sf = random_nvfp4(200, 512, 9)
+    q, sf = q.cuda(), sf.cuda()
+    y = gnq.nvfp4_linear(q, sf, q, sf, _gpu_scale(0.01), dtype=torch.float32)
+    y64, mag = linear64(q, sf, q, sf, float(torch.tensor(0.01)))
+    assert_within(y, y64, linear_tolerance(y64, mag, 512, torch.float32), "y")
+
+
+def test_a_stream_given_and_two_host_threads(gnq):
+    """Calls on a stream that is not the current one, from two threads at a time."""
+    import threading
+    T = torch.bfloat16
+    gw = _gpu_scale(300.0)
+    work = []
+    for i, M in enumerate((7, 300)):
+        x = torch.randn(M, 1024, generator=torch.Generator().manual_seed(i)).to(T).cuda()
+        w = torch.randn(640, 1024, generator=torch.Generator().manual_seed(9 + i)).to(T).cuda()
+        wq = gnq.quantize(w, gw, "nvfp4")
+        want = gnq.nvfp4_linear(*gnq.quantize(x, gw, "nvfp4"), *wq, _gpu_scale(1e-5))
+        work.append((x, wq, want, torch.cuda.Stream()))
+    alpha = _gpu_scale(1e-5)
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(x, wq, want, stream):
+        try:
+            outs = gnq.alloc_outputs(*x.shape, "nvfp4", False, x)[:2]
+            ys = [torch.empty_like(want) for _ in range(40)]
+            stream.wait_stream(torch.cuda.default_stream())
+            for y in ys:
+                q, sf = gnq.quantize(x, gw, "nvfp4", out=outs, stream=stream)
+                gnq.nvfp4_linear(q, sf, *wq, alpha, out=y, stream=stream)
+            stream.synchronize()
+            if not all(torch.equal(y, want) for y in ys):
+                errors.append("results differ")
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=a) for a in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every operator's first call is captured: what the library asks the
+    runtime for on first use is allowed there."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, nvfp4_quant_gemma_gb300 as gnq
+T = torch.bfloat16
+dev = torch.device("cuda")
+x = torch.randn(40, 512, device=dev).to(T); r = torch.randn(40, 512, device=dev).to(T); w = torch.randn(512, device=dev).to(T)
+s = torch.full((1,), 100.0, device=dev); a = torch.full((1,), 1e-4, device=dev)
+wq = torch.randint(0, 256, (1024, 256), dtype=torch.uint8, device=dev)
+wsf = torch.randint(0x28, 0x50, (1024, 32), dtype=torch.uint8, device=dev)
+big = torch.randint(0, 256, (600, 256), dtype=torch.uint8, device=dev)
+bsf = torch.randint(0x28, 0x50, (640, 32), dtype=torch.uint8, device=dev)
+h = torch.empty_like(r)
+torch.cuda.synchronize()
+
+def run():
+    q, sf, _ = gnq.gemma_sandwich_norm_quant(x, r, w, w, 1e-6, s, "nvfp4", residual_out=h)
+    y = gnq.nvfp4_linear(q, sf, wq, wsf, a)
+    q2, sf2, _ = gnq.gated_act_quant(y, s, "nvfp4")
+    q3, sf3 = gnq.quantize(x, s, "nvfp4")
+    return y, q2, gnq.nvfp4_dequantize(q3, sf3, s), gnq.nvfp4_linear(big, bsf, wq, wsf, a)
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+for u, v in zip(got, run()):
+    assert torch.equal(u, v)
+assert gnq.read_device_error() == 0
+print("capture ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert res.returncode == 0 and "capture ok" in res.stdout, res.stderr[-2000:]
