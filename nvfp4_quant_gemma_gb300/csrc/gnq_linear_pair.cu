@@ -294,8 +294,6 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
         if (elect_one()) tc_commit_pair(done);
         __syncwarp();
         if (!mbar_wait_bounded(done, 0, p.wait_limit)) give_up();
-    } else if (warp == 1) {
-        if (!mbar_wait_bounded(done, 0, 4 * p.wait_limit)) give_up();  // the first CTA's last arrival here
     } else if (warp >= 2) {
         // ---- sums out ----
         // Warps 2-5 take the shared columns of a tile first and then the
@@ -356,6 +354,9 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // the first CTA's last arrival here, before these barriers go away
+    if (rank == 1 && warp == 1 && !mbar_wait_bounded(done, 0, p.wait_limit)) give_up();
+    __syncwarp();
     cluster_arrive_release();
     cluster_wait();  // the peer's copies and barriers are no longer in use
     if (warp == 1) tmem_dealloc<2>(tmem, 512);

@@ -45,6 +45,16 @@ __device__ __forceinline__ void load_unit(const uint16_t *src, uint4 (&d)[U]) {
     }
 }
 
+// 1 / sqrt(v) with one Newton step on the fast value, which brings its error
+// from two units in the last place to about half a unit: it scales a whole row
+// of h, so its error is kept below that of the other steps.  (Values near the
+// ends of the range stay as they are: the step would turn 0 and inf into NaN.)
+__device__ __forceinline__ float rsqrt_refined(float v) {
+    const float y = rsqrtf(v);
+    const float e = fmaf(-v * y, y, 1.f);
+    return v > 0x1p-100f && v < 0x1p100f ? fmaf(0.5f * y, e, y) : y;
+}
+
 // Register budget of an instance.  At four 16-byte chunks per thread and
 // operand (256 threads a row for H = 8192), 64 registers keep four rows per
 // SM: fp16 16384 x 8192 into FP8 138.2 us (6.80 TB/s) and into NVFP4 129.7 us
@@ -126,7 +136,7 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
             tot = 0.f;
             for (uint32_t r = 0; r < C; ++r) tot += ld_peer_f32(&cta_ss[k], r);
         }
-        return inv_rms(p, tot);
+        return rsqrt_refined(fmaf(tot, p.inv_h, p.eps));
     };
 
     // ---- the norm after the block ----
