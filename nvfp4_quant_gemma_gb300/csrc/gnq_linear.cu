@@ -108,11 +108,15 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     pdl_wait();  // inputs may come from the preceding grid, outputs may still be read by it
     pdl_trigger();
 
+    // read now, used at the end
+    const int row = warp * 32 + lane, n = n0 + row;
+    const float alpha = ld_f32(p.alpha);
+    const uint16_t bias16 = p.bias && n < p.N ? ld_u16(p.bias + n) : 0;
+
     auto give_up = [&] {
         atomicOr(p.err, (unsigned)DEVERR_WAIT_TIMEOUT);
         *(volatile int *)&failed = 1;
     };
-
     auto gave_up = [&] { return *(volatile int *)&failed != 0; };
     if (warp == 0) {
         // ---- copies ----
@@ -189,10 +193,8 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     tc_fence_after();
     __syncthreads();  // `failed` agreed on, every copy landed
     const bool good = !failed;
-    const float alpha = ld_f32(p.alpha);
-    const int row = warp * 32 + lane, n = n0 + row;
     const int rows = (int)min((int64_t)p.T, p.M - t0);  // tokens in the tile
-    const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + n)) : 0.f;
+    const float bias = OutType<B>::bias(bias16);  // bits 0: +0
     auto result = [&](float v) { return fmaf(v, alpha, bias); };
     auto store = [&](int64_t m, float v) {
         O *const o = static_cast<O *>(p.y) + m * p.N + n;

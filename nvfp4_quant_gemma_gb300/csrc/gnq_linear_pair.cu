@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(320) linear_pair_kernel(
         for (int i = blockIdx.x / 2; i < tiles; i += G, ++j) {
             int mt, nt;
             tile_at(i, mt, nt);
+            // the tile's bias on its way while the products finish
+            if (p.bias && lane < 4 && nt * kPairTile + 64 * lane < p.N)
+                prefetch_l1_line(p.bias + nt * kPairTile + 64 * lane);
             const bool ok = mbar_wait_bounded(acc_full, j & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
             if (!__all_sync(0xffffffffu, ok)) {
                 give_up();

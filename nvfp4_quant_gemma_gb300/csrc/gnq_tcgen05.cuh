@@ -47,6 +47,8 @@ __device__ __forceinline__ uint16_t ld_u16(const void *p) {
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l1_line(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // ---- tensor memory ----
 template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
     if constexpr (CG == 1)
