@@ -12,9 +12,9 @@
 // neighbouring threads neighbouring units, so rows of any width keep every
 // lane busy.  The arithmetic that decides a code is that of the norm kernels
 // (epilogue_unit), so equal 16-bit values give equal codes whatever produced
-// them.  Measured on 16384 rows: fp16 8192 wide to NVFP4 57.2 us (6.0 TB/s),
+// them.  Measured on 16384 rows: fp16 8192 wide to NVFP4 54.6 us (6.3 TB/s),
 // bf16 to FP8 64.0 us (6.3), NVFP4 to bf16 50.1 us (6.9), SiLU of 7168 columns
-// to NVFP4 84.5 us (6.3).
+// to NVFP4 78.6 us (6.8).
 #include "gemma_nq.h"
 #include "gnq_host.cuh"
 #include "gnq_launch.cuh"
@@ -30,6 +30,7 @@ struct QuantParams {
     int64_t row_stride;  // elements from one row of x to the next
     int64_t units;       // units in the whole matrix
     int upr;             // units per row
+    int rows_ahead;      // rows from a unit to the one prefetched in its place
 };
 
 // act(g) * u of two elements in fp32.  silu(g) = g / (1 + e^-g); gelu_tanh(g)
@@ -120,6 +121,20 @@ __global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) q
         load_unit<T, V8>(src, g[v]);
         if constexpr (ACT != ACT_NONE) load_unit<T, V8>(src + p.H, u[v]);
     }
+    // The units that take this place three quarters of a round from now, into
+    // L2 with the evict-last priority: bytes in flight that need no register
+    // (SiLU of 16384 x 7168 to NVFP4 84.5 -> 75.3 us, tanh-GELU to FP8 100.7 ->
+    // 94.5, without quantization 106.9 -> 100.8, fp16 16384 x 8192 to NVFP4
+    // 57.2 -> 55.6; the plain FP8 and MXFP8 instances spill with it and lose).
+    if constexpr (ACT != ACT_NONE || MODE == MODE_NVFP4) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (m[v] + qp.rows_ahead < p.M) {
+                const uint16_t *src = p.x + (m[v] + qp.rows_ahead) * qp.row_stride + col[v];
+                prefetch_l2_line(src, true);
+                if (ACT != ACT_NONE) prefetch_l2_line(src + p.H, true);
+            }
+    }
     const QuantCtx qc = make_quant_ctx<false>(p, MODE, nullptr, t, NT);
     auto finish = [&](auto path) {
 #pragma unroll
@@ -161,6 +176,7 @@ cudaError_t launch_quant_vpt(QuantParams &qp, bool v8, cudaStream_t s) {
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     auto start = [&](auto fn) {
         qp.p.pf_ctas = one_wave_ctas(reinterpret_cast<const void *>(fn), NT);
+        qp.rows_ahead = (int)(((int64_t)qp.p.pf_ctas * 3 / 4 * NT * VPT + qp.upr - 1) / qp.upr);
         return launch(fn, grid, NT, 0, 1, s, qp);
     };
     if constexpr (MODE == MODE_NVFP4) {

@@ -57,20 +57,21 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
 
 // Register budget of an instance.  At four 16-byte chunks per thread and
 // operand (256 threads a row for H = 8192), 64 registers keep four rows per
-// SM: fp16 16384 x 8192 into FP8 138.2 us (6.80 TB/s) and into NVFP4 129.7 us
-// (6.79 TB/s), against 146 and 145 us with 72, 150 and 144 with 80, 187 and
-// 177 with 96, and 147 and 149 with 56, which spills.
-template <int MODE, int VPT> struct SandwichForm {
+// SM; with 72, 80 and 96 the fp16 16384 x 8192 batch lost 6, 9 and 36 % into
+// FP8 and 11, 11 and 37 % into NVFP4, and with 56, which spills, 7 and 15 %.
+// With a gate 64 spill too (bf16 2048 x 5120 into NVFP4 18.1 us, 16.1 with 72).
+// Now: fp16 16384 x 8192 into FP8 133.5 us (7.0 TB/s), into NVFP4 122.9 (7.2).
+template <int MODE, int VPT, bool GATED> struct SandwichForm {
     static constexpr int chunks = VPT * Unit<MODE>::U;  // of 16 bytes, per thread and operand
     static constexpr int cap = 65536 / (1024 / VPT) < 255 ? 65536 / (1024 / VPT) : 255;
-    static constexpr int maxnreg = chunks == 4 ? 64 : chunks == 8 ? 128 : cap;
+    static constexpr int maxnreg = chunks == 4 ? (GATED ? 72 : 64) : chunks == 8 ? 128 : cap;
 };
 
-// GROWS: a gate of its own for every row, read with x and the residual (the
-// weights and a gate per channel are the same lines for every row and come
-// from L1 where they are used).  V8: 256-bit accesses.
-template <typename T, int MODE, int VPT, bool GROWS, bool V8>
-__global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VPT>::maxnreg))
+// GATED: a gate, per row or per channel, read with x and the residual (where
+// it is used, after the first row sum, it cost bf16 16384 x 8192 302 us
+// against 179).  V8: 256-bit accesses.
+template <typename T, int MODE, int VPT, bool GATED, bool V8>
+__global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VPT, GATED>::maxnreg))
     sandwich_kernel(const __grid_constant__ SandwichParams sp) {
     constexpr int U = Unit<MODE>::U, E = Unit<MODE>::E;
     constexpr bool ESDIV = MODE == MODE_NVFP4;
@@ -105,12 +106,34 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     pdl_wait();  // inputs may come from the preceding grid
     pdl_trigger();
 
-    uint4 xv[VPT][U], rv[VPT][U], gv[GROWS ? VPT : 1][U];
+    uint4 xv[VPT][U], rv[VPT][U], gv[GATED ? VPT : 1][U];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         load_unit<LD_STREAM, V8>(p.x + row + lc[v], xv[v]);
         load_unit<LD_INOUT, V8>(p.residual + row + lc[v], rv[v]);
-        if constexpr (GROWS) load_unit<LD_STREAM, V8>(sp.gate + m * sp.gate_stride + lc[v], gv[v]);
+        if constexpr (GATED) {
+            if (sp.gate_stride) load_unit<LD_STREAM, V8>(sp.gate + m * sp.gate_stride + lc[v], gv[v]);
+            else load_unit<LD_WEIGHT, V8>(sp.gate + lc[v], gv[v]);
+        }
+    }
+    // Many rows: the one that takes a place three quarters of a round from
+    // now, into L2 with the evict-last priority, so that DRAM stays busy while
+    // the resident rows are at their sums (bf16 2048 x 5120 into FP8 15.5 ->
+    // 13.8 us, fp16 16384 x 8192 into NVFP4 130.4 -> 123.2; a quarter or a
+    // whole round ahead gains less on the large ones, a few per cent more or
+    // less on the small).
+    if constexpr (VPT > 1) {
+        const int64_t ahead = m + p.pf_ctas * 3 / 4;
+        if (C == 1 && ahead < p.M) {
+            const char *x = reinterpret_cast<const char *>(p.x + ahead * p.H);
+            const char *r = reinterpret_cast<const char *>(p.residual + ahead * p.H);
+            const char *g = reinterpret_cast<const char *>(sp.gate + ahead * sp.gate_stride);
+            for (int l = 128 * t; l < 2 * p.H; l += 128 * NT) {
+                prefetch_l2_line(x + l, true);
+                prefetch_l2_line(r + l, true);
+                if (GATED && sp.gate_stride) prefetch_l2_line(g + l, true);
+            }
+        }
     }
     // One unit per thread (few rows, bound by latency): the weights come in
     // with the activations.
@@ -119,7 +142,6 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     if constexpr (W_FIRST) {
         if (sp.w_post) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[0], pv);
         load_unit<LD_WEIGHT, V8>(p.w + lc[0], wv);
-        if (!GROWS && sp.gate) load_unit<LD_WEIGHT, V8>(sp.gate + lc[0], gv[0]);
     }
     const QuantCtx qc = make_quant_ctx<!ESDIV>(p, MODE, nullptr, t, NT);
 
@@ -160,7 +182,6 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     for (int v = 0; v < VPT; ++v) {
         if constexpr (!W_FIRST) {
             if (sp.w_post) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[v], pv);
-            if (!GROWS && sp.gate) load_unit<LD_WEIGHT, V8>(sp.gate + lc[v], gv[0]);
         }
         float sv = 0.f;
 #pragma unroll
@@ -172,8 +193,8 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], f[i], x[i]);  // x (1 + w_post)
             }
-            if (GROWS || sp.gate) {
-                Act<T>::unpack(gv[GROWS ? v : 0][c], f);
+            if constexpr (GATED) {
+                Act<T>::unpack(gv[v][c], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= f[i];
             }
@@ -219,9 +240,9 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     if (C > 1) cluster_wait();  // peers may still be reading this CTA's partials
 }
 
-template <typename T, int MODE, int VPT, bool GROWS, bool V8>
+template <typename T, int MODE, int VPT, bool GATED, bool V8>
 cudaError_t launch_instance(SandwichParams &sp, int cluster, cudaStream_t s) {
-    auto fn = sandwich_kernel<T, MODE, VPT, GROWS, V8>;
+    auto fn = sandwich_kernel<T, MODE, VPT, GATED, V8>;
     const int units = sp.p.seg / Unit<MODE>::E;
     const int threads = ((units + VPT - 1) / VPT + 31) / 32 * 32;
     sp.p.pf_ctas = one_wave_ctas(reinterpret_cast<const void *>(fn), threads);
@@ -230,13 +251,13 @@ cudaError_t launch_instance(SandwichParams &sp, int cluster, cudaStream_t s) {
 
 template <typename T, int MODE, int VPT>
 cudaError_t launch_vpt(SandwichParams &sp, bool v8, int cluster, cudaStream_t s) {
-    const bool rows = sp.gate && sp.gate_stride;
+    const bool gated = sp.gate != nullptr;
     if constexpr (MODE == MODE_NVFP4) {
         if (v8)
-            return rows ? launch_instance<T, MODE, VPT, true, true>(sp, cluster, s)
+            return gated ? launch_instance<T, MODE, VPT, true, true>(sp, cluster, s)
                         : launch_instance<T, MODE, VPT, false, true>(sp, cluster, s);
     }
-    return rows ? launch_instance<T, MODE, VPT, true, false>(sp, cluster, s)
+    return gated ? launch_instance<T, MODE, VPT, true, false>(sp, cluster, s)
                 : launch_instance<T, MODE, VPT, false, false>(sp, cluster, s);
 }
 
