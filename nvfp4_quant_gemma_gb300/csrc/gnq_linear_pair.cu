@@ -22,7 +22,7 @@
 // warps packs 32 rows of a chunk into shared memory and a tile store writes
 // it as whole lines (stores straight from the registers touch 32 rows per
 // instruction: 4864 x 8192 x 512 took 58 us with them).  An output whose rows
-// are not 16-byte aligned is stored value by value.
+// are not 16-byte aligned leaves from there row by row.
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA),
 // 2-9 take sums out: two warps for each 32 rows, chunks in turn.
@@ -112,32 +112,44 @@ __device__ __forceinline__ void store_chunk(const PairParams &pp, const CUtensor
     float v[COLS];
 #pragma unroll
     for (int h = 0; h < COLS / 32; ++h) scale_bias32<B>(pp, n + 32 * h, acc[h], alpha, v + 32 * h);
-    if (pp.tiled) {
-        constexpr int PER = COLS / 8;  // values per 16 bytes
+    constexpr int PER = COLS / 8;  // values per 16 bytes
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint4 w;
-            if constexpr (PER == 8) w = pack8<O>(&v[8 * i]);
-            else w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + 128u * lane + 16u * (i ^ (lane & 7))),
-                         "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                         : "memory");
-        }
+    for (int i = 0; i < 8; ++i) {
+        uint4 w;
+        if constexpr (PER == 8) w = pack8<O>(&v[8 * i]);
+        else w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                            __float_as_uint(v[4 * i + 3]));
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + 128u * lane + 16u * (i ^ (lane & 7))),
+                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                     : "memory");
+    }
+    if (pp.tiled) {
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
             if (m0 < p.M && n < p.N) tma_store_2d(map_y, n, (int)m0, buf);
-            tma_store_commit();  // a group per chunk, empty or not: the buffers take turns by count
+            tma_store_commit();  // a group per chunk, empty or not: the buffer is free by count
         }
-    } else if (m0 + lane < p.M) {
-        O *o = static_cast<O *>(p.y) + (m0 + lane) * p.N + n;
-#pragma unroll
-        for (int i = 0; i < COLS; ++i)
-            if (n + i < p.N) {
-                if constexpr (sizeof(O) == 4) o[i] = v[i];
-                else o[i] = OutType<O>::round(v[i]);
+    } else {
+        // rows of y that a tile store cannot take: each in one go of the warp,
+        // a word per lane (two values that are stored apart where N is odd)
+        __syncwarp();
+        constexpr int W = 4 / sizeof(O);  // values per word
+        const int col = n + W * lane, live = (int)min((int64_t)32, p.M - m0);
+        O *o = static_cast<O *>(p.y) + m0 * p.N + col;
+        for (int r = 0; r < live; ++r, o += p.N) {
+            uint32_t w;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(w)
+                         : "r"(buf + 128u * r + 16u * ((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+            if (W == 1 || p.N % 2 == 0) {
+                if (col < p.N) *reinterpret_cast<uint32_t *>(o) = w;
+            } else {
+                uint16_t *h = reinterpret_cast<uint16_t *>(o);
+                if (col < p.N) h[0] = (uint16_t)w;
+                if (col + 1 < p.N) h[1] = (uint16_t)(w >> 16);
             }
+        }
     }
     __syncwarp();
 }
