@@ -137,17 +137,25 @@ __device__ __forceinline__ void store_chunk(const PairParams &pp, const CUtensor
         constexpr int W = 4 / sizeof(O);  // values per word
         const int col = n + W * lane, live = (int)min((int64_t)32, p.M - m0);
         O *o = static_cast<O *>(p.y) + m0 * p.N + col;
-        for (int r = 0; r < live; ++r, o += p.N) {
-            uint32_t w;
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(w)
-                         : "r"(buf + 128u * r + 16u * ((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
-            if (W == 1 || p.N % 2 == 0) {
-                if (col < p.N) *reinterpret_cast<uint32_t *>(o) = w;
-            } else {
-                uint16_t *h = reinterpret_cast<uint16_t *>(o);
-                if (col < p.N) h[0] = (uint16_t)w;
-                if (col + 1 < p.N) h[1] = (uint16_t)(w >> 16);
+        for (int r0 = 0; r0 < live; r0 += 4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k;
+                asm volatile("ld.shared.u32 %0, [%1];"
+                             : "=r"(w[k])
+                             : "r"(buf + 128u * r + 16u * ((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k, o += p.N) {
+                if (r0 + k >= live) break;
+                if (W == 1 || p.N % 2 == 0) {
+                    if (col < p.N) *reinterpret_cast<uint32_t *>(o) = w[k];
+                } else {
+                    uint16_t *h = reinterpret_cast<uint16_t *>(o);
+                    if (col < p.N) h[0] = (uint16_t)w[k];
+                    if (col + 1 < p.N) h[1] = (uint16_t)(w[k] >> 16);
+                }
             }
         }
     }
