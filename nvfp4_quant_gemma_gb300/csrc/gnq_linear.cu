@@ -417,12 +417,15 @@ void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &
 // Both times follow the rounds of CTAs and the depth of K; the constants, in
 // microseconds, are fits to calls of 128 to 512 tokens (M = 128, N = 2048,
 // K = 5120: 7.8 against 10.4 us for pairs; 300 x 5000 x 4096: 11.4 against
-// 10.2; 512 x 4096 x 4096: 13 against 9.6).
-bool pairs_take(const DevInfo &d, int64_t M, int64_t N, const LinearParams &p, int64_t grid) {
+// 10.2; 512 x 4096 x 4096: 13 against 9.6).  Pairs store an output with rows
+// off 16 bytes more slowly (141 x 176 x 1088: 6.3 us for pairs, 7.2; 141 x 169:
+// 8.9 and 7.2).
+bool pairs_take(const DevInfo &d, int64_t M, int64_t N, int out_size, const LinearParams &p, int64_t grid) {
     if (M <= 64) return false;
     const int KT = (p.K64 + 3) / 4;
     const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), pairs = d.sms / 2;
-    const double pair = 4.2 + (double)((tiles + pairs - 1) / pairs) * (0.31 * KT + 0.4);
+    const double rounds = (double)((tiles + pairs - 1) / pairs);
+    const double pair = 4.2 + rounds * (0.31 * KT + 0.4) + (N * out_size % 16 ? 1.0 + 1.5 * rounds : 0.0);
     const double single = 3.0 + (double)((grid + d.sms - 1) / d.sms) * 0.47 * ((KT + p.split - 1) / p.split) +
                           (p.split > 1 ? 2.5 : 0.0);
     return pair < single;
@@ -476,7 +479,7 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     int64_t grid = 0;
     size_t smem = 0;
     shape_of(*d, M, N, p, grid, smem);
-    if (grid > 0x7FFFFFFF || pairs_take(*d, M, N, p, grid)) {
+    if (grid > 0x7FFFFFFF || pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid)) {
         e = launch_linear_pair(p, q, w_q, out_type, bias_type, d->sms, s);
         if (e == cudaSuccess) return GNQ_OK;
         cudaGetLastError();

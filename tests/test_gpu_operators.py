@@ -667,3 +667,29 @@ print("capture ok")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
     assert res.returncode == 0 and "capture ok" in res.stdout, res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float32])
+def test_linear_large_with_unaligned_rows(gnq, T):
+    """Rows of y that are not 16-byte aligned in a batch large enough for
+    256 x 256 tiles: the bits of the aligned call on the same weight rows,
+    some of which are held to the 64-bit form."""
+    M, N, K = 4101, 1296, 4096
+    q, sf = random_nvfp4(M, K, 1)
+    wq, wsf = random_nvfp4(N, K, 2)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    a = _gpu_scale(1e-3)
+    args = (q.cuda(), sf.cuda())
+    whole = gnq.nvfp4_linear(*args, wq.cuda(), wsf.cuda(), a, bias=bias.cuda(), dtype=T)
+    for n in (1290, 1291):
+        G = Guarded()
+        y = G((M, n), T)
+        gnq.nvfp4_linear(*args, wq.cuda()[:n], wsf.cuda(), a, bias=bias.cuda()[:n].contiguous(), out=y)
+        torch.cuda.synchronize()
+        G.check()
+        assert torch.equal(y, whole[:, :n])
+    rows = slice(4096, 4101)
+    tail = sf.reshape(-1, 128 * K // 16)[32:].reshape(-1, K // 16)
+    y64, mag = linear64(q[rows], tail, wq, wsf, float(a.cpu()), bias)
+    assert_within(whole[rows], y64, linear_tolerance(y64, mag, K, T), "y")
+    assert gnq.read_device_error() == 0
