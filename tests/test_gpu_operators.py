@@ -693,3 +693,33 @@ def test_linear_large_with_unaligned_rows(gnq, T):
     y64, mag = linear64(q[rows], tail, wq, wsf, float(a.cpu()), bias)
     assert_within(whole[rows], y64, linear_tolerance(y64, mag, K, T), "y")
     assert gnq.read_device_error() == 0
+
+
+def test_linear_wait_timeout_of_cta_pairs_writes_nothing(gnq):
+    """The same failure path in the kernel of large batches, whose CTA pairs wait on one another."""
+    M, N, K = 600, 8192, 1024
+    q, sf = random_nvfp4(M, K, 1)
+    wq, wsf = random_nvfp4(N, K, 2)
+    args = [t.cuda() for t in (q, sf, wq, wsf)]
+    want = gnq.nvfp4_linear(*args, _gpu_scale(1e-3))
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gnq.read_device_error()
+    gnq.inject_wait_timeout(True)
+    try:
+        gnq.nvfp4_linear(*args, _gpu_scale(1e-3), out=y)
+        torch.cuda.synchronize()
+    finally:
+        gnq.inject_wait_timeout(False)
+    assert gnq.read_device_error(clear=True) & 1
+    assert bool((y == 7.0).all())
+    assert torch.equal(gnq.nvfp4_linear(*args, _gpu_scale(1e-3)), want)
+    assert gnq.read_device_error() == 0
+
+
+@pytest.mark.parametrize("T,bias", [(torch.bfloat16, torch.bfloat16), (torch.float16, None), (torch.float32, torch.float16)])
+@pytest.mark.parametrize("M,N,K", [(600, 8200, 1088), (513, 8184, 1216), (770, 8192, 1280), (1300, 8193, 1152)])
+def test_linear_cta_pairs(gnq, M, N, K, T, bias):
+    """Shapes whose depth and tile count go to the 256 x 256 tiles of CTA
+    pairs (two rounds of them and more), with edges inside tiles of rows,
+    columns and K, against the 64-bit form."""
+    _run_linear(gnq, M, N, K, T, bias=bias, seed=M)
