@@ -365,6 +365,17 @@ int gnq_set_constant_weights(int enable);
 int gnq_inject_wait_timeout(int enable);
 
 /*
+ * Test hook for a split product that loses one part (off by default, cta =
+ * -1).  With cta = 0..7, later launches of nvfp4_linear that share a tile's K
+ * among several CTAs (a cluster) make that CTA of each cluster alone give up, in
+ * the way gnq_inject_wait_timeout does; bit 1 of the device error word is set
+ * and no CTA of the cluster writes output.  Launches without such a CTA are
+ * unaffected.  Not synchronised with calls in flight on other host threads.
+ * Returns GNQ_ERR_SHAPE for other values.
+ */
+int gnq_inject_split_timeout(int cta);
+
+/*
  * Device error word of the current device.  Every wait inside a kernel is
  * bounded; a kernel whose wait gives up (about a second without progress)
  * skips the rest of its work, sets bit 1 here and returns, leaving its

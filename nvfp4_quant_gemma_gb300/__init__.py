@@ -14,6 +14,7 @@ from ._binding import (  # noqa: F401
     gemma_add_rms_norm_quant,
     gemma_add_rms_norm_quant_parts,
     gemma_sandwich_norm_quant,
+    inject_split_timeout,
     inject_wait_timeout,
     library_path,
     nvfp4_dequantize,

@@ -59,6 +59,7 @@ def load() -> ctypes.CDLL:
             "gnq_set_pdl": [I],
             "gnq_set_constant_weights": [I],
             "gnq_inject_wait_timeout": [I],
+            "gnq_inject_split_timeout": [I],
             "gnq_quantize_fp8_values": [P, i64, P, P, P],
             "gnq_pdl_consumer": [P, i64, P, i64, P, I, P],
             "gnq_encode_e4m3_e2m1": [P, i64, P, P, P],
@@ -78,7 +79,7 @@ EXPORTS = ("gemma_add_rms_norm", "gemma_add_rms_norm_quant", "gemma_add_rms_norm
            "add_rms_norm_quant", "gnq_status_string", "gnq_set_launch_policy",
            "gnq_read_device_error", "gnq_set_pdl", "gnq_encode_e4m3_e2m1",
            "gnq_quantize_fp8_values", "gnq_query_launch", "gnq_set_constant_weights",
-           "gnq_inject_wait_timeout", "gnq_pdl_consumer", "gemma_sandwich_norm_quant",
+           "gnq_inject_wait_timeout", "gnq_inject_split_timeout", "gnq_pdl_consumer", "gemma_sandwich_norm_quant",
            "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear")
 
 
@@ -623,6 +624,12 @@ def inject_wait_timeout(enable: bool) -> None:
     """Test hook: later streaming launches make their bounded waits give up
     (device error bit 1, no outputs written); off by default."""
     _check(load().gnq_inject_wait_timeout(1 if enable else 0), "gnq_inject_wait_timeout")
+
+
+def inject_split_timeout(cta: int = -1) -> None:
+    """Test hook: CTA ``cta`` (0..7) of each cluster of later split products
+    gives up, alone (device error bit 1, no outputs written); -1 turns it off."""
+    _check(load().gnq_inject_split_timeout(int(cta)), "gnq_inject_split_timeout")
 
 
 def read_device_error(clear: bool = True) -> int:

@@ -41,9 +41,7 @@ std::atomic<int> g_force_form{0};  // 0 auto, 1 fp32 form, 2 packed (lean) form
 std::atomic<int> g_pdl{1};  // 1: launch as programmatic dependents, 0: plain launches
 std::atomic<int> g_const_w{0};  // 1: small batches read w and scale before the PDL wait
 std::atomic<int> g_inject_timeout{0};  // test hook: streaming waits give up (see the header)
-
-constexpr long long kWaitLimit = 1LL << 31;      // cycles: about a second
-constexpr long long kTestWaitLimit = 1LL << 20;  // cycles: under a millisecond
+std::atomic<int> g_inject_split{-1};   // test hook: this CTA of a split product gives up
 
 }  // namespace
 
@@ -72,6 +70,7 @@ const DevInfo *dev_info() {
 bool pdl_on() { return g_pdl.load() != 0; }
 bool constant_weights_on() { return g_const_w.load() != 0; }
 bool inject_timeout_on() { return g_inject_timeout.load() != 0; }
+int inject_split_timeout() { return g_inject_split.load(); }
 long long wait_limit_cycles() { return inject_timeout_on() ? kTestWaitLimit : kWaitLimit; }
 
 // True if `ptr` is plain device memory: the only memory the streaming
@@ -584,6 +583,12 @@ int gnq_set_constant_weights(int enable) {
 int gnq_inject_wait_timeout(int enable) {
     if (enable != 0 && enable != 1) return GNQ_ERR_SHAPE;
     gnq::g_inject_timeout.store(enable);
+    return GNQ_OK;
+}
+
+int gnq_inject_split_timeout(int cta) {
+    if (cta < -1 || cta > 7) return GNQ_ERR_SHAPE;
+    gnq::g_inject_split.store(cta);
     return GNQ_OK;
 }
 

@@ -25,12 +25,15 @@ struct DevInfo {
 const DevInfo *dev_info();
 
 // The switches of gnq_set_pdl, gnq_set_constant_weights and
-// gnq_inject_wait_timeout.
+// gnq_inject_wait_timeout; the CTA that gnq_inject_split_timeout names (-1: off).
 bool pdl_on();
 bool constant_weights_on();
 bool inject_timeout_on();
+int inject_split_timeout();
 
-// Clock cycles a bounded wait may spin (shorter under the test hook).
+// Clock cycles a bounded wait may spin (shorter under the test hooks).
+constexpr long long kWaitLimit = 1LL << 31;      // about a second
+constexpr long long kTestWaitLimit = 1LL << 20;  // under a millisecond
 long long wait_limit_cycles();
 
 // True if `ptr` is plain device memory (not pinned host, managed or unknown).

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     __shared__ __align__(16) uint4 topup[kMaxStages];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
+    __shared__ uint32_t cta_failed[kMaxSplit];  // of each CTA of the split, by its own account
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const uint32_t base = ((uint32_t)__cvta_generic_to_shared(dyn) + 1023u) & ~1023u;
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const int k_begin = KT * ks / S, n_k = KT * (ks + 1) / S - k_begin;
     const uint32_t bytes_x = (uint32_t)p.T * 128;
     const uint32_t stage_bytes = kBytesW + bytes_x + 2 * kBytesSf;
+    const uint32_t tx_extra = p.tx_cta < 0 || p.tx_cta == ks ? p.tx_extra : 0;
 
     // No CTA waits for another between taking tensor memory and giving it
     // back, so CTAs of several grids that share SMs cannot block each other:
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     const int k64 = p.K64 - 4 * k_begin;  // 64-element steps from this CTA's first
     auto copy_w = [&](int k, int s) {
         const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * min(4, k64 - 4 * k);
-        mbar_expect_tx(full(s), kBytesW + bytes_x + 2 * sf_bytes + p.tx_extra);
+        mbar_expect_tx(full(s), kBytesW + bytes_x + 2 * sf_bytes + tx_extra);
         tma_load_2d(at, &map_w, (k_begin + k) * 128, n0, full(s));
         bulk_g2s(at + kBytesW + bytes_x, w_sf + k * 2048, sf_bytes, full(s));
     };
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
                 const int s = j % p.stages;
                 if (mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit)) continue;
                 give_up();
-                if (p.tx_extra) bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, p.tx_extra, full(s));
+                if (tx_extra) bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, tx_extra, full(s));
                 mbar_wait_bounded(full(s), (j / p.stages) & 1, p.wait_limit);
             }
     } else if (warp == 1) {
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
             // (under the test hook a stage may complete late, by the copy that
             // makes up for the announcement)
             if (!warp_wait_bounded(full(s), parity, p.wait_limit) ||
-                (p.tx_extra && __any_sync(0xffffffffu, gave_up()))) {
+                (tx_extra && __any_sync(0xffffffffu, gave_up()))) {
                 give_up();
                 break;
             }
@@ -245,11 +247,13 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         // partial sums of a block into the shared memory of the CTA that adds
         // it, [source][token / 4][weight row][token % 4], then each adds in
         // source order: one way across the cluster and one barrier, and the
-        // order of the sum is fixed.
+        // order of the sum is fixed.  Each CTA tells the others along with the
+        // sums whether it gave up: nobody stores a sum that lacks a part.
         const int blk = join_block(p.T, S);
         const uint32_t part = base + stage_bytes * p.stages + 16u * row;
         const uint32_t src = 16u * kTileN * (blk / 4);  // bytes of one source
         cluster_wait();
+        if (t < S) st_cluster_u32(map_to_cta((uint32_t)__cvta_generic_to_shared(&cta_failed[ks]), t), !good);
         if (good) {
             int dst = -1, left = 0;
             uint32_t to = 0;
@@ -273,7 +277,9 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         free_tmem();
         cluster_arrive_release();
         cluster_wait();
-        if (good && n < p.N)
+        bool whole = true;
+        for (int r = 0; r < S; ++r) whole &= cta_failed[r] == 0;
+        if (whole && n < p.N)
             for (int i = 0; i < blk; i += 4) {
                 const int c = ks * blk + i;
                 if (c >= rows) break;
@@ -363,7 +369,7 @@ SplitShape split_shape(const DevInfo &d, int T, int split, int KT) {
 // (0 on error), asked once per device: SMs of a processing cluster that do
 // not make a whole one stay idle (GB300: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
 int resident_clusters(const DevInfo &d, int split) {
-    static std::atomic<int> cached[kMaxDevices][9];  // clusters + 1
+    static std::atomic<int> cached[kMaxDevices][kMaxSplit + 1];  // clusters + 1
     std::atomic<int> &c = cached[d.dev][split];
     int n = c.load() - 1;
     if (n < 0) {
@@ -402,7 +408,7 @@ void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &
     const int64_t tiles = p.n_tiles * ((M + p.T - 1) / p.T);
     p.split = 1;
     if (tiles <= d.sms)
-        for (int c = std::min(p.T >= 64 ? 6 : 8, KT / 2); c > 1 && p.split == 1; --c) {
+        for (int c = std::min(p.T >= 64 ? 6 : kMaxSplit, KT / 2); c > 1 && p.split == 1; --c) {
             const int64_t per_sm = d.smem_sm / ((int64_t)split_shape(d, p.T, c, KT).smem + 1024 + 512);
             if (resident_clusters(d, c) * per_sm >= tiles) p.split = c;
         }
@@ -473,6 +479,7 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     p.err = d->err;
     p.wait_limit = wait_limit_cycles();
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
+    p.tx_cta = -1;
     p.early_w = constant_weights_on();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -484,6 +491,11 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
         if (e == cudaSuccess) return GNQ_OK;
         cudaGetLastError();
         return GNQ_ERR_CUDA;
+    }
+    if (const int cta = inject_split_timeout(); cta >= 0 && cta < p.split && p.split > 1 && !p.tx_extra) {
+        p.wait_limit = kTestWaitLimit;
+        p.tx_extra = 16u;
+        p.tx_cta = cta;
     }
     CUtensorMap mw, mx;
     if (!encode_codes(&mw, w_q, N, K, kTileN) || !encode_codes(&mx, q, M, K, p.T)) return GNQ_ERR_CUDA;

@@ -11,6 +11,7 @@ namespace gnq {
 constexpr int kTileN = 128;      // weight rows per CTA
 constexpr int kStageK = 256;     // elements of K per stage
 constexpr int kMaxStages = 8;
+constexpr int kMaxSplit = 8;     // CTAs that share a tile's K
 constexpr uint32_t kBytesW = kTileN * kStageK / 2;
 constexpr uint32_t kBytesSf = 4 * 512;
 
@@ -30,6 +31,7 @@ struct LinearParams {
     long long wait_limit;
     bool early_w;       // the weight's first stages are read before the wait on the preceding grid
     uint32_t tx_extra;  // test hook: bytes announced per stage beyond the copies
+    int tx_cta;         // ... by this CTA of a split alone (-1: by all)
 };
 
 template <typename O> struct OutType;

@@ -1,0 +1,53 @@
+"""GPU tests of the operators around the NVFP4 linear where a call goes wrong
+in part, at the ends of a value range, or on a kernel that the size alone would
+not choose."""
+import pytest
+import torch
+
+import oracle
+from operators_ref import assert_within, linear64, linear_tolerance, random_nvfp4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gnq():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a CUDA device")
+    from nvfp4_quant_gemma_gb300 import build
+    build.build()
+    import nvfp4_quant_gemma_gb300 as pkg
+    pkg.load()
+    oracle.build()
+    return pkg
+
+
+def _one(v):
+    return torch.full((1,), v, dtype=torch.float32, device="cuda")
+
+
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cta", [0, 1, 3])
+@pytest.mark.parametrize("M", [5, 100])
+def test_a_split_product_that_loses_one_part_writes_nothing(gnq, M, cta, T):
+    """One CTA of each cluster gives up, its peers do not: the error bit, no
+    output from any of them, and the next call is sound.  (384 x 2048 at these
+    batches is split over four CTAs.)"""
+    q, sf = random_nvfp4(M, 2048, 1)
+    wq, wsf = random_nvfp4(384, 2048, 2)
+    args = [t.cuda() for t in (q, sf, wq, wsf)]
+    y = torch.full((M, 384), 7.0, dtype=T, device="cuda")
+    gnq.read_device_error()
+    gnq.inject_split_timeout(cta)
+    try:
+        gnq.nvfp4_linear(*args, _one(1.0), out=y)
+        torch.cuda.synchronize()
+    finally:
+        gnq.inject_split_timeout(-1)
+    assert gnq.read_device_error(clear=True) & 1
+    assert bool((y == 7.0).all())
+    gnq.nvfp4_linear(*args, _one(1e-3), out=y)
+    torch.cuda.synchronize()
+    assert gnq.read_device_error() == 0
+    y64, mag = linear64(q, sf, wq, wsf, float(torch.tensor(1e-3)))
+    assert_within(y, y64, linear_tolerance(y64, mag, 2048, T), "y")
