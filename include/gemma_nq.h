@@ -56,7 +56,10 @@
  *    H % 64 == 0 (whole 4-column scale tiles, so padded scale columns never
  *    exist) and MXFP8 H % 32 == 0.  H is at most 65536.
  *  - x and residual must not be the same buffer, and y must differ from both
- *    (GNQ_ERR_ALIAS).
+ *    (GNQ_ERR_ALIAS).  gemma_sandwich_norm_quant, gnq_quantize,
+ *    gated_act_quant, gnq_nvfp4_dequantize and nvfp4_linear check whole
+ *    ranges: what such a call writes may share no byte with what it reads
+ *    (but residual_out may be `residual` itself) nor with another output.
  *  - Every buffer must hold at least the elements its shape below states;
  *    the library receives raw pointers and cannot check sizes (the Python
  *    binding does, before any launch).
@@ -183,7 +186,7 @@ int add_rms_norm_quant(const void *x_parts, int k, int64_t part_stride,
  *   x            (M, H) the block's output, read only.
  *   residual     (M, H), required.
  *   residual_out (M, H) receives h; NULL or `residual` itself: updated in
- *                place.  Must not overlap x, the gate or (in part) residual.
+ *                place.
  *   w_post, w    (H,) Gemma weights; w_post may be NULL.
  *   gate         NULL, (H,) with gate_stride 0 (one gate per channel), or
  *                (M, H) with rows gate_stride elements apart (>= H, a multiple

@@ -525,7 +525,7 @@ const char *gnq_status_string(int status) {
         case GNQ_ERR_SHAPE: return "unsupported shape (M < 0, or H out of range / not a supported multiple)";
         case GNQ_ERR_DTYPE: return "dtype must be GNQ_BF16 or GNQ_FP16";
         case GNQ_ERR_MODE: return "unknown quantization mode or partial count";
-        case GNQ_ERR_ALIAS: return "x, residual and y must be distinct buffers";
+        case GNQ_ERR_ALIAS: return "x, residual and what a call writes must be distinct buffers";
         case GNQ_ERR_ALIGN: return "misaligned pointer or partial stride";
         case GNQ_ERR_CUDA: return "CUDA launch error";
         case GNQ_ERR_MEMORY: return "a buffer must be in device memory";

@@ -232,10 +232,14 @@ int run_quant(const void *x, int64_t row_stride, int act, const float *scale, in
     if (!x || (write_y && !y) || (mode != MODE_NONE && !q)) return GNQ_ERR_NULL;
     if ((mode == MODE_FP8 || mode == MODE_NVFP4) && !scale) return GNQ_ERR_NULL;
     if ((mode == MODE_NVFP4 || mode == MODE_MXFP8) && !block_scale) return GNQ_ERR_NULL;
-    if (write_y && y == x) return GNQ_ERR_ALIAS;
     if (!aligned(x, 16) || (write_y && !aligned(y, 16)) || (mode != MODE_NONE && !aligned(q, 16)) ||
         (scale && !aligned(scale, 4)) || (block_scale && mode >= MODE_NVFP4 && !aligned(block_scale, 4)))
         return GNQ_ERR_ALIGN;
+    const Extent written[] = {extent(q, code_bytes(mode, M, H)), extent(block_scale, scale_bytes(mode, M, H)),
+                              extent(y, write_y ? 2 * M * H : 0)};
+    const Extent read[] = {{x, M, 2 * row_stride, 2 * width},
+                           extent(scale, mode == MODE_FP8 || mode == MODE_NVFP4 ? 4 : 0)};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
     const DevInfo *d = dev_info();
     if (!d) return GNQ_ERR_CUDA;
     QuantParams qp = {};
@@ -404,10 +408,14 @@ int gnq_nvfp4_dequantize(const void *q, const void *block_scale, const float *sc
     if (M < 0 || M > gnq::kMaxM || K <= 0 || K > gnq::kMaxH || K % 64 != 0) return GNQ_ERR_SHAPE;
     if (M == 0) return GNQ_OK;
     if (!q || !block_scale || !out) return GNQ_ERR_NULL;
-    if (out == q || out == block_scale) return GNQ_ERR_ALIAS;
     if (!gnq::aligned(q, 16) || !gnq::aligned(out, 16) || !gnq::aligned(block_scale, 4) ||
         (scale && !gnq::aligned(scale, 4)))
         return GNQ_ERR_ALIGN;
+    const int size = out_type == GNQ_E4M3 ? 1 : out_type == GNQ_FP32 ? 4 : 2;
+    const gnq::Extent written[] = {gnq::extent(out, M * K * size)};
+    const gnq::Extent read[] = {gnq::extent(q, gnq::code_bytes(GNQ_NVFP4, M, K)),
+                                gnq::extent(block_scale, gnq::scale_bytes(GNQ_NVFP4, M, K)), gnq::extent(scale, 4)};
+    if (gnq::outputs_meet(written, read)) return GNQ_ERR_ALIAS;
     const gnq::DevInfo *d = gnq::dev_info();
     if (!d) return GNQ_ERR_CUDA;
     gnq::DequantParams p;

@@ -43,6 +43,45 @@ bool on_device(const void *ptr, int dev);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A stretch of memory of a call: `rows` rows of `width` bytes, `stride` bytes
+// apart; empty for a buffer that the call does not use.
+struct Extent {
+    const void *at;
+    int64_t rows, stride, width;
+};
+inline Extent extent(const void *p, int64_t bytes) { return {p, p ? 1 : 0, 0, bytes}; }
+
+// Whether the contiguous stretch `a` shares a byte with `b`.
+inline bool meets(const Extent &a, const Extent &b) {
+    if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), a1 = a0 + (uintptr_t)a.width;
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.at);
+    if (a1 <= b0) return false;
+    if (a0 <= b0 || b.rows == 1) return a0 < b0 + (uintptr_t)b.width;
+    // the last row that starts at or before `a`, then the next
+    const uintptr_t r = (a0 - b0) / (uintptr_t)b.stride, row = b0 + r * (uintptr_t)b.stride;
+    if (r >= (uintptr_t)b.rows) return false;
+    return a0 < row + (uintptr_t)b.width || (r + 1 < (uintptr_t)b.rows && a1 > row + (uintptr_t)b.stride);
+}
+
+// What a call writes may be neither read by it nor written twice: CTAs run
+// in any order.
+template <int W, int R> bool outputs_meet(const Extent (&written)[W], const Extent (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (meets(written[i], written[j])) return true;
+        for (const Extent &r : read)
+            if (meets(written[i], r)) return true;
+    }
+    return false;
+}
+
+// Bytes of the codes and block scales that a mode writes (0: none).
+inline int64_t code_bytes(int mode, int64_t M, int64_t H) { return mode < 0 ? 0 : mode == 1 ? M * H / 2 : M * H; }
+inline int64_t scale_bytes(int mode, int64_t M, int64_t H) {
+    return mode == 1 ? (M + 127) / 128 * 8 * H : mode == 2 ? M * (H / 32) : 0;
+}
+
 // Launch `fn` with these dimensions, `cluster` CTAs per cluster along x, as a
 // programmatic dependent where the switch is on.
 template <typename... P, typename... A>

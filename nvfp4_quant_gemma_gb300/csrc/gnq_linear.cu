@@ -459,10 +459,14 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     if (M < 0 || M > kMaxM || N <= 0 || N > kMaxM || K <= 0 || K > kMaxH || K % 64 != 0) return GNQ_ERR_SHAPE;
     if (M == 0) return GNQ_OK;
     if (!q || !block_scale || !w_q || !w_block_scale || !alpha || !y) return GNQ_ERR_NULL;
-    if (y == q || y == block_scale || y == w_q || y == w_block_scale || (bias && y == bias)) return GNQ_ERR_ALIAS;
     if (!aligned(q, 16) || !aligned(block_scale, 16) || !aligned(w_q, 16) || !aligned(w_block_scale, 16) ||
         !aligned(y, 16) || !aligned(alpha, 4) || (bias && !aligned(bias, 2)))
         return GNQ_ERR_ALIGN;
+    const Extent written[] = {extent(y, M * N * (out_type == GNQ_FP32 ? 4 : 2))};
+    const Extent read[] = {extent(q, code_bytes(GNQ_NVFP4, M, K)),   extent(block_scale, scale_bytes(GNQ_NVFP4, M, K)),
+                           extent(w_q, code_bytes(GNQ_NVFP4, N, K)), extent(w_block_scale, scale_bytes(GNQ_NVFP4, N, K)),
+                           extent(alpha, 4),                         extent(bias, 2 * N)};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
     const DevInfo *d = dev_info();
     if (!d) return GNQ_ERR_CUDA;
     for (const void *buf : {q, block_scale, w_q, w_block_scale, static_cast<const void *>(y)})

@@ -324,14 +324,22 @@ extern "C" int gemma_sandwich_norm_quant(const void *x, void *residual, void *re
     if (!x || !residual || !w || (write_y && !y) || (mode != MODE_NONE && !q)) return GNQ_ERR_NULL;
     if ((mode == MODE_FP8 || mode == MODE_NVFP4) && !scale) return GNQ_ERR_NULL;
     if ((mode == MODE_NVFP4 || mode == MODE_MXFP8) && !block_scale) return GNQ_ERR_NULL;
-    if (x == residual || x == residual_out || (gate && gate == residual_out) ||
-        (write_y && (y == x || y == residual || y == residual_out || (gate && y == gate))))
-        return GNQ_ERR_ALIAS;
+    if (x == residual) return GNQ_ERR_ALIAS;
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(w, 16) ||
         (w_post && !aligned(w_post, 16)) || (gate && !aligned(gate, 16)) || (write_y && !aligned(y, 16)) ||
         (mode != MODE_NONE && !aligned(q, 16)) || (scale && !aligned(scale, 4)) ||
         (block_scale && mode >= MODE_NVFP4 && !aligned(block_scale, 4)))
         return GNQ_ERR_ALIGN;
+    const int64_t n = 2 * M * H;
+    const Extent written[] = {extent(residual_out, n), extent(q, code_bytes(mode, M, H)),
+                              extent(block_scale, scale_bytes(mode, M, H)), extent(y, write_y ? n : 0)};
+    const Extent read[] = {extent(x, n), extent(w_post, 2 * H), extent(w, 2 * H),
+                           gate_stride ? Extent{gate, gate ? M : 0, 2 * gate_stride, 2 * H} : extent(gate, 2 * H),
+                           extent(scale, mode == MODE_FP8 || mode == MODE_NVFP4 ? 4 : 0)};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
+    if (residual_out != residual)  // in place is the same element read and written by one thread
+        for (const Extent &o : written)
+            if (meets(o, extent(residual, n))) return GNQ_ERR_ALIAS;
     const DevInfo *d = dev_info();
     if (!d) return GNQ_ERR_CUDA;
     SandwichParams sp = {};

@@ -51,3 +51,21 @@ def test_a_split_product_that_loses_one_part_writes_nothing(gnq, M, cta, T):
     assert gnq.read_device_error() == 0
     y64, mag = linear64(q, sf, wq, wsf, float(torch.tensor(1e-3)))
     assert_within(y, y64, linear_tolerance(y64, mag, 2048, T), "y")
+
+
+def test_outputs_between_the_rows_of_a_strided_input(gnq):
+    """What a call writes may lie in the gaps of what it reads: codes, scales
+    and y in the columns behind a wide stride."""
+    M, H, T = 4, 64, torch.bfloat16
+    x = torch.randn(M, 2 * H, generator=torch.Generator().manual_seed(1)).to(T).cuda()
+    s = _one(0.05)
+    want, _, wy = gnq.gated_act_quant(x, s, "fp8", act="silu", write_y=True)
+    arena = torch.zeros(M, 1024, dtype=T, device="cuda")
+    arena[:, :2 * H] = x
+    q = arena[0, 2 * H:2 * H + M * H // 2].view(torch.uint8).view(M, H)           # right behind row 0
+    y = arena[1, 1024 - M * H:].view(M, H)                                        # up to row 2
+    gnq.gated_act_quant(arena[:, :2 * H], s, "fp8", act="silu", write_y=True, out=(q, None, y))
+    torch.cuda.synchronize()
+    assert torch.equal(q, want.view(torch.uint8)) and torch.equal(y, wy) and torch.equal(arena[:, :2 * H], x)
+    with pytest.raises(RuntimeError, match="distinct"):
+        gnq.gated_act_quant(arena[:, :2 * H], s, "fp8", act="silu", out=(arena[2].view(torch.uint8)[:M * H].view(M, H), None, None))
