@@ -218,6 +218,9 @@ int gnq_quantize(const void *x, int64_t row_stride, const float *scale,
 /*
  * The gated activation between the products of an MLP, and the quantization
  * for the second: y = dtype(act(gate) * up) in fp32, rounded once; q = quant(y).
+ * (Before that rounding act(gate) * up is good to 5e-6 of its value while
+ * act(gate) is above 1e-4 of the gate, to 7e-5 below; an act(gate) below 2^-218
+ * gives 0.)
  *   x          (M, 2H): gate in the first H columns, up in the last; rows
  *              row_stride elements apart (>= 2H, a multiple of 8).
  *   act        GNQ_SILU: g / (1 + exp(-g)); GNQ_GELU_TANH: g/2 (1 + tanh(

@@ -34,12 +34,22 @@ struct QuantParams {
 };
 
 // act(g) * u of two elements in fp32.  silu(g) = g / (1 + e^-g); gelu_tanh(g)
-// = g / 2 * (1 + tanh t) = g / (1 + e^-2t), t = sqrt(2/pi) (g + 0.044715 g^3).
-// The powers of two and reciprocals are the fast ones, good to about 1e-6 of
-// the result, far inside the one rounding to 16 bits that follows; both forms
-// go to -0 and to g as g goes to -inf and +inf.  The rest is paired fp32
-// arithmetic: with one operation per instruction a 16384 x 7168 batch into
-// FP8 was bound by instruction issue.
+// = g / 2 * (1 + tanh z) = g / (1 + e^-2z), z = sqrt(2/pi) (g + 0.044715 g^3):
+// both g / (1 + 2^t).  The power of two and the reciprocal are the fast ones:
+// relative errors of 2^-22 and 2^-23, and the roundings of t count |t| ln 2
+// times 1.25 (SiLU) or at most 6 (tanh-GELU) units of 2^-24: 5e-7 for g near 0,
+// 1.2e-6 and 4e-6 where act(g) is 1e-4 of g, 6e-5 at the end of the range.  The
+// one rounding to 16 bits that follows is 2^-8 (bf16) or 2^-11 (fp16).  The rest
+// is paired fp32 arithmetic: with one operation per instruction a 16384 x 7168
+// batch into FP8 was bound by instruction issue.
+// FAR: beyond t = 100 everything is taken 2^100 times smaller until the last
+// product, so that 1 + 2^t does not pass 2^126, whose reciprocal is subnormal
+// and would be 0 (silu(-88) is -5.3e-37, a normal bf16 value).  Exact scaling:
+// for t <= 100 the bits are those of the plain path.  Past t = 226, where act(g)
+// is below 2^-218, the result is 0; both forms go to -0 and to g as g goes to
+// -inf and +inf.  A warp takes this form for eight gates a lane where one of
+// them is that far out (tanh-GELU of 16384 x 7168 into FP8: 96.8 us without such
+// a gate, 108.1 where every warp has one; taken always 106.6).
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -50,7 +60,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-template <int ACT> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint64_t u) {
+template <int ACT, bool FAR> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint64_t u) {
     constexpr float kLog2e = 1.4426950408889634f;
     uint64_t t;  // the exponent of two
     if (ACT == ACT_SILU) {
@@ -61,8 +71,26 @@ template <int ACT> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint
     }
     float t0, t1, d0, d1;
     upk2(t, t0, t1);
-    upk2(add2(pk2(exp2_fast(t0), exp2_fast(t1)), pk2(1.f, 1.f)), d0, d1);
-    return mul2(mul2(g, pk2(rcp_fast(d0), rcp_fast(d1))), u);
+    uint64_t one = pk2(1.f, 1.f);
+    if constexpr (FAR) {
+        const bool f0 = t0 > 100.f, f1 = t1 > 100.f;
+        one = pk2(f0 ? 0x1p-100f : 1.f, f1 ? 0x1p-100f : 1.f);
+        t0 = f0 ? t0 - 100.f : t0;
+        t1 = f1 ? t1 - 100.f : t1;
+    }
+    upk2(add2(pk2(exp2_fast(t0), exp2_fast(t1)), one), d0, d1);
+    const uint64_t y = mul2(mul2(g, pk2(rcp_fast(d0), rcp_fast(d1))), u);
+    return FAR ? mul2(y, one) : y;
+}
+
+// Whether any of 8 packed gates may have t > 100.
+template <typename T, int ACT> __device__ __forceinline__ bool gates_far(const uint4 &g) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 *v = reinterpret_cast<const T2 *>(&g);
+    const T2 m = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+    float lo, hi;
+    Act<T>::unpack2(*reinterpret_cast<const uint32_t *>(&m), lo, hi);
+    return fminf(lo, hi) < (ACT == ACT_SILU ? -69.f : -9.f);  // t = 99.5, 95.8
 }
 
 template <typename T, bool V8, int U>
@@ -141,16 +169,21 @@ __global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) q
         for (int v = 0; v < VPT; ++v) {
             float y[E];
 #pragma unroll
-            for (int c = 0; c < U; ++c) {
-                Act<T>::unpack(g[v][c], &y[8 * c]);
-                if constexpr (ACT != ACT_NONE) {
-                    float f[8];
-                    Act<T>::unpack(u[v][c], f);
+            for (int c = 0; c < U; ++c) Act<T>::unpack(g[v][c], &y[8 * c]);
+            if constexpr (ACT != ACT_NONE) {
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        float *o = &y[8 * c + i];
-                        upk2(act_mul2<ACT>(pk2(o[0], o[1]), pk2(f[i], f[i + 1])), o[0], o[1]);
-                    }
+                for (int c = 0; c < U; ++c) {
+                    auto activate = [&](auto far) {
+                        float f[8];
+                        Act<T>::unpack(u[v][c], f);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            float *o = &y[8 * c + i];
+                            upk2(act_mul2<ACT, decltype(far)::value>(pk2(o[0], o[1]), pk2(f[i], f[i + 1])), o[0], o[1]);
+                        }
+                    };
+                    if (__any_sync(0xffffffffu, gates_far<T, ACT>(g[v][c]))) activate(std::true_type{});
+                    else activate(std::false_type{});
                 }
             }
             const RowOut o = row_out<MODE>(p, m[v]);

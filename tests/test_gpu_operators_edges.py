@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import oracle
-from operators_ref import assert_within, linear64, linear_tolerance, random_nvfp4
+from gnq_testutil import DTYPES
+from operators_ref import act64, assert_within, linear64, linear_tolerance, random_nvfp4, rounding
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +70,50 @@ def test_outputs_between_the_rows_of_a_strided_input(gnq):
     assert torch.equal(q, want.view(torch.uint8)) and torch.equal(y, wy) and torch.equal(arena[:, :2 * H], x)
     with pytest.raises(RuntimeError, match="distinct"):
         gnq.gated_act_quant(arena[:, :2 * H], s, "fp8", act="silu", out=(arena[2].view(torch.uint8)[:M * H].view(M, H), None, None))
+
+
+def _far_gates(T):
+    """Gates over the whole range where the activation is not just 0 or the gate."""
+    g = torch.cat([torch.linspace(-200, 100, 4096), torch.linspace(-92, -86, 1024), torch.linspace(-13, -8.5, 1024),
+                   torch.linspace(-4, 4, 2048)]).to(T)
+    return g
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gated_activation_over_the_range_of_the_gate(gnq, dtype, act):
+    """The errors that the kernel may have, added up: 2^-22 (power of two) and
+    2^-23 (reciprocal), 4 roundings of 2^-24, and those of the exponent t =
+    log2(e) g or its cubic form, which the power of two multiplies by |t| ln 2:
+    the constant and the product for SiLU (1.25 units of 2^-24: float(log2 e) is
+    1.3e-8 off), two constants of up to three roundings and three operations
+    for tanh-GELU (6 units).  An act(gate) below 2^-218 may be 0."""
+    T = DTYPES[dtype]
+    g = _far_gates(T)
+    up = [1.0, -0.0078, 61440.0] + ([2.0 ** 100, -1e-30] if dtype == "bf16" else [])
+    M, H = len(up), g.numel()
+    x = torch.empty(M, 2 * H, dtype=T)
+    x[:, :H] = g
+    x[:, H:] = torch.tensor(up).to(T)[:, None]
+    y = gnq.gated_act_quant(x.cuda(), None, "none", act=act)[2]
+    g64, u64 = x[:, :H].double(), x[:, H:].double()
+    t = g64.abs() * 1.4427 if act == "silu" else 2.3022 * (g64 + 0.044715 * g64 ** 3).abs()
+    y64 = act64(x, act)
+    err = (2.0 ** -22 + 2.0 ** -23 + (4 + (1.25 if act == "silu" else 6) * 0.6932 * t) * 2.0 ** -24) * y64.abs()
+    err = err + 2.0 ** -218 * u64.abs()
+    fits = y64.abs() < torch.finfo(T).max
+    assert_within(y.cpu()[fits], y64[fits], (err + rounding(y64.abs() + err, T))[fits], "y")
+    assert bool(torch.isinf(y.cpu()[y64.abs() > 1.01 * torch.finfo(T).max]).all())
+
+
+def test_gated_activation_does_not_depend_on_its_neighbours(gnq):
+    """A gate far below 0 in a group does not move the others' bits."""
+    T = torch.bfloat16
+    x = (torch.randn(64, 1024, generator=torch.Generator().manual_seed(3)) * 3).to(T)
+    far = x.clone()
+    far[:, 5:512:16] = -88.0
+    for act in ("silu", "gelu_tanh"):
+        a, b = (gnq.gated_act_quant(v.cuda(), None, "none", act=act)[2].cpu() for v in (x, far))
+        keep = torch.ones(512, dtype=torch.bool)
+        keep[5::16] = False
+        assert torch.equal(a[:, keep], b[:, keep])
