@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gnq {
 
 constexpr int64_t kMaxH = 65536;
@@ -42,6 +44,14 @@ bool in_device_memory(const void *ptr);
 bool on_device(const void *ptr, int dev);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// An answer (0 or more) that `ask` gives once and `slot`, 0 at first, keeps; -1
+// where `ask` fails with -1, which is not kept: the next call asks again.
+template <typename Ask> int answer_once(std::atomic<int> &slot, Ask ask) {
+    int n = slot.load() - 1;
+    if (n < 0 && (n = ask()) >= 0) slot.store(n + 1);
+    return n;
+}
 
 // A stretch of memory of a call: `rows` rows of `width` bytes, `stride` bytes
 // apart; empty for a buffer that the call does not use.

@@ -366,15 +366,14 @@ SplitShape split_shape(const DevInfo &d, int T, int split, int KT) {
 }
 
 // Clusters of `split` CTAs that the device runs at a time with one CTA per SM
-// (0 on error), asked once per device: SMs of a processing cluster that do
-// not make a whole one stay idle (GB300: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
+// (0 on error, for this call), asked once per device: SMs of a processing
+// cluster that do not make a whole one stay idle (GB300: 76, 46, 36, 28, 23, 15,
+// 15 for 2 to 8).
 int resident_clusters(const DevInfo &d, int split) {
     static std::atomic<int> cached[kMaxDevices][kMaxSplit + 1];  // clusters + 1
-    std::atomic<int> &c = cached[d.dev][split];
-    int n = c.load() - 1;
-    if (n < 0) {
+    const int n = answer_once(cached[d.dev][split], [&] {
         auto fn = linear_kernel<__nv_bfloat16, __nv_bfloat16>;
-        if (opt_in_dynamic_smem(reinterpret_cast<const void *>(fn)) != cudaSuccess) return 0;
+        if (opt_in_dynamic_smem(reinterpret_cast<const void *>(fn)) != cudaSuccess) return -1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(split * d.sms), 1, 1);
         cfg.blockDim = dim3(128, 1, 1);
@@ -385,13 +384,12 @@ int resident_clusters(const DevInfo &d, int split) {
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.numAttrs = 1;
         cfg.attrs = &attr;
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-        c.store(n + 1);
-    }
-    return n;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess) return clusters;
+        cudaGetLastError();
+        return -1;
+    });
+    return std::max(n, 0);
 }
 
 // Tile and split of a call: the smallest tile that holds the tokens (128 at

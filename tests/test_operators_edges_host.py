@@ -1,9 +1,12 @@
 """CPU checks of the operators around the NVFP4 linear: what their entry points
 refuse beyond single arguments, and host code that a GPU test cannot make fail."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P, i64, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
 
 
@@ -82,3 +85,18 @@ def test_dequantize_refuses_an_output_over_what_it_reads(lib, out):
 @pytest.mark.parametrize("y", [A, A + 112, B + 496, C + 2032, D - 496, E, E + 0x1000 - 496])
 def test_linear_refuses_an_output_over_what_it_reads(lib, y):
     assert lib.nvfp4_linear(P(A), P(B), P(C), P(D), P(E), P(E + 0x1000), P(y), i64(4), i64(64), i64(64), 0, 0, None) == 5
+
+
+def test_a_failed_question_to_the_runtime_is_asked_again(tmp_path):
+    """Resident clusters (and with them the split of a product) are asked for
+    once per device; one failed answer must not stay for the process."""
+    exe = tmp_path / "host_helpers"
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-x", "c++", os.path.join(ROOT, "tests", "c", "host_helpers.cpp"), "-I",
+                    os.path.join(ROOT, "nvfp4_quant_gemma_gb300", "csrc"), "-I", os.path.join(cuda, "include"), "-o",
+                    str(exe)], check=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert res.returncode == 0 and "host helpers ok" in res.stdout, res.stderr
+    linear = open(os.path.join(ROOT, "nvfp4_quant_gemma_gb300", "csrc", "gnq_linear.cu")).read()
+    body = linear[linear.index("int resident_clusters("):]
+    assert "answer_once(" in body[:body.index("\n}")]
