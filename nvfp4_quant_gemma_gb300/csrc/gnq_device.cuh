@@ -561,18 +561,38 @@ __device__ __forceinline__ uint32_t cluster_id_x() {
 __device__ __forceinline__ void cluster_arrive_release() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+// Orders nothing: only for an arrival that no access of this CTA has to precede.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer_f32(const float *local, uint32_t rank) {
-    uint32_t a = (uint32_t)__cvta_generic_to_shared(local), ra;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
-    return v;
+// Address of the same shared memory in another CTA of the cluster.
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The sum of `tot` over the C CTAs of a cluster, in rank order.  Each CTA stores
+// its part into every CTA's `slots`, its own included, and reads only its own:
+// no read of a peer can be under way when that peer leaves, so the barrier below
+// is the last that a CTA waits on.  Before it, every CTA of the cluster has
+// arrived once (cluster_arrive_relaxed at its start): they all exist.
+__device__ __forceinline__ float cluster_total(float *slots, float tot, uint32_t rank, uint32_t C, int t) {
+    if (t < (int)C) st_cluster_u32(map_to_cta((uint32_t)__cvta_generic_to_shared(slots + rank), t), __float_as_uint(tot));
+    cluster_arrive_release();
+    cluster_wait();
+    tot = 0.f;
+    for (uint32_t r = 0; r < C; ++r) tot += slots[r];
+    return tot;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -270,7 +270,7 @@ template <int MODE, int VPT, bool PARTS, bool LEAN> struct RowForm {
 // (segment = VPT units x threads), so no unit needs a check.  OPT: OPT_A32
 // and OPT_EARLYW (see gnq_device.cuh).
 template <typename T, int MODE, bool PARTS, int VPT, bool LEAN, bool FULL, int OPT>
-__device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float &cta_ss,
+__device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float *cta_ss,
                                          float *es_smem) {
     constexpr int U = Unit<MODE>::U, E = Unit<MODE>::E;
     constexpr bool V8 = (OPT & OPT_A32) && U == 2;
@@ -289,6 +289,7 @@ __device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float 
     const int t = threadIdx.x;
     const int nunits = p.seg / E;
     const int64_t row = m * (int64_t)p.H;
+    if (C > 1) cluster_arrive_relaxed();
 
     constexpr bool PRED = Pred<MODE>::value;
     int col[VPT], lc[VPT];  // lc: the column a unit loads (PRED: clamped in range)
@@ -482,12 +483,8 @@ __device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float 
     __syncthreads();
     float tot = block_total(warp_ss, NT >> 5, t & 31);
     if (C > 1) {
-        if (t == 0) cta_ss = tot;
-        cluster_arrive_release();
-        cluster_wait();
-        tot = 0.f;
-        for (uint32_t r = 0; r < C; ++r) tot += ld_peer_f32(&cta_ss, r);
-        cluster_arrive_relaxed();  // this CTA's reads of its peers are done
+        cluster_wait();  // the peers have started
+        tot = cluster_total(cta_ss, tot, rank, C, t);
         store_residual();
     }
     const float inv = inv_rms(p, tot);
@@ -540,13 +537,11 @@ __device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float 
     };
     if (MODE == MODE_FP8 && !qc.fd.fast) finish(std::integral_constant<int, FP8_IEEE>{});
     else finish(std::integral_constant<int, FP8_PAIR>{});
-
-    if (C > 1) cluster_wait();  // peers may still be reading this CTA's partial
 }
 
 #define GNQ_ROW_SMEM                                  \
     __shared__ __align__(16) float warp_ss[32];       \
-    __shared__ float cta_ss;                          \
+    __shared__ float cta_ss[8];                       \
     __shared__ float es_smem[MODE == MODE_NVFP4 ? 256 : 1];
 
 // FP8, MXFP8 and no-quant rows: the compiler's own register choice.

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     constexpr int U = Unit<MODE>::U, E = Unit<MODE>::E;
     constexpr bool ESDIV = MODE == MODE_NVFP4;
     __shared__ __align__(16) float warp_ss[2][32];
-    __shared__ float cta_ss[2];
+    __shared__ float cta_ss[2][8];
     const Params &p = sp.p;
     const uint32_t C = cluster_size();
     const uint32_t rank = C > 1 ? cluster_rank() : 0;
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
         col[v] = (int)rank * p.seg + u * E;
         lc[v] = ok[v] ? col[v] : (int)rank * p.seg;
     }
+    if (C > 1) cluster_arrive_relaxed();
     // The first wave's rows into L2 while the preceding grid drains: a hint
     // (the values are read after the wait), as in the single norm.
     if ((int)blockIdx.x < p.pf_ctas) {
@@ -152,11 +153,8 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
         __syncthreads();
         float tot = block_total(warp_ss[k], nw, t & 31);
         if (C > 1) {
-            if (t == 0) cta_ss[k] = tot;
-            cluster_arrive_release();
-            cluster_wait();
-            tot = 0.f;
-            for (uint32_t r = 0; r < C; ++r) tot += ld_peer_f32(&cta_ss[k], r);
+            if (k == 0 || !sp.w_post) cluster_wait();  // the peers have started
+            tot = cluster_total(cta_ss[k], tot, rank, C, t);
         }
         return rsqrt_refined(fmaf(tot, p.inv_h, p.eps));
     };
@@ -214,7 +212,6 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
         }
     }
     const float inv = row_inv(ss, 1);
-    if (C > 1) cluster_arrive_relaxed();  // this CTA's reads of its peers are done
 
     // ---- the norm before the next block, then the quantization ----
     const RowOut o = row_out<MODE>(p, m);
@@ -237,7 +234,6 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
     };
     if (MODE == MODE_FP8 && !qc.fd.fast) finish(std::integral_constant<int, FP8_IEEE>{});
     else finish(std::integral_constant<int, FP8_PAIR>{});
-    if (C > 1) cluster_wait();  // peers may still be reading this CTA's partials
 }
 
 template <typename T, int MODE, int VPT, bool GATED, bool V8>

@@ -18,19 +18,6 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Address of the same shared memory in another CTA of the cluster.
-__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
 // Bounded wait of a whole converged warp, with one answer for all its lanes:
 // a lane that gave up takes the others along, so the warp stays converged.
 __device__ __forceinline__ bool warp_wait_bounded(uint32_t bar, uint32_t parity, long long limit) {

@@ -2,6 +2,7 @@
 refuse beyond single arguments, and host code that a GPU test cannot make fail."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -100,3 +101,20 @@ def test_a_failed_question_to_the_runtime_is_asked_again(tmp_path):
     linear = open(os.path.join(ROOT, "nvfp4_quant_gemma_gb300", "csrc", "gnq_linear.cu")).read()
     body = linear[linear.index("int resident_clusters("):]
     assert "answer_once(" in body[:body.index("\n}")]
+
+
+def test_no_cta_reads_the_shared_memory_of_a_peer():
+    """A read of another CTA's shared memory has to be over before that CTA
+    leaves, and a relaxed arrival on the cluster barrier does not say so: CTAs
+    store into their peers instead, and the next arrival releases it.  Read off
+    the sources, as a GPU could only show a slip by faulting."""
+    csrc = os.path.join(ROOT, "nvfp4_quant_gemma_gb300", "csrc")
+    stores = 0
+    for name in sorted(os.listdir(csrc)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        assert "ld.shared::cluster" not in text, name
+        for store in re.finditer(r"(?<!void )\bst_cluster_\w+\(", text):
+            arrival = re.search(r"\bcluster_arrive_(\w+)\(", text[store.end():])
+            assert arrival and arrival.group(1) == "release", name
+            stores += 1
+    assert stores >= 3  # a row's sums, and the parts and the status of a split product
