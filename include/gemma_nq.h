@@ -314,6 +314,26 @@ int gnq_query_launch(int64_t M, int64_t H, int k, int has_residual, int write_y,
                      int *form);
 
 /*
+ * Tuning hook: force the kernel of later nvfp4_linear calls in this process.
+ * kernel 0 = automatic; 1 = tiles of one CTA, K split over a cluster where
+ * that fills the device; 2 = CTA pairs on 256 x 256 tiles.  (More tiles than a
+ * grid holds go to pairs all the same.)  A split adds its parts last, so y may
+ * move by a rounding step of the fp32 sum.  Not synchronised with calls in
+ * flight on other host threads.  Returns GNQ_ERR_SHAPE for other values.
+ */
+int gnq_set_linear_policy(int kernel);
+
+/*
+ * The kernel that nvfp4_linear picks by itself for a shape on the current
+ * device, in the terms of gnq_set_linear_policy (a forced one is not applied):
+ * *kernel 1 or 2, *tokens the tokens of a tile, *split the CTAs that share a
+ * tile's K.  M >= 1.  Returns GNQ_OK; GNQ_ERR_NULL, GNQ_ERR_DTYPE or
+ * GNQ_ERR_SHAPE for arguments that a call would reject; GNQ_ERR_CUDA without a
+ * usable device.
+ */
+int gnq_query_linear(int64_t M, int64_t N, int64_t K, int out_type, int *kernel, int *tokens, int *split);
+
+/*
  * Programmatic dependent launch (on by default): each launch may start while
  * the preceding kernel on the stream drains, and waits inside the kernel
  * (griddepcontrol.wait) until that kernel's results are visible before its

@@ -25,7 +25,9 @@ from ._binding import (  # noqa: F401
     load,
     pdl_consumer,
     query_launch,
+    query_linear,
     set_launch_policy,
+    set_linear_policy,
     set_constant_weights,
     set_pdl,
     status_string,

@@ -54,6 +54,8 @@ def load() -> ctypes.CDLL:
             "gnq_nvfp4_dequantize": [P, P, P, P, i64, i64, I, P],
             "nvfp4_linear": [P, P, P, P, P, P, P, i64, i64, i64, I, I, P],
             "gnq_set_launch_policy": [I, I, I, I],
+            "gnq_set_linear_policy": [I],
+            "gnq_query_linear": [i64, i64, i64, I, P, P, P],
             "gnq_query_launch": [i64, i64, I, I, I, I, I, F, P, P, P, P],
             "gnq_read_device_error": [P, I],
             "gnq_set_pdl": [I],
@@ -80,7 +82,7 @@ EXPORTS = ("gemma_add_rms_norm", "gemma_add_rms_norm_quant", "gemma_add_rms_norm
            "gnq_read_device_error", "gnq_set_pdl", "gnq_encode_e4m3_e2m1",
            "gnq_quantize_fp8_values", "gnq_query_launch", "gnq_set_constant_weights",
            "gnq_inject_wait_timeout", "gnq_inject_split_timeout", "gnq_pdl_consumer", "gemma_sandwich_norm_quant",
-           "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear")
+           "gnq_set_linear_policy", "gnq_query_linear", "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear")
 
 
 def status_string(status: int) -> str:
@@ -592,6 +594,21 @@ def query_launch(M: int, H: int, mode, dtype: str = "bf16", k: int = 1, residual
     _check(load().gnq_query_launch(int(M), int(H), int(k), int(bool(residual)), int(bool(write_y)),
                                    _mode(mode), dt, float(weight_bias),
                                    *[ctypes.byref(o) for o in out]), "gnq_query_launch")
+    return tuple(o.value for o in out)
+
+
+def set_linear_policy(kernel: int = 0) -> None:
+    """Force the kernel of later nvfp4_linear calls (0 = automatic): 1 = tiles
+    of one CTA with a split K, 2 = CTA pairs on 256 x 256 tiles."""
+    _check(load().gnq_set_linear_policy(int(kernel)), "gnq_set_linear_policy")
+
+
+def query_linear(M: int, N: int, K: int, dtype=torch.bfloat16) -> tuple[int, int, int]:
+    """(kernel, tokens of a tile, CTAs that share a tile's K) that nvfp4_linear
+    picks by itself, in set_linear_policy's terms."""
+    out = [ctypes.c_int(0) for _ in range(3)]
+    _check(load().gnq_query_linear(int(M), int(N), int(K), _OUT_TYPE[dtype], *[ctypes.byref(o) for o in out]),
+           "gnq_query_linear")
     return tuple(o.value for o in out)
 
 

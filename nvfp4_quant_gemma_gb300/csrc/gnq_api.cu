@@ -38,6 +38,7 @@ std::atomic<int> g_force_kernel{0};  // 0 auto, 1 row kernel, 2 streaming kernel
 std::atomic<int> g_force_cluster{0};
 std::atomic<int> g_force_vpt{0};
 std::atomic<int> g_force_form{0};  // 0 auto, 1 fp32 form, 2 packed (lean) form
+std::atomic<int> g_force_linear{0};  // 0 auto, 1 tiles of one CTA, 2 CTA pairs
 std::atomic<int> g_pdl{1};  // 1: launch as programmatic dependents, 0: plain launches
 std::atomic<int> g_const_w{0};  // 1: small batches read w and scale before the PDL wait
 std::atomic<int> g_inject_timeout{0};  // test hook: streaming waits give up (see the header)
@@ -71,6 +72,7 @@ bool pdl_on() { return g_pdl.load() != 0; }
 bool constant_weights_on() { return g_const_w.load() != 0; }
 bool inject_timeout_on() { return g_inject_timeout.load() != 0; }
 int inject_split_timeout() { return g_inject_split.load(); }
+int linear_policy() { return g_force_linear.load(); }
 long long wait_limit_cycles() { return inject_timeout_on() ? kTestWaitLimit : kWaitLimit; }
 
 // True if `ptr` is plain device memory: the only memory the streaming
@@ -565,6 +567,12 @@ int gnq_query_launch(int64_t M, int64_t H, int k, int has_residual, int write_y,
     *cluster = ls.stream ? 0 : ls.cluster;
     *vpt = ls.vpt;
     *form = ls.lean ? 2 : 1;
+    return GNQ_OK;
+}
+
+int gnq_set_linear_policy(int kernel) {
+    if (kernel < 0 || kernel > 2) return GNQ_ERR_SHAPE;
+    gnq::g_force_linear.store(kernel);
     return GNQ_OK;
 }
 

@@ -32,6 +32,8 @@ bool pdl_on();
 bool constant_weights_on();
 bool inject_timeout_on();
 int inject_split_timeout();
+// Kernel that gnq_set_linear_policy forces (0: the automatic choice).
+int linear_policy();
 
 // Clock cycles a bounded wait may spin (shorter under the test hooks).
 constexpr long long kWaitLimit = 1LL << 31;      // about a second

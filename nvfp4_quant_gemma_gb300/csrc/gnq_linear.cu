@@ -447,6 +447,25 @@ cudaError_t launch_linear(const CUtensorMap &mw, const CUtensorMap &mx, const Li
 }  // namespace
 }  // namespace gnq
 
+extern "C" int gnq_query_linear(int64_t M, int64_t N, int64_t K, int out_type, int *kernel, int *tokens, int *split) {
+    using namespace gnq;
+    if (!kernel || !tokens || !split) return GNQ_ERR_NULL;
+    if (out_type < GNQ_BF16 || out_type > GNQ_FP32) return GNQ_ERR_DTYPE;
+    if (M < 1 || M > kMaxM || N <= 0 || N > kMaxM || K <= 0 || K > kMaxH || K % 64 != 0) return GNQ_ERR_SHAPE;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
+    LinearParams p = {};
+    p.K64 = (int)(K / 64);
+    int64_t grid = 0;
+    size_t smem = 0;
+    shape_of(*d, M, N, p, grid, smem);
+    const bool pairs = grid > 0x7FFFFFFF || pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid);
+    *kernel = pairs ? 2 : 1;
+    *tokens = pairs ? 256 : p.T;
+    *split = pairs ? 1 : p.split;
+    return GNQ_OK;
+}
+
 extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *w_q, const void *w_block_scale,
                             const float *alpha, const void *bias, void *y, int64_t M, int64_t N, int64_t K,
                             int out_type, int bias_type, void *stream) {
@@ -488,7 +507,9 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     int64_t grid = 0;
     size_t smem = 0;
     shape_of(*d, M, N, p, grid, smem);
-    if (grid > 0x7FFFFFFF || pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid)) {
+    const int forced = linear_policy();
+    if (grid > 0x7FFFFFFF ||
+        (forced ? forced == 2 : pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid))) {
         e = launch_linear_pair(p, q, w_q, out_type, bias_type, d->sms, s);
         if (e == cudaSuccess) return GNQ_OK;
         cudaGetLastError();

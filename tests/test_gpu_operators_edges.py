@@ -1,6 +1,11 @@
 """GPU tests of the operators around the NVFP4 linear where a call goes wrong
 in part, at the ends of a value range, or on a kernel that the size alone would
 not choose."""
+import contextlib
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -117,3 +122,105 @@ def test_gated_activation_does_not_depend_on_its_neighbours(gnq):
         keep = torch.ones(512, dtype=torch.bool)
         keep[5::16] = False
         assert torch.equal(a[:, keep], b[:, keep])
+
+
+# ---------------------------------------------------------------------------
+# both kernels of the product on shapes that the choice would give to the other
+# ---------------------------------------------------------------------------
+@contextlib.contextmanager
+def linear_kernel(gnq, kernel):
+    gnq.set_linear_policy(kernel)
+    try:
+        yield
+    finally:
+        gnq.set_linear_policy(0)
+
+
+def _product(gnq, M, N, K, T, bias=None, shift=0, seed=0):
+    """One product between guard bytes, against 64 bits; the bias starts
+    `shift` elements into its buffer."""
+    q, sf = random_nvfp4(M, K, seed)
+    wq, wsf = random_nvfp4(N, K, seed + 1)
+    a = _one(0.0078125 * 1.37 / K ** 0.5)
+    b = None
+    if bias is not None:
+        buf = (torch.randn(N + shift, generator=torch.Generator().manual_seed(seed)) * 2).to(bias).cuda()
+        b = buf[shift:]
+    size = torch.empty((), dtype=T).element_size()
+    raw = torch.full((M * N * size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = raw[256:256 + M * N * size].view(T).view(M, N)
+    gnq.nvfp4_linear(q.cuda(), sf.cuda(), wq.cuda(), wsf.cuda(), a, bias=b, out=y)
+    torch.cuda.synchronize()
+    assert bool((raw[:256] == 0xA5).all()) and bool((raw[256 + M * N * size:] == 0xA5).all())
+    assert gnq.read_device_error() == 0
+    y64, mag = linear64(q, sf, wq, wsf, float(a.cpu()), b)
+    assert_within(y, y64, linear_tolerance(y64, mag, K, T), "y")
+
+
+@pytest.mark.parametrize("M", [1, 65, 128, 129, 257])
+@pytest.mark.parametrize("N,K", [(1, 64), (8, 320), (255, 128), (257, 192), (1000, 64), (8193, 320)])
+def test_cta_pairs_on_small_and_odd_shapes(gnq, M, N, K):
+    """Tiles mostly or (the second CTA of a pair) wholly behind the last token,
+    one column, and a K inside the first stage."""
+    with linear_kernel(gnq, 2):
+        _product(gnq, M, N, K, torch.bfloat16, bias=torch.bfloat16, seed=M + N)
+        _product(gnq, M, N, K, torch.float32, bias=torch.float16, seed=M + N)
+
+
+@pytest.mark.parametrize("T,bias", [(torch.bfloat16, None), (torch.float16, torch.float16), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("M,N,K", [(1300, 8193, 1152), (300, 1001, 512), (1500, 2500, 320), (700, 8200, 192), (600, 1024, 512)])
+def test_cta_pairs_where_the_choice_takes_single_ctas(gnq, M, N, K, T, bias):
+    assert gnq.query_linear(M, N, K, T)[0] == 1
+    with linear_kernel(gnq, 2):
+        _product(gnq, M, N, K, T, bias=bias, seed=M)
+
+
+@pytest.mark.parametrize("M,N,K", [(600, 8200, 1088), (513, 8184, 1216), (770, 8192, 1280), (600, 8192, 1024)])
+def test_single_ctas_where_the_choice_takes_cta_pairs(gnq, M, N, K):
+    assert gnq.query_linear(M, N, K)[0] == 2
+    with linear_kernel(gnq, 1):
+        _product(gnq, M, N, K, torch.bfloat16, bias=torch.bfloat16, seed=M)
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("T,bias", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float16)])
+@pytest.mark.parametrize("N", [512, 515])
+def test_a_bias_off_16_bytes(gnq, kernel, T, bias, N):
+    with linear_kernel(gnq, kernel):
+        for M in (20, 300):
+            for shift in (1, 4):
+                _product(gnq, M, N, 512, T, bias=bias, shift=shift, seed=shift)
+
+
+def test_first_calls_of_both_product_kernels_inside_a_capture():
+    """What the library asks the runtime for on a kernel's first use is allowed there."""
+    code = """
+import torch, nvfp4_quant_gemma_gb300 as gnq
+dev = torch.device("cuda")
+gen = torch.Generator(device=dev).manual_seed(1)
+rnd = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=gen, dtype=torch.uint8, device=dev)
+q, sf, wq, wsf = rnd(0, 256, 600, 256), rnd(0x28, 0x50, 640, 32), rnd(0, 256, 1024, 256), rnd(0x28, 0x50, 1024, 32)
+a = torch.full((1,), 1e-4, device=dev)
+torch.cuda.synchronize()
+
+def run(T):
+    out = []
+    for kernel in (2, 1):
+        gnq.set_linear_policy(kernel)
+        out.append(gnq.nvfp4_linear(q, sf, wq, wsf, a, dtype=T))
+    return out
+
+for T in (torch.bfloat16, torch.float16, torch.float32):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(T)
+    g.replay()
+    torch.cuda.synchronize()
+    for u, v in zip(got, run(T)):
+        assert torch.equal(u, v) and bool((u != 0).any())
+assert gnq.read_device_error() == 0
+print("capture ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert res.returncode == 0 and "capture ok" in res.stdout, res.stderr[-2000:]

@@ -118,3 +118,14 @@ def test_no_cta_reads_the_shared_memory_of_a_peer():
             assert arrival and arrival.group(1) == "release", name
             stores += 1
     assert stores >= 3  # a row's sums, and the parts and the status of a split product
+
+
+def test_linear_policy_and_query_arguments(lib):
+    f = lib.gnq_set_linear_policy
+    assert f(3) == 2 and f(-1) == 2
+    assert f(2) == 0 and f(0) == 0
+    out = [ctypes.byref(ctypes.c_int()) for _ in range(3)]
+    q = lambda M=16, N=64, K=64, t=0, o=out: lib.gnq_query_linear(i64(M), i64(N), i64(K), t, *o)
+    assert q(o=(None, *out[1:])) == 1 and q(t=3) == 3 and q(t=-1) == 3
+    assert q(M=0) == 2 and q(N=0) == 2 and q(K=96) == 2 and q(K=65600) == 2
+    assert q() in (0, 7)  # a choice, or no device here
