@@ -11,7 +11,8 @@ import torch
 
 import oracle
 from gnq_testutil import DTYPES
-from operators_ref import act64, assert_within, linear64, linear_tolerance, random_nvfp4, rounding
+from operators_ref import (act64, assert_within, check_codes, linear64, linear_tolerance, norm64, random_nvfp4, rounding,
+                           sandwich64, swizzle_index)
 
 pytestmark = pytest.mark.gpu
 
@@ -224,3 +225,101 @@ print("capture ok")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
     assert res.returncode == 0 and "capture ok" in res.stdout, res.stderr[-2000:]
+
+
+# ---------------------------------------------------------------------------
+# infinities and NaN, and a scale that the preceding kernel writes
+# ---------------------------------------------------------------------------
+INF, NAN = float("inf"), float("nan")
+
+
+def _same_or_near(got, want, tol, what):
+    """NaN where the definition has NaN, infinities equal, the rest within tol."""
+    got, want = got.double().cpu(), want.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN elsewhere"
+    big = torch.isinf(want)
+    assert torch.equal(got[big], want[big]), f"{what}: infinities differ"
+    rest = ~big & ~torch.isnan(want)
+    assert_within(got[rest], want[rest], tol.cpu()[rest], what)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gated_activation_of_infinities_and_nan(gnq, dtype, act):
+    T = DTYPES[dtype]
+    vals = [0.0, -0.0, 1.0, -1.0, 30.0, -30.0, -88.0, INF, -INF, NAN, 6e4, -6e4]
+    g = torch.tensor(vals).repeat_interleave(len(vals))
+    u = torch.tensor(vals).repeat(len(vals))
+    M, H = 3, g.numel()  # 144: a multiple of 8
+    x = torch.cat([g, u]).to(T)[None].repeat(M, 1)
+    x[1, :H] = 1.5       # a clean row between
+    x[1, H:] = 2.0
+    y = gnq.gated_act_quant(x.cuda(), None, "none", act=act)[2]
+    y64 = act64(x, act)
+    y64 = torch.where(y64.abs() > torch.finfo(T).max * (1 + 2.0 ** -12), torch.copysign(torch.tensor(INF).double(), y64), y64)
+    err = 2.0 ** -13 * y64.abs() + 2.0 ** -218 * x[:, H:].double().abs()
+    _same_or_near(y, y64, err + rounding(y64.abs() + err, T), "y")
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("M,H", [(12, 256), (600, 2048), (4, 16384)])
+def test_sandwich_infinities_and_nan_stay_in_their_rows(gnq, M, H, gate):
+    T = torch.bfloat16
+    gen = torch.Generator().manual_seed(7)
+    x, r, g = (torch.randn(M, H, generator=gen).to(T) for _ in range(3))
+    wp, w = ((torch.randn(H, generator=gen) * 0.3).to(T) for _ in range(2))
+    bx, br = x.clone(), r.clone()
+    bx[1, 9], br[2, 17], bx[3, 40] = INF, -INF, NAN
+
+    def run(a, b):
+        h = torch.empty(M, H, dtype=T, device="cuda")
+        y = gnq.gemma_sandwich_norm_quant(a.cuda(), b.cuda(), wp.cuda(), w.cuda(), 1e-6, None, "none",
+                                          gate=g.cuda() if gate else None, residual_out=h)[2]
+        return h.cpu(), y.cpu()
+
+    (h0, y0), (h, y) = run(x, r), run(bx, br)
+    clean = torch.ones(M, dtype=torch.bool)
+    clean[1:4] = False
+    assert torch.equal(h[clean], h0[clean]) and torch.equal(y[clean], y0[clean])
+    h64, err = sandwich64(bx, br, wp, g if gate else None, 1.0)
+    _same_or_near(h[1:4], h64[1:4], (err + rounding(h64.abs() + err, T))[1:4], "h")
+    y64 = norm64(h, w)
+    _same_or_near(y[1:4], y64[1:4], (2.0 ** -17 * y64.abs() + rounding(y64.abs(), T))[1:4], "y")
+
+
+def test_a_scale_written_by_the_preceding_kernel(gnq):
+    """A kernel that lets its successor start early and writes the successor's
+    scale last (a product with one output): every operator reads the new value."""
+    T, M, H = torch.bfloat16, 40, 1024
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(M, 2 * H, generator=gen).to(T).cuda()
+    r, w = torch.randn(M, H, generator=gen).to(T).cuda(), (torch.randn(H, generator=gen) * 0.3).to(T).cuda()
+    q, sf = (t.cuda() for t in random_nvfp4(1, 4096, 3))
+    one = float(gnq.nvfp4_linear(q, sf, q, sf, _one(1.0), dtype=torch.float32))
+    alphas = [_one(v / one) for v in (150.0, 90.0, 310.0, 40.0)]
+    s = torch.zeros(1, 1, dtype=torch.float32, device="cuda")
+    h, xc = torch.empty_like(r), x[:, :H].contiguous()
+
+    def chain():
+        out = []
+        for a in alphas * 3:
+            for call in (lambda: gnq.quantize(x[:, :H], s, "nvfp4")[0], lambda: gnq.quantize(x[:, :H], s, "fp8")[0],
+                         lambda: gnq.gated_act_quant(x, s, "nvfp4")[0], lambda: gnq.gated_act_quant(x, s, "fp8")[0],
+                         lambda: gnq.gemma_sandwich_norm_quant(xc, r, w, w, 1e-6, s, "nvfp4", residual_out=h)[0],
+                         lambda: gnq.gemma_sandwich_norm_quant(xc, r, w, w, 1e-6, s, "fp8", residual_out=h)[0],
+                         lambda: gnq.nvfp4_dequantize(q, sf, s)):
+                s.fill_(1.0)
+                gnq.nvfp4_linear(q, sf, q, sf, a, out=s)
+                out.append(call())
+        torch.cuda.synchronize()
+        return [t.view(torch.uint8) for t in out]
+
+    got = chain()
+    gnq.set_pdl(False)
+    try:
+        want = chain()
+    finally:
+        gnq.set_pdl(True)
+    for i, (u, v) in enumerate(zip(got, want)):
+        assert torch.equal(u, v), i
+    assert not torch.equal(got[0], got[7])  # another scale, other codes
