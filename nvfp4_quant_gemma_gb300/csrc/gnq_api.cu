@@ -431,7 +431,7 @@ int run(const void *x, int k, int64_t part_stride, void *residual, const void *w
 // bf16/fp16 values that cannot overflow), or IEEE division for extreme
 // scales.  The ragged tail is padded to a group.
 __global__ void fp8_values_kernel(const float *y, int64_t n, const float *scale, uint8_t *q) {
-    const Fp8Div fd = make_fp8_div(*scale);
+    const Fp8Div fd = make_fp8_div<__nv_bfloat16>(*scale);
     const int64_t groups = (n + 7) / 8;
     for (int64_t g = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; g < groups;
          g += (int64_t)gridDim.x * blockDim.x) {

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace gnq {
 
 enum { MODE_NONE = -1, MODE_FP8 = 0, MODE_NVFP4 = 1, MODE_MXFP8 = 2 };
@@ -442,31 +444,37 @@ template <int N> __device__ __forceinline__ void mul_arr_s(float *v, float c) {
 
 // The static FP8 quotient y / s as the E4M3 encoder needs it.  Two paths,
 // chosen once per CTA:
-//   FP8_PAIR  (2^-80 <= s <= 2^80): the correction step on pairs, in negated
+//   FP8_PAIR  (2^-80 <= s <= 2^80, fp16: <= 141): the correction step on pairs, in negated
 //             form: n0 = RN(y * -r), rem = y + n0 * s (exact),
 //             n1 = RN(rem * -r + n0) = -RN(y / s), signed zeros included; the
 //             code signs are flipped back.  The correction is exact for
 //             |y| >= 2^-103 (below that |y/s| < 2^-23, a zero code of the
-//             right sign either way).  y * (1/s) must be finite: fp16 y is at
-//             most 65504 < 2^126 * s; bf16 y is first clamped to
-//             |y| <= ylim = RD_bf16(1024 s) with its sign kept (any clamped
-//             value has a quotient >= 464 that saturates to 448, like the
-//             true one; NaN passes through).
+//             right sign either way).  y * (1/s) must be finite, so y is first
+//             clamped with its sign kept: bf16 to |y| <= ylim = RD_bf16(1024 s),
+//             fp16 (its infinities alone) to 65504.  A clamped value has a
+//             quotient >= 464 that saturates to 448, like the true one; NaN
+//             passes through.
 //   FP8_IEEE  other scales: IEEE division.
 enum { FP8_IEEE = 0, FP8_PAIR = 2 };
 
 struct Fp8Div {
     float s, r;
-    uint32_t ylim2;  // RD_bf16(1024 s), in both halves of a bf16x2 word
-    float ylim;      // the same value as fp32
+    uint32_t ylim2;  // the clamp's magnitude, in both halves of a 16-bit pair
+    float ylim;      // bf16: the same value as fp32
     bool fast;
 };
 
-__device__ __forceinline__ Fp8Div make_fp8_div(float s) {
+template <typename T> __device__ __forceinline__ Fp8Div make_fp8_div(float s) {
     Fp8Div d;
     d.s = s;
     d.r = __frcp_rn(s);
-    d.fast = s >= 0x1p-80f && s <= 0x1p80f;
+    constexpr bool half = std::is_same<T, __half>::value;
+    d.fast = s >= 0x1p-80f && s <= (half ? 141.f : 0x1p80f);
+    if constexpr (half) {
+        d.ylim2 = 0x7BFF7BFFu;
+        d.ylim = 65504.f;
+        return d;
+    }
     const uint32_t t = __float_as_uint(s * 1024.f) >> 16;  // exact product, then toward zero
     d.ylim2 = t | (t << 16);
     d.ylim = __uint_as_float(t << 16);
@@ -479,14 +487,17 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return d;
 }
 
-// Both bf16 halves of v with their magnitude clamped to ylim2's, signs kept.
-__device__ __forceinline__ uint32_t clamp_bf16x2(uint32_t v, uint32_t ylim2) {
+// Both halves of v with their magnitude clamped to ylim2's, signs kept.
+template <typename T> __device__ __forceinline__ uint32_t clamp16x2(uint32_t v, uint32_t ylim2) {
     uint32_t d;
-    asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(ylim2));
+    if constexpr (std::is_same<T, __half>::value)
+        asm("min.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(ylim2));
+    else
+        asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(ylim2));
     return d;
 }
 
-// Eight E4M3 codes of y[0..8) / s as two words (y already clamped for bf16).
+// Eight E4M3 codes of y[0..8) / s as two words (y already clamped).
 template <int PATH>
 __device__ __forceinline__ void fp8_codes8(const float *y, const Fp8Div &d, uint32_t &lo,
                                            uint32_t &hi) {

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) q
                 if (ACT != ACT_NONE) prefetch_l2_line(src + p.H, true);
             }
     }
-    const QuantCtx qc = make_quant_ctx<false>(p, MODE, nullptr, t, NT);
+    const QuantCtx qc = make_quant_ctx<T, false>(p, MODE, nullptr, t, NT);
     auto finish = [&](auto path) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {

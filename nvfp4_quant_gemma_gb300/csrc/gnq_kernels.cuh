@@ -77,14 +77,14 @@ __device__ __forceinline__ void fill_es_table(float *tab, float g, int t, int nt
 
 // TABLE: NVFP4 blocks look their element scale up in a per-CTA table (else
 // each block divides once; see row_body).
-template <bool TABLE = true>
+template <typename T, bool TABLE = true>
 __device__ __forceinline__ QuantCtx make_quant_ctx(const Params &p, int mode, float *es_smem,
                                                    int t, int nt) {
     QuantCtx qc;
-    qc.fd = make_fp8_div(1.f);
+    qc.fd = make_fp8_div<T>(1.f);
     qc.g = 0.f;
     qc.es_tab = es_smem;
-    if (mode == MODE_FP8) qc.fd = make_fp8_div(__ldg(p.scale));
+    if (mode == MODE_FP8) qc.fd = make_fp8_div<T>(__ldg(p.scale));
     if (mode == MODE_NVFP4) {
         qc.g = __ldg(p.scale);
         if (TABLE) fill_es_table(es_smem, qc.g, t, nt);  // visible after the next __syncthreads
@@ -171,12 +171,12 @@ __device__ __forceinline__ void epilogue_unit(const Params &p, const QuantCtx &q
 
     if (MODE == MODE_FP8) {
         uint4 yq = yb[0];
-        if (FP8PATH == FP8_PAIR && std::is_same<T, __nv_bfloat16>::value) {
+        if (FP8PATH == FP8_PAIR) {
             // keep y * (1/s) finite; clamped values still saturate to 448
-            yq.x = clamp_bf16x2(yq.x, qc.fd.ylim2);
-            yq.y = clamp_bf16x2(yq.y, qc.fd.ylim2);
-            yq.z = clamp_bf16x2(yq.z, qc.fd.ylim2);
-            yq.w = clamp_bf16x2(yq.w, qc.fd.ylim2);
+            yq.x = clamp16x2<T>(yq.x, qc.fd.ylim2);
+            yq.y = clamp16x2<T>(yq.y, qc.fd.ylim2);
+            yq.z = clamp16x2<T>(yq.z, qc.fd.ylim2);
+            yq.w = clamp16x2<T>(yq.w, qc.fd.ylim2);
         }
         Act<T>::unpack(yq, yf);  // the rounded y feeds the quantizer
         uint32_t lo, hi;
@@ -343,7 +343,7 @@ __device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float 
     QuantCtx qc_early{};
     if constexpr (EARLY) {  // constants first, then the wait on the preceding grid
         load_w();
-        qc_early = make_quant_ctx<!ESDIV>(p, MODE, es_smem, t, NT);
+        qc_early = make_quant_ctx<T, !ESDIV>(p, MODE, es_smem, t, NT);
     }
 
     pdl_wait();  // inputs may come from the preceding grid
@@ -414,7 +414,7 @@ __device__ __forceinline__ void row_body(const Params &p, float *warp_ss, float 
     }
     if constexpr (!EARLY) load_w();
 
-    const QuantCtx qc = EARLY ? qc_early : make_quant_ctx<!ESDIV>(p, MODE, es_smem, t, NT);
+    const QuantCtx qc = EARLY ? qc_early : make_quant_ctx<T, !ESDIV>(p, MODE, es_smem, t, NT);
 
     // ---- h = dtype(a + residual), sum of squares ----
     uint4 hb[VPT][U];                        // packed h (the new residual)
@@ -717,7 +717,7 @@ __device__ __forceinline__ void stream_body(const Params &p, uint8_t *dsmem, flo
         }
     }
     const uint32_t b16 = p.weight_bias == 1.f ? one16<T>() : 0u;  // LEAN: bias 1 or 0
-    const QuantCtx qc = make_quant_ctx(p, MODE, es_smem, t, NT);
+    const QuantCtx qc = make_quant_ctx<T>(p, MODE, es_smem, t, NT);
 
     __syncthreads();  // barriers initialised, table filled
 

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(1024 / VPT) __maxnreg__((SandwichForm<MODE, VP
         if (sp.w_post) load_unit<LD_WEIGHT, V8>(sp.w_post + lc[0], pv);
         load_unit<LD_WEIGHT, V8>(p.w + lc[0], wv);
     }
-    const QuantCtx qc = make_quant_ctx<!ESDIV>(p, MODE, nullptr, t, NT);
+    const QuantCtx qc = make_quant_ctx<T, !ESDIV>(p, MODE, nullptr, t, NT);
 
     // The mean of squares of `ss` over the row, as inv = rsqrt(mean + eps).
     auto row_inv = [&](float ss, int k) {

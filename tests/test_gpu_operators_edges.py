@@ -243,6 +243,37 @@ def _same_or_near(got, want, tol, what):
     assert_within(got[rest], want[rest], tol.cpu()[rest], what)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("mode", ["fp8", "nvfp4", "mxfp8"])
+def test_quantize_infinities_and_nan(gnq, mode, dtype):
+    """Infinities saturate as the oracle's encoders say; a NaN reaches only its
+    own block's codes and (FP8) only its own code, which is NaN."""
+    T, scale = DTYPES[dtype], {"fp8": 0.05, "nvfp4": 168.0, "mxfp8": 1.0}[mode]
+    M, H = 37, 512
+    x = (torch.randn(M, H, generator=torch.Generator().manual_seed(4)) * 2).to(T)
+    inf = x.clone()
+    inf[3, 7], inf[3, 100], inf[5] = INF, -INF, INF
+    q, bs = gnq.quantize(inf.cuda(), _one(scale), mode)
+    check_codes(oracle, inf, q, bs, scale, mode, dtype)
+    nan = x.clone()
+    nan[9, 33], nan[9, 300] = NAN, -NAN
+    a, abs_ = gnq.quantize(x.cuda(), _one(scale), mode)
+    b, bbs = gnq.quantize(nan.cuda(), _one(scale), mode)
+    block = {"fp8": 1, "nvfp4": 16, "mxfp8": 32}[mode]
+    hit = torch.zeros(M, H // block, dtype=torch.bool)
+    hit[9, 33 // block] = hit[9, 300 // block] = True
+    per = block // 2 if mode == "nvfp4" else block
+    a, b = (t.view(torch.uint8).cpu().reshape(M, H // block, per) for t in (a, b))
+    assert torch.equal(a[~hit], b[~hit])
+    if mode == "fp8":
+        assert bool(((b[hit] & 0x7F) == 0x7F).all())
+    if mode == "mxfp8":
+        assert torch.equal(abs_.cpu()[~hit], bbs.cpu()[~hit])
+    if mode == "nvfp4":
+        i = swizzle_index(M, H // 16).reshape(-1)[~hit.reshape(-1)]
+        assert torch.equal(abs_.view(torch.uint8).reshape(-1).cpu()[i], bbs.view(torch.uint8).reshape(-1).cpu()[i])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_gated_activation_of_infinities_and_nan(gnq, dtype, act):
@@ -323,3 +354,41 @@ def test_a_scale_written_by_the_preceding_kernel(gnq):
     for i, (u, v) in enumerate(zip(got, want)):
         assert torch.equal(u, v), i
     assert not torch.equal(got[0], got[7])  # another scale, other codes
+
+
+@pytest.mark.parametrize("scale", [0.05, 100.0, 145.0, 1e4, 2.0 ** 80])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_fp8_of_values_that_overflow_16_bits(gnq, dtype, scale):
+    """A y of infinity saturates at 448 / -448 in FP8, at any scale, whichever
+    operator made it: the norm (both kernels, one activation and partial sums),
+    the sandwich norm, the gated activation, the quantization."""
+    T, M, H = DTYPES[dtype], 300, 1024
+    gen = torch.Generator().manual_seed(8)
+    huge = 6e4 if dtype == "fp16" else 3e38
+    x, r = (torch.randn(M, H, generator=gen).to(T).cuda() for _ in range(2))
+    w = torch.randn(H, generator=gen) * 0.3
+    w[5:37:3], w[40] = huge, -huge
+    w = w.to(T).cuda()
+    s = _one(scale)
+
+    def check(q, y, some=True):
+        assert not some or bool(torch.isinf(y).any())
+        check_codes(oracle, y, q, None, scale, "fp8", dtype)
+
+    for kernel in (1, 2):
+        gnq.set_launch_policy(kernel)
+        try:
+            for parts in (x, torch.stack((x, r))):
+                q, _, y = gnq.gemma_add_rms_norm_quant_parts(parts, r.clone(), w, 1e-6, s, "fp8", write_y=True)
+                check(q, y)
+        finally:
+            gnq.set_launch_policy()
+    q, _, y = gnq.gemma_sandwich_norm_quant(x, r.clone(), None, w, 1e-6, s, "fp8", write_y=True)
+    check(q, y)
+    g = torch.randn(M, 2 * H, generator=gen)
+    g[::7, ::5], g[::7, H::5] = huge, huge * 0.99
+    g[1::7, H + 2::5] = -INF
+    q, _, y = gnq.gated_act_quant(g.to(T).cuda(), s, "fp8", act="silu", write_y=True)
+    check(q, y)
+    q, _ = gnq.quantize(y, s, "fp8")
+    check(q, y)
