@@ -410,7 +410,7 @@ def gemma_sandwich_norm_quant(x, residual, post_weight, weight, eps, scale=None,
     st = (_lib or load()).gemma_sandwich_norm_quant(
         x.data_ptr(), residual.data_ptr(), None if residual_out is None else residual_out.data_ptr(),
         None if post_weight is None else post_weight.data_ptr(), weight.data_ptr(),
-        None if gate is None else gate.data_ptr(), gate_stride, residual_scale, eps,
+        None if gate is None else gate.data_ptr(), gate_stride, float(residual_scale), float(eps),
         None if scale is None else scale.data_ptr(), m, 1 if write_y else 0, None if q is None else q.data_ptr(),
         None if bs is None else bs.data_ptr(), None if y is None else y.data_ptr(), M, H, _DTYPE[dt],
         _current_stream(dev) if stream is None else _stream(stream))

@@ -6,6 +6,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -392,3 +393,15 @@ def test_fp8_of_values_that_overflow_16_bits(gnq, dtype, scale):
     check(q, y)
     q, _ = gnq.quantize(y, s, "fp8")
     check(q, y)
+
+
+def test_sandwich_takes_any_real_number(gnq):
+    """eps and the residual scale as a NumPy or a one-element torch value, as the other norms take eps."""
+    T = torch.bfloat16
+    x, r = (torch.randn(5, 256, generator=torch.Generator().manual_seed(i)).to(T).cuda() for i in (1, 2))
+    w = torch.zeros(256, dtype=T, device="cuda")
+    run = lambda s, e: gnq.gemma_sandwich_norm_quant(x, r.clone(), w, w, e, None, "none", residual_scale=s)[2]
+    want = run(0.5, 2.0 ** -20)
+    for s, e in ((np.float32(0.5), np.float32(2.0 ** -20)), (torch.tensor(0.5), torch.tensor(2.0 ** -20))):
+        assert torch.equal(run(s, e), want)
+    assert torch.equal(run(1, 1e-6), run(1.0, 1e-6))
