@@ -39,9 +39,15 @@ struct QuantParams {
 // relative errors of 2^-22 and 2^-23, and the roundings of t count |t| ln 2
 // times 1.25 (SiLU) or at most 6 (tanh-GELU) units of 2^-24: 5e-7 for g near 0,
 // 1.2e-6 and 4e-6 where act(g) is 1e-4 of g, 6e-5 at the end of the range.  The
-// one rounding to 16 bits that follows is 2^-8 (bf16) or 2^-11 (fp16).  The rest
-// is paired fp32 arithmetic: with one operation per instruction a 16384 x 7168
-// batch into FP8 was bound by instruction issue.
+// one rounding to 16 bits that follows is 2^-8 (bf16) or 2^-11 (fp16).  Two fp16
+// values have an exact product in fp32, so there it is formed first: one rounding
+// less, and nearly as many results rounded rightly as with an exact exponential
+// and quotient (wrong ones of a SiLU of standard normal gates 6.0e-5, 5.3e-5
+// with those, 6.8e-5 with the product last; a Newton step on the reciprocal and
+// a two-part exponent give 5.8e-5 and cost a quarter of the time).  In bf16 that
+// product could overflow, and rounding hides the difference.  The rest is paired
+// fp32 arithmetic: with one operation per instruction a 16384 x 7168 batch into
+// FP8 was bound by instruction issue.
 // FAR: beyond t = 100 everything is taken 2^100 times smaller until the last
 // product, so that 1 + 2^t does not pass 2^126, whose reciprocal is subnormal
 // and would be 0 (silu(-88) is -5.3e-37, a normal bf16 value).  Exact scaling:
@@ -60,7 +66,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-template <int ACT, bool FAR> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint64_t u) {
+template <typename T, int ACT, bool FAR> __device__ __forceinline__ uint64_t act_mul2(uint64_t g, uint64_t u) {
     constexpr float kLog2e = 1.4426950408889634f;
     uint64_t t;  // the exponent of two
     if (ACT == ACT_SILU) {
@@ -79,7 +85,10 @@ template <int ACT, bool FAR> __device__ __forceinline__ uint64_t act_mul2(uint64
         t1 = f1 ? t1 - 100.f : t1;
     }
     upk2(add2(pk2(exp2_fast(t0), exp2_fast(t1)), one), d0, d1);
-    const uint64_t y = mul2(mul2(g, pk2(rcp_fast(d0), rcp_fast(d1))), u);
+    const uint64_t r = pk2(rcp_fast(d0), rcp_fast(d1));
+    uint64_t y;
+    if constexpr (std::is_same<T, __half>::value) y = mul2(mul2(g, u), r);
+    else y = mul2(mul2(g, r), u);
     return FAR ? mul2(y, one) : y;
 }
 
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) q
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             float *o = &y[8 * c + i];
-                            upk2(act_mul2<ACT, decltype(far)::value>(pk2(o[0], o[1]), pk2(f[i], f[i + 1])), o[0], o[1]);
+                            upk2(act_mul2<T, ACT, decltype(far)::value>(pk2(o[0], o[1]), pk2(f[i], f[i + 1])), o[0], o[1]);
                         }
                     };
                     if (__any_sync(0xffffffffu, gates_far<T, ACT>(g[v][c]))) activate(std::true_type{});
