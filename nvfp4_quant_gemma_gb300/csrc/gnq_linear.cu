@@ -418,20 +418,31 @@ void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &
 }
 
 // Whether CTA pairs on 256 x 256 tiles take the call (more than 64 tokens).
-// Both times follow the rounds of CTAs and the depth of K; the constants, in
-// microseconds, are fits to calls of 128 to 512 tokens (M = 128, N = 2048,
-// K = 5120: 7.8 against 10.4 us for pairs; 300 x 5000 x 4096: 11.4 against
-// 10.2; 512 x 4096 x 4096: 13 against 9.6).  Pairs store an output with rows
-// off 16 bytes more slowly (141 x 176 x 1088: 6.3 us for pairs, 7.2; 141 x 169:
-// 8.9 and 7.2).
-bool pairs_take(const DevInfo &d, int64_t M, int64_t N, int out_size, const LinearParams &p, int64_t grid) {
+// Both times follow the rounds of CTAs and the depth of K.  A round of the other
+// kernel holds two CTAs per SM where their shared and tensor memory fit; they
+// share what the SM takes in, so a stage of such a round costs 0.455 us against
+// 0.37 alone.  Unsplit tiles of 4-byte outputs, or of odd rows, are stored value by
+// value; pairs store an output with rows off 16 bytes, and 4-byte ones, more
+// slowly.  The constants, in microseconds, are fits to shapes of 65 to 4096 tokens,
+// 32 to 16384 outputs and a K of 64 to 8192, each timed in both kernels; on 2917
+// such shapes, 843 of them with 4-byte outputs, the choice loses 0.6 % on average
+// against the faster kernel, and more than 10 % on 69 (300 x 5000 x 4096: 7.9 us for two CTAs per SM, 10.6 for pairs; 512 x
+// 4096 x 4096: 8.0 and 10.2; 128 x 2048 x 5120: 7.8 and 10.9; 256 x 8192 x 5120:
+// 12.5 and 12.0; 8192 x 8192 x 5120: 159 and 114.5).
+bool pairs_take(const DevInfo &d, int64_t M, int64_t N, int out_size, const LinearParams &p, int64_t grid,
+                size_t smem) {
     if (M <= 64) return false;
-    const int KT = (p.K64 + 3) / 4;
+    const int KT = (p.K64 + 3) / 4, ks = (KT + p.split - 1) / p.split;
     const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), pairs = d.sms / 2;
     const double rounds = (double)((tiles + pairs - 1) / pairs);
-    const double pair = 4.2 + rounds * (0.31 * KT + 0.4) + (N * out_size % 16 ? 1.0 + 1.5 * rounds : 0.0);
-    const double single = 3.0 + (double)((grid + d.sms - 1) / d.sms) * 0.47 * ((KT + p.split - 1) / p.split) +
-                          (p.split > 1 ? 2.5 : 0.0);
+    const double pair = 3.2 + rounds * (2.2 + 0.31 * KT + (N * out_size % 16 ? 2.1 : 0.0) + (out_size == 4 ? 1.1 : 0.0));
+    const bool share = 2 * (smem + 1024 + 512) <= (size_t)d.smem_sm && p.tmem_cols <= 256;
+    const int64_t wave = share ? 2 * d.sms : d.sms, rest = grid % wave;
+    const double whole = (double)(grid / wave) + (rest > (share ? d.sms : 0));  // rounds of `wave` CTAs
+    const double one = share ? (double)(rest > 0 && rest <= d.sms) : whole, two = share ? whole : 0.0;
+    const double slow = p.split == 1 && (out_size == 4 || N % 2) ? 2.1 : 0.0;
+    const double single = 1.2 + one * (1.9 + 0.37 * ks + slow) + two * (2.8 + 0.455 * ks + 2 * slow) +
+                          (p.split > 1 ? 3.0 : 0.0);
     return pair < single;
 }
 
@@ -459,7 +470,7 @@ extern "C" int gnq_query_linear(int64_t M, int64_t N, int64_t K, int out_type, i
     int64_t grid = 0;
     size_t smem = 0;
     shape_of(*d, M, N, p, grid, smem);
-    const bool pairs = grid > 0x7FFFFFFF || pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid);
+    const bool pairs = grid > 0x7FFFFFFF || pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid, smem);
     *kernel = pairs ? 2 : 1;
     *tokens = pairs ? 256 : p.T;
     *split = pairs ? 1 : p.split;
@@ -509,7 +520,7 @@ extern "C" int nvfp4_linear(const void *q, const void *block_scale, const void *
     shape_of(*d, M, N, p, grid, smem);
     const int forced = linear_policy();
     if (grid > 0x7FFFFFFF ||
-        (forced ? forced == 2 : pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid))) {
+        (forced ? forced == 2 : pairs_take(*d, M, N, out_type == GNQ_FP32 ? 4 : 2, p, grid, smem))) {
         e = launch_linear_pair(p, q, w_q, out_type, bias_type, d->sms, s);
         if (e == cudaSuccess) return GNQ_OK;
         cudaGetLastError();

@@ -169,19 +169,27 @@ def test_cta_pairs_on_small_and_odd_shapes(gnq, M, N, K):
         _product(gnq, M, N, K, torch.float32, bias=torch.float16, seed=M + N)
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
 @pytest.mark.parametrize("T,bias", [(torch.bfloat16, None), (torch.float16, torch.float16), (torch.float32, torch.bfloat16)])
-@pytest.mark.parametrize("M,N,K", [(1300, 8193, 1152), (300, 1001, 512), (1500, 2500, 320), (700, 8200, 192), (600, 1024, 512)])
-def test_cta_pairs_where_the_choice_takes_single_ctas(gnq, M, N, K, T, bias):
-    assert gnq.query_linear(M, N, K, T)[0] == 1
-    with linear_kernel(gnq, 2):
+@pytest.mark.parametrize("M,N,K", [(1300, 8193, 1152), (300, 1001, 512), (1500, 2500, 320), (700, 8200, 192),
+                                   (600, 1024, 512), (600, 8200, 1088), (513, 8184, 1216), (770, 8192, 1280)])
+def test_both_kernels_of_the_product(gnq, M, N, K, T, bias, kernel):
+    """Each, whichever of the two the call would take by itself."""
+    with linear_kernel(gnq, kernel):
         _product(gnq, M, N, K, T, bias=bias, seed=M)
 
 
-@pytest.mark.parametrize("M,N,K", [(600, 8200, 1088), (513, 8184, 1216), (770, 8192, 1280), (600, 8192, 1024)])
-def test_single_ctas_where_the_choice_takes_cta_pairs(gnq, M, N, K):
-    assert gnq.query_linear(M, N, K)[0] == 2
-    with linear_kernel(gnq, 1):
-        _product(gnq, M, N, K, torch.bfloat16, bias=torch.bfloat16, seed=M)
+def test_the_choice_between_the_kernels_of_the_product(gnq):
+    """Shapes where one is faster by 15 % or more: two CTAs of the first share
+    an SM, so a grid of up to two per SM is one round."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("the shapes are those of a device of 152 SMs")
+    B, F = torch.bfloat16, torch.float32
+    for M, N, K, T in ((300, 5000, 4096, B), (512, 4096, 4096, B), (2048, 2048, 1024, B), (128, 2048, 5120, B),
+                       (384, 5000, 4096, B)):
+        assert gnq.query_linear(M, N, K, T)[0] == 1, (M, N, K)
+    for M, N, K, T in ((8192, 8192, 5120, B), (3420, 1224, 192, F), (16384, 8192, 1024, B)):
+        assert gnq.query_linear(M, N, K, T)[0] == 2, (M, N, K)
 
 
 @pytest.mark.parametrize("kernel", [1, 2])
