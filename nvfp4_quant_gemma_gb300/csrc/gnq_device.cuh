@@ -444,8 +444,8 @@ template <int N> __device__ __forceinline__ void mul_arr_s(float *v, float c) {
 
 // The static FP8 quotient y / s as the E4M3 encoder needs it.  Two paths,
 // chosen once per CTA:
-//   FP8_PAIR  (2^-80 <= s <= 2^80, fp16: <= 141): the correction step on pairs, in negated
-//             form: n0 = RN(y * -r), rem = y + n0 * s (exact),
+//   FP8_PAIR  (2^-80 <= s <= 2^80, for fp16 y s <= 141): the correction step on
+//             pairs, in negated form: n0 = RN(y * -r), rem = y + n0 * s (exact),
 //             n1 = RN(rem * -r + n0) = -RN(y / s), signed zeros included; the
 //             code signs are flipped back.  The correction is exact for
 //             |y| >= 2^-103 (below that |y/s| < 2^-23, a zero code of the

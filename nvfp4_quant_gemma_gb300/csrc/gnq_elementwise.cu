@@ -12,9 +12,10 @@
 // neighbouring threads neighbouring units, so rows of any width keep every
 // lane busy.  The arithmetic that decides a code is that of the norm kernels
 // (epilogue_unit), so equal 16-bit values give equal codes whatever produced
-// them.  Measured on 16384 rows: fp16 8192 wide to NVFP4 54.6 us (6.3 TB/s),
-// bf16 to FP8 64.0 us (6.3), NVFP4 to bf16 50.1 us (6.9), SiLU of 7168 columns
-// to NVFP4 78.6 us (6.8).
+// them.  Measured on 16384 rows: fp16 8192 wide to NVFP4 54.8 us (6.3 TB/s),
+// bf16 to FP8 63.9 us (6.3), to MXFP8 67.0 (6.1), NVFP4 to bf16 50.0 us (6.9), to
+// fp32 113.6 (5.4), to E4M3 34.2 (6.1), SiLU of 7168 columns to NVFP4 78.5 us
+// (6.8), tanh-GELU to FP8 96.6 (6.1), to MXFP8 96.3 (6.1), not quantized 99.5 (7.1).
 #include "gemma_nq.h"
 #include "gnq_host.cuh"
 #include "gnq_launch.cuh"
@@ -160,9 +161,9 @@ __global__ void __launch_bounds__(256, VPT == 4 && MODE != MODE_NVFP4 ? 6 : 0) q
     }
     // The units that take this place three quarters of a round from now, into
     // L2 with the evict-last priority: bytes in flight that need no register
-    // (SiLU of 16384 x 7168 to NVFP4 84.5 -> 75.3 us, tanh-GELU to FP8 100.7 ->
-    // 94.5, without quantization 106.9 -> 100.8, fp16 16384 x 8192 to NVFP4
-    // 57.2 -> 55.6; the plain FP8 and MXFP8 instances spill with it and lose).
+    // (SiLU of 16384 x 7168 to NVFP4 86.1 -> 78.5 us, tanh-GELU to FP8 102.4 ->
+    // 96.6, without quantization 105.1 -> 99.5, fp16 16384 x 8192 to NVFP4
+    // 57.3 -> 54.9; the plain FP8 and MXFP8 instances spill with it and lose).
     if constexpr (ACT != ACT_NONE || MODE == MODE_NVFP4) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v)

@@ -16,7 +16,7 @@
 //
 // A decode batch is bound by the weight's bytes and, at these sizes, by
 // latency: launch, the first copy, the join and the stores are 3.5 us of the
-// 5.3 us of M = 16, N = 8192, K = 5120 (23.9 MB, 3.5 us at 6.8 TB/s; M = 1,
+// 5.4 us of M = 16, N = 8192, K = 5120 (23.9 MB, 3.5 us at 6.8 TB/s; M = 1,
 // N = 4096, K = 2048: 3.5 us).  So K is split until one round of CTAs fills
 // the SMs, and the split is joined in shared memory across a cluster.
 #include <algorithm>
@@ -419,16 +419,17 @@ void shape_of(const DevInfo &d, int64_t M, int64_t N, LinearParams &p, int64_t &
 
 // Whether CTA pairs on 256 x 256 tiles take the call (more than 64 tokens).
 // Both times follow the rounds of CTAs and the depth of K.  A round of the other
-// kernel holds two CTAs per SM where their shared and tensor memory fit; they
-// share what the SM takes in, so a stage of such a round costs 0.455 us against
-// 0.37 alone.  Unsplit tiles of 4-byte outputs, or of odd rows, are stored value by
+// kernel holds up to two CTAs per SM where their shared and tensor memory fit;
+// with more CTAs than SMs two share what an SM takes in, and a stage of theirs
+// costs 0.455 us against 0.37 alone.  Unsplit tiles of 4-byte outputs, or of odd rows, are stored value by
 // value; pairs store an output with rows off 16 bytes, and 4-byte ones, more
 // slowly.  The constants, in microseconds, are fits to shapes of 65 to 4096 tokens,
 // 32 to 16384 outputs and a K of 64 to 8192, each timed in both kernels; on 2917
 // such shapes, 843 of them with 4-byte outputs, the choice loses 0.6 % on average
-// against the faster kernel, and more than 10 % on 69 (300 x 5000 x 4096: 7.9 us for two CTAs per SM, 10.6 for pairs; 512 x
-// 4096 x 4096: 8.0 and 10.2; 128 x 2048 x 5120: 7.8 and 10.9; 256 x 8192 x 5120:
-// 12.5 and 12.0; 8192 x 8192 x 5120: 159 and 114.5).
+// against the faster kernel, and more than 10 % on 69 (300 x 5000 x 4096: 7.9 us
+// on 120 single CTAs, 10.6 on 40 pairs; 512 x 4096 x 4096: 8.0 on 128, 10.2; 2048 x
+// 2048 x 1024, two per SM: 5.7 and 7.4; 128 x 2048 x 5120, split six ways: 7.8 and
+// 10.9; 256 x 8192 x 5120: 12.9 and 12.0; 8192 x 8192 x 5120: 160 and 114).
 bool pairs_take(const DevInfo &d, int64_t M, int64_t N, int out_size, const LinearParams &p, int64_t grid,
                 size_t smem) {
     if (M <= 64) return false;

@@ -8,10 +8,12 @@
 // What bounds it: a stage is 512 cycles of the tensor cores but 38 912 bytes
 // into each SM, and 608 cycles at 64 bytes a cycle is what a stage takes with
 // the scale copies into tensor memory left out (650 with them; on 40 pairs as
-// on 76, so it is the SM's intake, not the L2).  A larger tile does not fit
-// tensor memory.  The rest is the hand-over between tiles, about 1300 cycles.
-// 4864 x 8192 x 16384: 188 us, 6.9 PFLOP/s; 8192 x 8192 x 5120 (14 rounds for
-// 13.5 of tiles): 113 us, 6.1 PFLOP/s.
+// on 76, so it is the SM's intake, not the L2).  A 256 x 384 tile would take in 768
+// cycles' worth for 768 of products; with its scales it needs 448 columns of
+// tensor memory, so one fits, but not the next tile's sums beside those on their
+// way out.  Which of the two costs more has not been measured.  The rest is the
+// hand-over between tiles, about 1300 cycles.  4864 x 8192 x 16384: 188 us, 6.9
+// PFLOP/s; 8192 x 8192 x 5120 (14 rounds for 13.5 of tiles): 114 us, 6.0 PFLOP/s.
 //
 // Tensor memory (512 columns): the sums of even tiles in columns 0-255, of
 // odd tiles in 192-447, the scales behind.  Two whole tiles and the scales do

@@ -7,7 +7,7 @@
 //   y = dtype(h * rsqrt(mean(h^2) + eps) * (1 + w))   from the rounded h
 //   q = quant(y)
 //
-// Per element it reads x, the residual and a per-token gate, writes h and the
+// Per element it reads x, the residual and a gate of its own, writes h and the
 // codes, and computes about 14 operations: bound by HBM, like the single norm,
 // and by latency below about one row per SM.  One CTA (a cluster for rows
 // wider than 1024 units) holds a row in registers from the first load to the
@@ -57,10 +57,10 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
 
 // Register budget of an instance.  At four 16-byte chunks per thread and
 // operand (256 threads a row for H = 8192), 64 registers keep four rows per
-// SM; with 72, 80 and 96 the fp16 16384 x 8192 batch lost 6, 9 and 36 % into
-// FP8 and 11, 11 and 37 % into NVFP4, and with 56, which spills, 7 and 15 %.
-// With a gate 64 spill too (bf16 2048 x 5120 into NVFP4 18.1 us, 16.1 with 72).
-// Now: fp16 16384 x 8192 into FP8 133.5 us (7.0 TB/s), into NVFP4 122.9 (7.2).
+// SM: fp16 16384 x 8192 into NVFP4 123.2 us with 64 (7.2 TB/s), 131 with 72 and
+// 80, 158 with 96; into FP8 134.9 (7.0 TB/s), 133.8, 133.5, 170; bf16 into MXFP8
+// 134.3, 145.6, 144.7; bf16 8192 x 16384 into FP8, two CTAs a row, 198, 230, 233.
+// With a gate bf16 2048 x 5120 into NVFP4 takes 14.4 us with 72, 14.8 with 64.
 template <int MODE, int VPT, bool GATED> struct SandwichForm {
     static constexpr int chunks = VPT * Unit<MODE>::U;  // of 16 bytes, per thread and operand
     static constexpr int cap = 65536 / (1024 / VPT) < 255 ? 65536 / (1024 / VPT) : 255;

@@ -180,8 +180,7 @@ def test_both_kernels_of_the_product(gnq, M, N, K, T, bias, kernel):
 
 
 def test_the_choice_between_the_kernels_of_the_product(gnq):
-    """Shapes where one is faster by 15 % or more: two CTAs of the first share
-    an SM, so a grid of up to two per SM is one round."""
+    """Shapes where one of them was measured faster by 15 % or more."""
     if torch.cuda.get_device_properties(0).multi_processor_count != 152:
         pytest.skip("the shapes are those of a device of 152 SMs")
     B, F = torch.bfloat16, torch.float32
