@@ -324,7 +324,8 @@ def run(s):
         if op == "quantize":
             fan = s["act"] == "none"
             q, sf = gnq.expert_quantize(s["x"], s["offsets"], s["scale"], slots=s["slots"] if fan else None,
-                                        act=None if fan else s["act"], out=(s["q"], s["sf"]))
+                                        experts=s["experts"] if fan else None, act=None if fan else s["act"],
+                                        out=(s["q"], s["sf"]))
             return gnq.expert_dequantize(q, sf, s["offsets"], s["scale"], out=s["back"]), sf
         if op == "linear":
             return gnq.nvfp4_expert_linear(s["aq"], s["asf"], s["wq"], s["wsf"], s["alpha"], s["offsets"],
