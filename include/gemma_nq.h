@@ -57,9 +57,10 @@
  *    exist) and MXFP8 H % 32 == 0.  H is at most 65536.
  *  - x and residual must not be the same buffer, and y must differ from both
  *    (GNQ_ERR_ALIAS).  gemma_sandwich_norm_quant, gnq_quantize,
- *    gated_act_quant, gnq_nvfp4_dequantize and nvfp4_linear check whole
- *    ranges: what such a call writes may share no byte with what it reads
- *    (but residual_out may be `residual` itself) nor with another output.
+ *    gated_act_quant, gnq_nvfp4_dequantize, nvfp4_linear and the entry points
+ *    of a mixture of experts check whole ranges: what such a call writes may
+ *    share no byte with what it reads (but residual_out may be `residual`
+ *    itself, and out of gnq_expert_combine its `add`) nor with another output.
  *  - Every buffer must hold at least the elements its shape below states;
  *    the library receives raw pointers and cannot check sizes (the Python
  *    binding does, before any launch).
@@ -271,6 +272,117 @@ int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
                  const void *bias, void *y, int64_t M, int64_t N, int64_t K,
                  int out_type, int bias_type, void *stream);
 
+/*
+ * Mixture of experts.  The five entry points below share one order of rows,
+ * by expert: expert e owns rows offsets[e] .. offsets[e + 1] - 1 of the R rows
+ * that a buffer holds; offsets are E + 1 int32 on the device, ascending from 0
+ * to at most R, and are never read on the host.  Rows from offsets[E] on belong
+ * to nobody: they are not read, and what is written leaves them as they were.
+ * Block scales keep the 128x4 layout, each expert's rows starting a 128-row
+ * tile of their own, tile offsets[e] / 128 + e (rounded down): a buffer of
+ * R / 128 + E tiles of 128 rows holds any split.  Bytes of a tile beyond an
+ * expert's last row are not written and influence nothing.
+ * 1 <= E <= 1024 and 1 <= k <= 32.  scale_stride (alpha_stride) is 1 for one
+ * fp32 per expert, 0 for one that all share (GNQ_ERR_MODE otherwise).
+ * Offsets that do not ascend within 0 .. R, and slots that are not a row of
+ * their expert, are found on the device: bit 2 of the device error word is set
+ * (gnq_read_device_error), what they name is left out, and nothing outside the
+ * buffers is touched.
+ */
+
+/*
+ * The router: the k largest logits of each token and their softmax weights,
+ * and the rows of the chosen experts.
+ *
+ *   logits      (M, E) of logits_type GNQ_BF16, GNQ_FP16 or GNQ_FP32 (exact in
+ *               fp32, compared there), rows row_stride >= E elements apart,
+ *               aligned to their size.
+ *   experts     (M, k) int32: by falling logit, equal logits by rising index,
+ *               NaN above every number.  A logit of -inf is never chosen:
+ *               where only such are left, expert and slot are -1 and the
+ *               weight is 0 (a token of a padded batch has -inf alone).
+ *   weights     (M, k) fp32: scale * exp(l_j - l_0) / sum, the sum over the
+ *               chosen (renormalize nonzero) or over all E logits.  A NaN or
+ *               +inf among the summed logits makes the token's weights NaN.
+ *   offsets     (E + 1) int32, written; offsets[E] is the number of rows.
+ *   slots       (M, k) int32: the row of (t, j).  An expert's rows are in
+ *               token order.
+ * M may be 0 (the offsets are then 0); k <= E; M * k < 2^31.
+ */
+int gnq_expert_route(const void *logits, int64_t row_stride, int logits_type,
+                     int64_t M, int64_t E, int k, int renormalize, float scale,
+                     int32_t *experts, float *weights, int32_t *offsets,
+                     int32_t *slots, void *stream);
+
+/*
+ * Rows to NVFP4 with the global scale of their expert, in expert order.
+ *   x           (M, H), or (M, 2H) with act, rows row_stride elements apart as
+ *               for gnq_quantize and gated_act_quant.
+ *   act         0: y = x; GNQ_SILU, GNQ_GELU_TANH: y = dtype(act(gate) * up) as
+ *               gated_act_quant computes it.
+ *   slots, experts  (M, k) as gnq_expert_route gives them: y[t] goes to every
+ *               row slots[t, j] (those below 0 are dropped).  Two slots must
+ *               not name the same row.  Both NULL: x is in expert order
+ *               already, M equals R, and k is ignored.
+ *   scale       global scale(s) g.
+ *   q           (R, H/2) packed codes.
+ *   block_scale (R / 128 + E) * 128 rows of H/16 scale bytes.
+ * H is a multiple of 64.
+ */
+int gnq_expert_quantize(const void *x, int64_t row_stride, int act,
+                        const int32_t *offsets, int64_t E, const int32_t *slots,
+                        const int32_t *experts, int k, const float *scale,
+                        int scale_stride, void *q, void *block_scale, int64_t R,
+                        int64_t M, int64_t H, int dtype, void *stream);
+
+/*
+ * The way back: out = type(code * (block scale / g)) as gnq_nvfp4_dequantize,
+ * for rows in expert order.  scale may be NULL (1).
+ */
+int gnq_expert_dequantize(const void *q, const void *block_scale,
+                          const int32_t *offsets, int64_t E, const float *scale,
+                          int scale_stride, void *out, int64_t R, int64_t K,
+                          int out_type, void *stream);
+
+/*
+ * Products grouped by expert: row r of expert e gives
+ *
+ *     y[r, n] = type(alpha[e] * sum_k a[r, k] w[e, n, k] + bias[e, n])
+ *
+ *   q, block_scale  the activation, as gnq_expert_quantize writes it.
+ *   w_q             (E, N, K/2) packed codes.
+ *   w_block_scale   E times the swizzled (round_up(N,128), K/16) scales of one
+ *                   expert's weight, as gnq_quantize writes them.
+ *   alpha           device fp32, usually 1 / (scale of a * scale of w).
+ *   bias            (E, N) or NULL, of bias_type, as for nvfp4_linear.
+ *   y               (R, N) of out_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
+ * K is a multiple of 64, at most 65536; N is any size, N * E < 2^28.  Memory
+ * and alignment as for nvfp4_linear.
+ */
+int nvfp4_expert_linear(const void *q, const void *block_scale, const void *w_q,
+                        const void *w_block_scale, const float *alpha,
+                        int alpha_stride, const void *bias,
+                        const int32_t *offsets, int64_t E, void *y, int64_t R,
+                        int64_t N, int64_t K, int out_type, int bias_type,
+                        void *stream);
+
+/*
+ * The weighted sum of a token's rows:
+ *
+ *     out[t] = type(sum_j weights[t, j] * y[slots[t, j]] + add[t])
+ *
+ * in fp32, in the order of j, `add` last, rounded once.  Slots below 0 add
+ * nothing; a slot of R or more is reported as above and adds nothing.
+ *   y        (R, H) of y_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
+ *   weights  (M, k) fp32.
+ *   add      (M, H) of out_type or NULL; may be `out` itself.
+ *   out      (M, H) of out_type: y_type, or any of the three if that is GNQ_FP32.
+ * H is a multiple of 8.
+ */
+int gnq_expert_combine(const void *y, const int32_t *slots, const float *weights,
+                       const void *add, void *out, int64_t R, int64_t M,
+                       int64_t H, int k, int y_type, int out_type, void *stream);
+
 /* Human-readable text of a gnq_status (static storage, never NULL). */
 const char *gnq_status_string(int status);
 
@@ -376,8 +488,8 @@ int gnq_set_constant_weights(int enable);
 
 /*
  * Test hook for the failure path of the bounded waits (off by default).
- * With enable = 1, later launches of the persistent streaming kernel and of
- * nvfp4_linear in this process announce 16 bytes more per row (per stage of
+ * With enable = 1, later launches of the persistent streaming kernel, of
+ * nvfp4_linear and of nvfp4_expert_linear in this process announce 16 bytes more per row (per stage of
  * K) than their copies deliver and give a wait at most ~2^20 clock cycles, so
  * each CTA's wait for its first row (stage) gives up: the kernel sets bit 1
  * of the device error word, completes each outstanding barrier with one more
@@ -405,7 +517,8 @@ int gnq_inject_split_timeout(int cta);
  * Device error word of the current device.  Every wait inside a kernel is
  * bounded; a kernel whose wait gives up (about a second without progress)
  * skips the rest of its work, sets bit 1 here and returns, leaving its
- * outputs incomplete.  Copies the word into *flags (synchronising the device)
+ * outputs incomplete.  Bit 2: an entry point of a mixture of experts met
+ * offsets or slots that name no row.  Copies the word into *flags (synchronising the device)
  * and clears it when `clear` is nonzero.
  */
 int gnq_read_device_error(unsigned int *flags, int clear);

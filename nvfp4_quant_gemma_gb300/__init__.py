@@ -9,6 +9,11 @@ from ._binding import (  # noqa: F401
     add_rms_norm_quant,
     alloc_outputs,
     encode_e4m3_e2m1,
+    expert_combine,
+    expert_dequantize,
+    expert_quantize,
+    expert_route,
+    expert_scale_rows,
     gated_act_quant,
     gemma_add_rms_norm,
     gemma_add_rms_norm_quant,
@@ -18,6 +23,7 @@ from ._binding import (  # noqa: F401
     inject_wait_timeout,
     library_path,
     nvfp4_dequantize,
+    nvfp4_expert_linear,
     nvfp4_linear,
     quantize,
     quantize_fp8_values,

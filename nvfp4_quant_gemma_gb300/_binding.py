@@ -53,6 +53,11 @@ def load() -> ctypes.CDLL:
             "gated_act_quant": [P, i64, I, P, I, I, P, P, P, i64, i64, I, P],
             "gnq_nvfp4_dequantize": [P, P, P, P, i64, i64, I, P],
             "nvfp4_linear": [P, P, P, P, P, P, P, i64, i64, i64, I, I, P],
+            "gnq_expert_route": [P, i64, I, i64, i64, I, I, F, P, P, P, P, P],
+            "gnq_expert_quantize": [P, i64, I, P, i64, P, P, I, P, I, P, P, i64, i64, i64, I, P],
+            "gnq_expert_dequantize": [P, P, P, i64, P, I, P, i64, i64, I, P],
+            "nvfp4_expert_linear": [P, P, P, P, P, I, P, P, i64, P, i64, i64, i64, I, I, P],
+            "gnq_expert_combine": [P, P, P, P, P, i64, i64, i64, I, I, I, P],
             "gnq_set_launch_policy": [I, I, I, I],
             "gnq_set_linear_policy": [I],
             "gnq_query_linear": [i64, i64, i64, I, P, P, P],
@@ -82,7 +87,9 @@ EXPORTS = ("gemma_add_rms_norm", "gemma_add_rms_norm_quant", "gemma_add_rms_norm
            "gnq_read_device_error", "gnq_set_pdl", "gnq_encode_e4m3_e2m1",
            "gnq_quantize_fp8_values", "gnq_query_launch", "gnq_set_constant_weights",
            "gnq_inject_wait_timeout", "gnq_inject_split_timeout", "gnq_pdl_consumer", "gemma_sandwich_norm_quant",
-           "gnq_set_linear_policy", "gnq_query_linear", "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear")
+           "gnq_set_linear_policy", "gnq_query_linear", "gnq_quantize", "gated_act_quant", "gnq_nvfp4_dequantize", "nvfp4_linear",
+           "gnq_expert_route", "gnq_expert_quantize", "gnq_expert_dequantize", "nvfp4_expert_linear",
+           "gnq_expert_combine")
 
 
 def status_string(status: int) -> str:
@@ -574,6 +581,234 @@ def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None,
         0 if bias is None else _DTYPE.get(bias.dtype, 2), _current_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "nvfp4_linear")
+    return out
+
+
+# Rows in expert order: expert e owns rows offsets[e] .. offsets[e + 1] - 1
+# (include/gemma_nq.h states the layout of their block scales).
+_I32 = torch.int32
+
+
+def expert_scale_rows(R: int, E: int) -> int:
+    """Rows of the block scales of R rows in expert order."""
+    return (R // 128 + E) * 128
+
+
+def _ints_ok(dev: int, t, n: int) -> bool:
+    return t.dtype is _I32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
+
+
+def _floats_ok(dev: int, t, n: int) -> bool:
+    return t.dtype is _F32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
+
+
+def _expert_count(offsets) -> int:
+    _need(offsets, "offsets", 8, (_I32,))
+    if offsets.dim() != 1:
+        raise ValueError("offsets must be a 1-D tensor of E + 1 rows")
+    return offsets.numel() - 1
+
+
+def _expert_values(t, name: str, E: int) -> int:
+    """1 if `t` holds one fp32 per expert, 0 if one for all."""
+    _need(t, name, 4, (_F32,))
+    if t.numel() == E:
+        return 1
+    if t.numel() == 1:
+        return 0
+    raise ValueError(f"{name} must hold one fp32, or one per expert ({E})")
+
+
+def _choices(slots, name: str, M: int | None = None):
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2 or (M is not None and slots.shape[0] != M):
+        raise ValueError(f"{name} must be a 2-D int32 tensor, a row per token")
+    _need(slots, name, 0, (_I32,))
+    return slots.shape
+
+
+def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
+    """The router of a mixture of experts: the ``k`` largest of the logits
+    (M, E) of each token (bf16, fp16 or fp32; dense rows), and where their rows
+    go.  Returns (experts, weights, offsets, slots): (M, k) int32 by falling
+    logit, ties by index; (M, k) fp32, ``scale`` times the softmax over the
+    chosen (``renormalize``) or over all; (E + 1) int32, the first row of each
+    expert; (M, k) int32, the row of each choice, an expert's rows in token
+    order.  A logit of -inf is never chosen (-1, weight 0, slot -1).  ``out``
+    may supply the four."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or _OUT_TYPE.get(logits.dtype, 3) > 2:
+        raise ValueError("logits must be a 2-D bf16, fp16 or fp32 tensor")
+    M, E = logits.shape
+    stride, sn = logits.stride()
+    if E > 1 and sn != 1:
+        raise ValueError("logits must have contiguous rows")
+    if M <= 1:
+        stride = E
+    k = int(k)
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"k must be 1 .. {min(E, 32)}")
+    if out is None:
+        kw = {"device": logits.device} if logits.is_cuda else {"pin_memory": True}
+        out = (torch.empty((M, k), dtype=_I32, **kw), torch.empty((M, k), dtype=_F32, **kw),
+               torch.empty(E + 1, dtype=_I32, **kw), torch.empty((M, k), dtype=_I32, **kw))
+    experts, weights, offsets, slots = out
+    dev, n = logits.get_device(), M * k
+    try:
+        ok = (dev >= 0 and dev == _current_device() and _ints_ok(dev, experts, n) and _floats_ok(dev, weights, n)
+              and _ints_ok(dev, offsets, E + 1) and _ints_ok(dev, slots, n))
+    except AttributeError:
+        ok = False
+    if not ok:
+        for t, name, size in ((experts, "experts", n), (offsets, "offsets", E + 1), (slots, "slots", n)):
+            _need(t, name, 4 * size, (_I32,))
+        _need(weights, "weights", 4 * n, (_F32,))
+        dev = _place((logits, experts, weights, offsets, slots))
+    st = (_lib or load()).gnq_expert_route(
+        logits.data_ptr(), stride, _OUT_TYPE[logits.dtype], M, E, k, 1 if renormalize else 0, float(scale),
+        experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "expert_route")
+    return experts, weights, offsets, slots
+
+
+def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=None, stream=None):
+    """Rows to NVFP4 in expert order, with the global scale of each row's
+    expert (``scale``: one fp32 per expert, or one).  With ``slots`` and
+    ``experts`` of expert_route, x (M, H) is in token order and each token goes
+    to all of its rows; without, x is in expert order.  ``act`` "silu" or
+    "gelu_tanh": x = [gate | up] (., 2H) and act(gate) * up is quantized.
+    Returns (q, block_scale): (R, H/2) codes and the scales,
+    expert_scale_rows(R, E) rows; ``out`` may supply them."""
+    if act is not None and act not in _ACTS:
+        raise ValueError(f"act must be None or one of {sorted(_ACTS)}")
+    M, H, stride = _rows(x, "x")
+    if act is not None:
+        if H % 2:
+            raise ValueError("x must hold gate and up side by side: an even number of columns")
+        H //= 2
+    if (slots is None) != (experts is None):
+        raise ValueError("slots and experts come together")
+    E = _expert_count(offsets)
+    k, R = 0, M
+    if slots is not None:
+        k = _choices(slots, "slots", M)[1]
+        if _choices(experts, "experts", M)[1] != k:
+            raise ValueError("slots and experts must have the same shape")
+        R = M * k
+    rows = expert_scale_rows(R, E)
+    if out is None:
+        kw = {"device": x.device} if x.is_cuda else {"pin_memory": True}
+        out = (torch.empty((R, H // 2), dtype=_U8, **kw), torch.empty((rows, H // 16), dtype=_U8, **kw).view(_E4M3))
+    q, bs = out
+    per_expert = _expert_values(scale, "scale", E)
+    _need(q, "q", R * H // 2, (_U8,))
+    _need(bs, "block_scale", rows * (H // 16), (_E4M3, _U8))
+    dev = _place((x, offsets, scale, slots, experts, q, bs))
+    st = (_lib or load()).gnq_expert_quantize(
+        x.data_ptr(), stride, 0 if act is None else _ACTS[act], offsets.data_ptr(), E,
+        None if slots is None else slots.data_ptr(), None if experts is None else experts.data_ptr(), k,
+        scale.data_ptr(), per_expert, q.data_ptr(), bs.data_ptr(), R, M, H, _DTYPE[x.dtype],
+        _current_stream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "expert_quantize")
+    return q, bs
+
+
+def _expert_packed(q, block_scale, E: int):
+    """(rows, K) of packed NVFP4 codes in expert order with their block scales."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError("q must be a 2-D tensor of packed codes")
+    R, half = q.shape
+    _need(q, "q", 0, (_U8,))
+    _need(block_scale, "q's block scales", expert_scale_rows(R, E) * (half // 8), (_E4M3, _U8))
+    return R, 2 * half
+
+
+def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None, stream=None):
+    """NVFP4 rows in expert order back to values, code * (block scale / scale
+    of the row's expert), as bf16 (default), fp16, fp32 or E4M3."""
+    E = _expert_count(offsets)
+    R, K = _expert_packed(q, block_scale, E)
+    if out is None:
+        kw = {"device": q.device} if q.is_cuda else {"pin_memory": True}
+        out = torch.empty((R, K), dtype=dtype or torch.bfloat16, **kw)
+    if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
+        raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
+    _need(out, "out", R * K * out.element_size(), (out.dtype,))
+    per_expert = 0 if scale is None else _expert_values(scale, "scale", E)
+    dev = _place((q, block_scale, offsets, scale, out))
+    st = (_lib or load()).gnq_expert_dequantize(
+        q.data_ptr(), block_scale.data_ptr(), offsets.data_ptr(), E, None if scale is None else scale.data_ptr(),
+        per_expert, out.data_ptr(), R, K, _OUT_TYPE[out.dtype],
+        _current_stream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "expert_dequantize")
+    return out
+
+
+def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias=None, dtype=None, out=None,
+                        stream=None):
+    """Products grouped by expert: row r of expert e gives alpha[e] * (row @
+    weight[e]^T) + bias[e].  ``q`` (R, K/2) and ``block_scale`` as
+    expert_quantize returns them; ``weight_q`` (E, N, K/2) and
+    ``weight_block_scale`` (E, round_up(N, 128), K/16), each expert's as
+    ``quantize`` returns it; ``alpha`` one fp32 per expert, or one; ``bias``
+    (E, N).  The output (R, N) is bf16 (default), fp16 or fp32; rows behind the
+    last used one are left as they were."""
+    E = _expert_count(offsets)
+    R, K = _expert_packed(q, block_scale, E)
+    if not isinstance(weight_q, torch.Tensor) or weight_q.dim() != 3 or weight_q.shape[0] != E:
+        raise ValueError(f"weight_q must be a 3-D tensor of packed codes, one matrix for each of {E} experts")
+    N = weight_q.shape[1]
+    _need(weight_q, "weight_q", 0, (_U8,))
+    if 2 * weight_q.shape[2] != K:
+        raise ValueError(f"the activation has K = {K}, the weight {2 * weight_q.shape[2]}")
+    _need(weight_block_scale, "weight_q's block scales", E * round_up(N, 128) * (K // 16), (_E4M3, _U8))
+    per_expert = _expert_values(alpha, "alpha", E)
+    if out is None:
+        out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
+    ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
+    if ot == 3 or (dtype is not None and out.dtype != dtype):
+        raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
+    _need(out, "out", R * N * out.element_size(), (out.dtype,))
+    if bias is not None:
+        _need(bias, "bias", E * N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
+    dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias, out), pinned=False)
+    st = (_lib or load()).nvfp4_expert_linear(
+        q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(), weight_block_scale.data_ptr(), alpha.data_ptr(),
+        per_expert, None if bias is None else bias.data_ptr(), offsets.data_ptr(), E, out.data_ptr(), R, N, K, ot,
+        0 if bias is None else _DTYPE[bias.dtype], _current_stream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "nvfp4_expert_linear")
+    return out
+
+
+def expert_combine(y, slots, weights, add=None, out=None, stream=None):
+    """The weighted sum of a token's rows: out[t] = sum_j weights[t, j] *
+    y[slots[t, j]] + add[t], in fp32, rounded once; slots below 0 add nothing.
+    y (R, H) is bf16, fp16 or fp32; ``out`` (M, H) of y's type, or of any of the
+    three where y is fp32; ``add`` of out's type (``out`` itself, too)."""
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or _OUT_TYPE.get(y.dtype, 3) > 2:
+        raise ValueError("y must be a 2-D bf16, fp16 or fp32 tensor")
+    _need(y, "y", 0, (y.dtype,))
+    R, H = y.shape
+    M, k = _choices(slots, "slots")
+    if out is None:
+        kw = {"device": y.device} if y.is_cuda else {"pin_memory": True}
+        out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, **kw)
+    if not isinstance(out, torch.Tensor) or _OUT_TYPE.get(out.dtype, 3) > 2:
+        raise ValueError("the output must be bf16, fp16 or fp32")
+    _need(weights, "weights", 4 * M * k, (_F32,))
+    _need(out, "out", M * H * out.element_size(), (out.dtype,) if y.dtype is _F32 else (y.dtype,))
+    if add is not None:
+        _need(add, "add", M * H * out.element_size(), (out.dtype,))
+    dev = _place((y, slots, weights, add, out))
+    st = (_lib or load()).gnq_expert_combine(
+        y.data_ptr(), slots.data_ptr(), weights.data_ptr(), None if add is None else add.data_ptr(), out.data_ptr(),
+        R, M, H, k, _OUT_TYPE[y.dtype], _OUT_TYPE[out.dtype],
+        _current_stream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "expert_combine")
     return out
 
 

@@ -15,7 +15,7 @@ namespace gnq {
 enum { MODE_NONE = -1, MODE_FP8 = 0, MODE_NVFP4 = 1, MODE_MXFP8 = 2 };
 
 // Bits of the device error word (set by a kernel, read by gnq_device_error).
-enum { DEVERR_WAIT_TIMEOUT = 1 };
+enum { DEVERR_WAIT_TIMEOUT = 1, DEVERR_BAD_ROW = 2 };
 
 // Compile-time options of a kernel instance (the OPT template argument):
 //   OPT_A32     NVFP4: every 16-bit tensor is 32-byte aligned, so a unit's

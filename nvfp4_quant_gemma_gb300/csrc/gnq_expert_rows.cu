@@ -1,0 +1,390 @@
+// Quantization of rows by expert, the way back, and the weighted combination
+// of a token's rows.  The contracts are in include/gemma_nq.h.
+//
+//   quantize   q = quant(y) with the global scale of the row's expert, y = x
+//              or dtype(act(gate) * up); a token's row goes to every row that
+//              its slots name, or row r to row r
+//   dequantize out = type(code * (block scale / global scale))
+//   combine    out[t] = type(sum_j w[t, j] y[slots[t, j]] + add[t])
+//
+// One pass, a few operations per byte: bound by HBM.  A thread owns whole
+// units (a 16-element block, a pair of blocks, 8 elements) of a flat index, so
+// rows of any width keep every lane busy.  The arithmetic that decides a code
+// is that of the norm kernels, so equal 16-bit values and scales give equal
+// codes whatever produced them.
+#include "gemma_nq.h"
+#include "gnq_elementwise.cuh"
+#include "gnq_expert.cuh"
+#include "gnq_host.cuh"
+#include "gnq_launch.cuh"
+#include "gnq_tcgen05.cuh"
+
+namespace gnq {
+namespace {
+
+constexpr int NT = 256;
+
+struct ExpertRows {
+    const int32_t *offsets;
+    int E, R;            // experts, rows that the buffers in expert order hold
+    const float *scale;  // one per expert, or one
+    int scale_stride;    // 1 or 0
+    unsigned int *err;
+};
+
+// The expert of row `m`, one past the last where it has none (reported unless
+// the row lies behind the last used one); `e` is a lower bound of it.
+__device__ __forceinline__ int expert_from(const ExpertRows &x, int e, int m, int &o) {
+    while (e < x.E && ld_i32(x.offsets + e + 1) <= m) ++e;
+    o = 0;
+    if (e < x.E) {
+        o = row_bound(x.offsets, e, x.R);
+        if (o > m) {
+            atomicOr(x.err, (unsigned)DEVERR_BAD_ROW);
+            e = x.E;
+        }
+    }
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit rows -> NVFP4
+// ---------------------------------------------------------------------------
+struct ExpertQuantParams {
+    ExpertRows x;
+    const uint16_t *in;
+    int64_t row_stride;
+    const int32_t *slots, *experts;  // (M, k), or nullptr: row m goes to row m
+    int k;
+    uint8_t *q, *block_scale;
+    int64_t units;  // 16-element blocks in all rows of `in`
+    int H, upr;     // elements and units of a row
+};
+
+// The block's codes and scale byte for global scale g: the steps of
+// epilogue_unit.
+template <typename T>
+__device__ __forceinline__ void nvfp4_block(const uint4 (&y)[2], float sixth, float g, uint32_t &lo, uint32_t &hi,
+                                            uint32_t &sf) {
+    float v[16];
+    sf = e4m3x2(__fmul_rn(g, sixth), 0.f) & 0xFF;
+    Act<T>::unpack(y[0], &v[0]);
+    Act<T>::unpack(y[1], &v[8]);
+    mul_arr_s<16>(v, element_scale(g, sf));
+    lo = e2m1x8(&v[0]);
+    hi = e2m1x8(&v[8]);
+}
+
+template <typename T, int ACT, bool FAN, bool V8>
+__global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant__ ExpertQuantParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
+    const bool ok = at < p.units;
+    const int m = ok ? (int)(at / p.upr) : 0, col = ok ? (int)(at - (int64_t)m * p.upr) * 16 : 0;
+    pdl_wait();
+    pdl_trigger();
+    const uint16_t *src = p.in + m * p.row_stride + col;
+    uint4 y[2], u[2];
+    load_unit<T, V8>(src, y);
+    if constexpr (ACT != ACT_NONE) {
+        load_unit<T, V8>(src + p.H, u);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float g[8], f[8];
+            Act<T>::unpack(y[c], g);
+            Act<T>::unpack(u[c], f);
+            auto activate = [&](auto far) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2)
+                    upk2(act_mul2<T, ACT, decltype(far)::value>(pk2(g[i], g[i + 1]), pk2(f[i], f[i + 1])), g[i], g[i + 1]);
+            };
+            if (__any_sync(0xffffffffu, gates_far<T, ACT>(y[c]))) activate(std::true_type{});
+            else activate(std::false_type{});
+            y[c] = pack8<T>(g);
+        }
+    }
+    const float sixth = div6(absmax16<T>(y[0], y[1]));
+    const int Kp4 = p.upr >> 2;
+    uint32_t lo, hi, sf;
+    auto store = [&](int row, int e, int o) {
+        st_v2(p.q + (int64_t)row * (p.H >> 1) + (col >> 1), lo, hi);
+        st_u8(p.block_scale + expert_scale_row(e, o, row - o, Kp4) + sf_col_offset(col), sf);
+    };
+    if constexpr (FAN) {
+        if (!ok) return;
+        if (p.x.scale_stride == 0) nvfp4_block<T>(y, sixth, ld_f32(p.x.scale), lo, hi, sf);
+        for (int j = 0; j < p.k; ++j) {
+            const int64_t tj = (int64_t)m * p.k + j;
+            const int row = ld_i32(p.slots + tj), e = ld_i32(p.experts + tj);
+            if (row < 0) continue;
+            const int o = (unsigned)e < (unsigned)p.x.E ? row_bound(p.x.offsets, e, p.x.R) : p.x.R;
+            if (row < o || row >= row_bound(p.x.offsets, min(max(e, 0), p.x.E - 1) + 1, p.x.R)) {
+                atomicOr(p.x.err, (unsigned)DEVERR_BAD_ROW);
+                continue;
+            }
+            if (p.x.scale_stride) nvfp4_block<T>(y, sixth, ld_f32(p.x.scale + e), lo, hi, sf);
+            store(row, e, o);
+        }
+    } else {
+        // one search for the warp, from there each lane by itself
+        int o, e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
+        if (!ok) return;
+        e = expert_from(p.x, e, m, o);
+        if (e == p.x.E) return;
+        nvfp4_block<T>(y, sixth, ld_f32(p.x.scale + e * p.x.scale_stride), lo, hi, sf);
+        store(m, e, o);
+    }
+}
+
+template <typename T, int ACT> cudaError_t launch_expert_quant(const ExpertQuantParams &p, bool v8, cudaStream_t s) {
+    const int64_t grid = (p.units + NT - 1) / NT;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (p.slots)
+        return v8 ? launch(expert_quant_kernel<T, ACT, true, true>, grid, NT, 0, 1, s, p)
+                  : launch(expert_quant_kernel<T, ACT, true, false>, grid, NT, 0, 1, s, p);
+    return v8 ? launch(expert_quant_kernel<T, ACT, false, true>, grid, NT, 0, 1, s, p)
+              : launch(expert_quant_kernel<T, ACT, false, false>, grid, NT, 0, 1, s, p);
+}
+
+template <typename T> cudaError_t launch_expert_quant_act(const ExpertQuantParams &p, int act, bool v8, cudaStream_t s) {
+    if (act == ACT_SILU) return launch_expert_quant<T, ACT_SILU>(p, v8, s);
+    if (act == ACT_GELU_TANH) return launch_expert_quant<T, ACT_GELU_TANH>(p, v8, s);
+    return launch_expert_quant<T, ACT_NONE>(p, v8, s);
+}
+
+// ---------------------------------------------------------------------------
+// NVFP4 -> values
+// ---------------------------------------------------------------------------
+struct ExpertDequantParams {
+    ExpertRows x;
+    const uint8_t *q, *block_scale;
+    void *out;
+    int64_t pairs;  // pairs of 16-element blocks in all rows
+    int ppr, Kp4;   // of a row; scale tiles per 128 rows
+};
+
+template <int OUT, bool V8>
+__global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
+    const bool ok = at < p.pairs;
+    const int m = ok ? (int)(at / p.ppr) : 0, b = ok ? 2 * (int)(at - (int64_t)m * p.ppr) : 0;
+    pdl_wait();
+    pdl_trigger();
+    int o, e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
+    if (!ok) return;
+    e = expert_from(p.x, e, m, o);
+    if (e == p.x.E) return;
+    const uint4 code = ld_stream(p.q + 16 * at);
+    const uint32_t sf = ld_u16(p.block_scale + expert_scale_row(e, o, m - o, p.Kp4) + (b >> 2) * 512 + (b & 3));
+    const float g = p.x.scale ? ld_f32(p.x.scale + e * p.x.scale_stride) : 1.f;
+    nvfp4_pair_out<OUT, V8>(p.out, at * 32, code, sf, g);
+}
+
+template <int OUT> cudaError_t launch_expert_dequant(const ExpertDequantParams &p, cudaStream_t s) {
+    const int64_t grid = (p.pairs + NT - 1) / NT;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (aligned(p.out, 32)) return launch(expert_dequant_kernel<OUT, true>, grid, NT, 0, 1, s, p);
+    return launch(expert_dequant_kernel<OUT, false>, grid, NT, 0, 1, s, p);
+}
+
+// ---------------------------------------------------------------------------
+// weighted combination
+// ---------------------------------------------------------------------------
+struct CombineParams {
+    const void *y, *add;
+    const int32_t *slots;
+    const float *weights;
+    void *out;
+    int64_t units;  // of 8 elements, in all tokens
+    int upr, k, R, H;
+    unsigned int *err;
+};
+
+template <typename T> struct Row8 {  // 8 values of a row, 16 bytes
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const void *p, int64_t i) { return ld_inout(static_cast<const uint16_t *>(p) + i); }
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) { Act<T>::unpack(r, f); }
+    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&f)[8]) {
+        st_v4(static_cast<uint16_t *>(p) + i, pack8<T>(f));
+    }
+};
+template <> struct Row8<float> {
+    struct Raw {
+        uint4 a, b;
+    };
+    static __device__ __forceinline__ Raw load(const void *p, int64_t i) {
+        const float *f = static_cast<const float *>(p) + i;
+        return {ld_inout(f), ld_inout(f + 4)};
+    }
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&f)[8]) {
+        float *o = static_cast<float *>(p) + i;
+        st_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        st_v4(o + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+    }
+};
+
+// Y: type of the rows, O: of `add` and the result.  Sums in fp32, in the order
+// of j, `add` last, one rounding.
+template <typename Y, typename O>
+__global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constant__ CombineParams p) {
+    const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (at >= p.units) return;
+    const int64_t t = at / p.upr;
+    const int col = (int)(at - t * p.upr) * 8;
+    pdl_wait();
+    pdl_trigger();
+    float acc[8] = {};
+    for (int j = 0; j < p.k; ++j) {
+        const int row = ld_i32(p.slots + t * p.k + j);
+        if (row < 0) continue;
+        if (row >= p.R) {
+            atomicOr(p.err, (unsigned)DEVERR_BAD_ROW);
+            continue;
+        }
+        const float w = ld_f32(p.weights + t * p.k + j);
+        float f[8];
+        Row8<Y>::unpack(Row8<Y>::load(p.y, (int64_t)row * p.H + col), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+    }
+    if (p.add) {
+        float f[8];
+        Row8<O>::unpack(Row8<O>::load(p.add, t * p.H + col), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += f[i];
+    }
+    Row8<O>::store(p.out, t * p.H + col, acc);
+}
+
+template <typename Y, typename O> cudaError_t launch_combine(const CombineParams &p, cudaStream_t s) {
+    const int64_t grid = (p.units + NT - 1) / NT;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch(expert_combine_kernel<Y, O>, grid, NT, 0, 1, s, p);
+}
+
+}  // namespace
+}  // namespace gnq
+
+extern "C" {
+
+int gnq_expert_quantize(const void *x, int64_t row_stride, int act, const int32_t *offsets, int64_t E,
+                        const int32_t *slots, const int32_t *experts, int k, const float *scale, int scale_stride,
+                        void *q, void *block_scale, int64_t R, int64_t M, int64_t H, int dtype, void *stream) {
+    using namespace gnq;
+    if (dtype != GNQ_BF16 && dtype != GNQ_FP16) return GNQ_ERR_DTYPE;
+    if (act != ACT_NONE && act != GNQ_SILU && act != GNQ_GELU_TANH) return GNQ_ERR_MODE;
+    if (scale_stride != 0 && scale_stride != 1) return GNQ_ERR_MODE;
+    if (E < 1 || E > kMaxExperts || R < 0 || R > kMaxM || M < 0 || M > kMaxM) return GNQ_ERR_SHAPE;
+    if (H <= 0 || H > kMaxH || H % 64 != 0) return GNQ_ERR_SHAPE;
+    if (slots ? k < 1 || k > kMaxTopK : M != R) return GNQ_ERR_SHAPE;
+    const int64_t width = act == ACT_NONE ? H : 2 * H;
+    if (row_stride < width || row_stride % 8 != 0 || row_stride > (int64_t)1 << 32) return GNQ_ERR_ALIGN;
+    if (M == 0 || R == 0) return GNQ_OK;
+    if (!x || !offsets || !scale || !q || !block_scale || !slots != !experts) return GNQ_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(block_scale, 4) || !aligned(offsets, 4) || !aligned(scale, 4) ||
+        !aligned(slots, 4) || !aligned(experts, 4))
+        return GNQ_ERR_ALIGN;
+    const Extent written[] = {extent(q, code_bytes(GNQ_NVFP4, R, H)), extent(block_scale, (R / 128 + E) * 8 * H)};
+    const Extent read[] = {{x, M, 2 * row_stride, 2 * width}, extent(offsets, 4 * (E + 1)),
+                           extent(scale, 4 * (scale_stride ? E : 1)), extent(slots, 4 * M * k), extent(experts, 4 * M * k)};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
+    ExpertQuantParams p = {};
+    p.x = {offsets, (int)E, (int)R, scale, scale_stride, d->err};
+    p.in = static_cast<const uint16_t *>(x);
+    p.row_stride = row_stride;
+    p.slots = slots;
+    p.experts = experts;
+    p.k = k;
+    p.q = static_cast<uint8_t *>(q);
+    p.block_scale = static_cast<uint8_t *>(block_scale);
+    p.H = (int)H;
+    p.upr = (int)(H / 16);
+    p.units = M * p.upr;
+    const bool v8 = aligned(x, 32) && row_stride % 16 == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return status_of(dtype == GNQ_BF16 ? launch_expert_quant_act<__nv_bfloat16>(p, act, v8, s)
+                                       : launch_expert_quant_act<__half>(p, act, v8, s));
+}
+
+int gnq_expert_dequantize(const void *q, const void *block_scale, const int32_t *offsets, int64_t E,
+                          const float *scale, int scale_stride, void *out, int64_t R, int64_t K, int out_type,
+                          void *stream) {
+    using namespace gnq;
+    if (out_type < GNQ_BF16 || out_type > GNQ_E4M3) return GNQ_ERR_DTYPE;
+    if (scale_stride != 0 && scale_stride != 1) return GNQ_ERR_MODE;
+    if (E < 1 || E > kMaxExperts || R < 0 || R > kMaxM || K <= 0 || K > kMaxH || K % 64 != 0) return GNQ_ERR_SHAPE;
+    if (R == 0) return GNQ_OK;
+    if (!q || !block_scale || !offsets || !out) return GNQ_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_scale, 4) || !aligned(offsets, 4) || !aligned(scale, 4))
+        return GNQ_ERR_ALIGN;
+    const int size = out_type == GNQ_E4M3 ? 1 : out_type == GNQ_FP32 ? 4 : 2;
+    const Extent written[] = {extent(out, R * K * size)};
+    const Extent read[] = {extent(q, code_bytes(GNQ_NVFP4, R, K)), extent(block_scale, (R / 128 + E) * 8 * K),
+                           extent(offsets, 4 * (E + 1)), extent(scale, 4 * (scale_stride ? E : 1))};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
+    ExpertDequantParams p = {};
+    p.x = {offsets, (int)E, (int)R, scale, scale_stride, d->err};
+    p.q = static_cast<const uint8_t *>(q);
+    p.block_scale = static_cast<const uint8_t *>(block_scale);
+    p.out = out;
+    p.ppr = (int)(K / 32);
+    p.Kp4 = (int)(K / 64);
+    p.pairs = R * p.ppr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (out_type) {
+        case GNQ_BF16: return status_of(launch_expert_dequant<OUT_BF16>(p, s));
+        case GNQ_FP16: return status_of(launch_expert_dequant<OUT_FP16>(p, s));
+        case GNQ_FP32: return status_of(launch_expert_dequant<OUT_FP32>(p, s));
+        default: return status_of(launch_expert_dequant<OUT_E4M3>(p, s));
+    }
+}
+
+int gnq_expert_combine(const void *y, const int32_t *slots, const float *weights, const void *add, void *out,
+                       int64_t R, int64_t M, int64_t H, int k, int y_type, int out_type, void *stream) {
+    using namespace gnq;
+    if (y_type < GNQ_BF16 || y_type > GNQ_FP32 || out_type < GNQ_BF16 || out_type > GNQ_FP32) return GNQ_ERR_DTYPE;
+    if (y_type != GNQ_FP32 && y_type != out_type) return GNQ_ERR_DTYPE;
+    if (R < 0 || R > kMaxM || M < 0 || M > kMaxM || k < 1 || k > kMaxTopK) return GNQ_ERR_SHAPE;
+    if (H <= 0 || H > kMaxH || H % 8 != 0) return GNQ_ERR_SHAPE;
+    if (M == 0) return GNQ_OK;
+    if ((!y && R > 0) || !slots || !weights || !out) return GNQ_ERR_NULL;
+    if (!aligned(y, 16) || !aligned(out, 16) || !aligned(add, 16) || !aligned(slots, 4) || !aligned(weights, 4))
+        return GNQ_ERR_ALIGN;
+    const int64_t size = out_type == GNQ_FP32 ? 4 : 2;
+    const Extent written[] = {extent(out, M * H * size)};
+    const Extent read[] = {extent(y, R * H * (y_type == GNQ_FP32 ? 4 : 2)), extent(slots, 4 * M * k),
+                           extent(weights, 4 * M * k), extent(add == out ? nullptr : add, M * H * size)};
+    if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
+    CombineParams p = {};
+    p.y = y;
+    p.add = add;
+    p.slots = slots;
+    p.weights = weights;
+    p.out = out;
+    p.upr = (int)(H / 8);
+    p.units = M * p.upr;
+    p.k = k;
+    p.R = (int)R;
+    p.H = (int)H;
+    p.err = d->err;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (y_type == GNQ_BF16) return status_of(launch_combine<__nv_bfloat16, __nv_bfloat16>(p, s));
+    if (y_type == GNQ_FP16) return status_of(launch_combine<__half, __half>(p, s));
+    if (out_type == GNQ_BF16) return status_of(launch_combine<float, __nv_bfloat16>(p, s));
+    if (out_type == GNQ_FP16) return status_of(launch_combine<float, __half>(p, s));
+    return status_of(launch_combine<float, float>(p, s));
+}
+
+}  // extern "C"

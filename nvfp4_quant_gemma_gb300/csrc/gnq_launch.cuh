@@ -5,9 +5,17 @@
 // parallel.
 #pragma once
 
+#include "gemma_nq.h"
 #include "gnq_kernels.cuh"
 
 namespace gnq {
+
+// Status of a launch.
+inline int status_of(cudaError_t e) {
+    if (e == cudaSuccess) return GNQ_OK;
+    cudaGetLastError();  // reported here; do not leave it for the caller's next check
+    return GNQ_ERR_CUDA;
+}
 
 struct LaunchShape {
     bool stream;     // persistent streaming kernel (else one CTA/cluster per row)
