@@ -49,7 +49,8 @@ KERNEL_SOURCES = ["nvfp4_quant_gemma_gb300/csrc/" + f for f in (
     "gnq_mode_fp8.cu", "gnq_mode_nvfp4.cu", "gnq_mode_mxfp8.cu", "gnq_host.cuh", "gnq_tcgen05.cuh",
     "gnq_sandwich.cu", "gnq_elementwise.cuh", "gnq_elementwise.cu", "gnq_linear.cu",
     "gnq_linear.cuh", "gnq_linear_pair.cu", "gnq_expert.cuh", "gnq_expert_route.cu",
-    "gnq_expert_rows.cu", "gnq_expert_linear.cuh", "gnq_expert_linear.cu")]
+    "gnq_expert_rows.cu", "gnq_expert_linear.cuh", "gnq_expert_linear.cu",
+    "gnq_expert_linear_pair.cu")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "dram_traffic.txt")
 
 

@@ -249,6 +249,11 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
     return launch(fn, grid, 32 * kWarps, smem, 1, s, mw, mx, x);
 }
 
+// Whether CTA pairs take the call.
+bool pairs_take(int64_t E, int64_t R, int64_t N) {
+    return R > 64 && std::min(E, R) * ((N + 255) / 256) >= 152;
+}
+
 }  // namespace
 }  // namespace gnq
 
@@ -295,6 +300,9 @@ extern "C" int nvfp4_expert_linear(const void *q, const void *block_scale, const
     p.err = d->err;
     p.wait_limit = wait_limit_cycles();
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int forced = linear_policy();
+    if (forced ? forced == 2 : pairs_take(E, R, N)) return status_of(launch_expert_linear_pair(x, q, w_q, out_type, bias_type, d->sms, s));
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
     p.T = R <= 32 ? 32 : R <= 64 ? 64 : 128;
     p.tmem_cols = p.T == 32 ? 128 : p.T == 64 ? 256 : 512;  // two tiles' sums and the scales
@@ -306,7 +314,6 @@ extern "C" int nvfp4_expert_linear(const void *q, const void *block_scale, const
     const int64_t grid = std::min<int64_t>(tiles, d->sms);
     CUtensorMap mw, mx;
     if (!encode_codes(&mw, w_q, E * N, K, kTileN) || !encode_codes(&mx, q, R, K, kRowBox)) return GNQ_ERR_CUDA;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (out_type == GNQ_BF16) return status_of(launch_expert_linear<__nv_bfloat16, __nv_bfloat16>(mw, mx, x, grid, smem, s));
     if (out_type == GNQ_FP16) return status_of(launch_expert_linear<__half, __half>(mw, mx, x, grid, smem, s));
     if (bias_type == GNQ_FP16) return status_of(launch_expert_linear<float, __half>(mw, mx, x, grid, smem, s));

@@ -90,4 +90,8 @@ __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int
     return {before, row0, E, T, x.p.n_tiles, (int64_t)total * x.p.n_tiles};
 }
 
+// The kernel of CTA pairs (gnq_expert_linear_pair.cu): out_type as in the ABI.
+cudaError_t launch_expert_linear_pair(ExpertLinearParams x, const void *q, const void *w_q, int out_type, int bias_type,
+                                      int sms, cudaStream_t s);
+
 }  // namespace gnq

@@ -327,6 +327,42 @@ def test_linear_many_experts_and_tiles(gnq):
     _run_linear(gnq, [(i * 53) % 500 for i in range(20)], 1101, 192, torch.float32, seed=4)
 
 
+@pytest.mark.parametrize("T,bias", [(torch.bfloat16, torch.bfloat16), (torch.float16, None), (torch.float32, torch.float16)])
+@pytest.mark.parametrize("counts", [[1], [0, 0], [3, 0, 16, 17], [31, 32, 33, 0, 63, 64, 65], [127, 0, 128, 129, 160],
+                                    [255, 256, 257, 7], [700, 1, 513]])
+@pytest.mark.parametrize("N,K", [(256, 256), (130, 64), (257, 1088), (1001, 192)])
+def test_linear_both_kernels(gnq, counts, N, K, T, bias):
+    """Either kernel, whichever would be picked, and the same bits from both."""
+    got = []
+    for kernel in (1, 2):
+        gnq.set_linear_policy(kernel)
+        try:
+            got.append(_run_linear(gnq, counts, N, K, T, bias=bias, seed=N)[3])
+        finally:
+            gnq.set_linear_policy(0)
+    assert torch.equal(got[0][:sum(counts)], got[1][:sum(counts)])
+
+
+def test_linear_wait_timeout_in_both_kernels(gnq):
+    for kernel in (1, 2):
+        for counts in ([3, 0, 2], [700, 0, 600]):
+            offsets, q, sf, wq, wsf = _operands(counts, 1024, 1024, 1)
+            args = [t.cuda() for t in (q, sf, wq, wsf)]
+            y = torch.full((offsets[-1], 1024), 7.0, dtype=torch.bfloat16, device="cuda")
+            gnq.read_device_error()
+            gnq.set_linear_policy(kernel)
+            gnq.inject_wait_timeout(True)
+            try:
+                gnq.nvfp4_expert_linear(*args, fp32([1.0]), ints(offsets), out=y)
+                torch.cuda.synchronize()
+            finally:
+                gnq.inject_wait_timeout(False)
+                gnq.set_linear_policy(0)
+            assert gnq.read_device_error(clear=True) & 1
+            assert bool((y == 7.0).all())
+            _run_linear(gnq, counts, 384, 1024, torch.bfloat16)
+
+
 @pytest.mark.parametrize("extra", [0, 200])
 def test_linear_without_rows(gnq, extra):
     """No expert has a row: nothing is written."""
