@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
         uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         const int sf_rows = (p.N + 127) / 128;
         bool good = true;
-        for (int64_t i = blockIdx.x; good && i < list.count; i += gridDim.x) {
+        for (int i = blockIdx.x; good && i < list.count; i += (int)gridDim.x) {
             const TileList::Tile tile = list.at(i, e, lane);
             e = tile.e;
             const int w0 = tile.e * p.N + tile.n * kTileN, boxes = (tile.rows + kRowBox - 1) / kRowBox;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
         int s = 0, j = 0, e = 0;
         uint32_t parity = 0;
         bool good = true;
-        for (int64_t i = blockIdx.x; good && i < list.count; i += gridDim.x, ++j) {
+        for (int i = blockIdx.x; good && i < list.count; i += gridDim.x, ++j) {
             const TileList::Tile tile = list.at(i, e, lane);
             e = tile.e;
             const uint32_t idesc = idesc_nvfp4(kTileN, (tile.rows + 15) & ~15);
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
         const int quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
         int j = 0, e = 0;
-        for (int64_t i = blockIdx.x; i < list.count; i += gridDim.x, ++j) {
+        for (int i = blockIdx.x; i < list.count; i += gridDim.x, ++j) {
             const TileList::Tile tile = list.at(i, e, lane);
             e = tile.e;
             const int n = tile.n * kTileN + row;
@@ -307,7 +307,7 @@ extern "C" int nvfp4_expert_linear(const void *q, const void *block_scale, const
     p.T = R <= 32 ? 32 : R <= 64 ? 64 : 128;
     p.tmem_cols = p.T == 32 ? 128 : p.T == 64 ? 256 : 512;  // two tiles' sums and the scales
     const int64_t tiles = (R / p.T + std::min(E, R)) * p.n_tiles;  // at most
-    if (tiles > (int64_t)1 << 40) return GNQ_ERR_SHAPE;
+    if (tiles > 0x3FFFFFFF) return GNQ_ERR_SHAPE;
     const int64_t stage = kBytesW + p.T * 128 + 2 * kBytesSf, lists = TileList::bytes((int)E, kWarps);
     p.stages = (int)std::min<int64_t>(kMaxStages, (d->smem_optin - 1024 - 1024 - lists) / stage);
     const size_t smem = (size_t)(1024 + p.stages * stage + lists);

@@ -21,7 +21,7 @@ struct ExpertLinearParams {
 struct TileList {
     const int *tiles_before, *row0;
     int E, T, n_tiles;
-    int64_t count;
+    int count;
 
     static __host__ __device__ constexpr uint32_t bytes(int E, int warps) { return (2 * (E + 1) + warps) * 4; }
 
@@ -30,8 +30,8 @@ struct TileList {
     };
 
     // Tile `i` (< count), by a converged warp; `e` is the expert of an earlier tile.
-    __device__ __forceinline__ Tile at(int64_t i, int e, int lane) const {
-        const int q = (int)(i / n_tiles);
+    __device__ __forceinline__ Tile at(int i, int e, int lane) const {
+        const int q = (int)((unsigned)i / (unsigned)n_tiles);
         uint32_t above;
         for (;; e += 32) {
             above = __ballot_sync(0xffffffffu, e + lane < E && tiles_before[e + lane + 1] > q);
@@ -39,8 +39,7 @@ struct TileList {
         }
         e += __ffs(above) - 1;
         const int before = tiles_before[e], tiles = tiles_before[e + 1] - before;
-        const int64_t j = i - (int64_t)before * n_tiles;
-        const int n = (int)(j / tiles), t = (int)(j - (int64_t)n * tiles);
+        const int j = i - before * n_tiles, n = (int)((unsigned)j / (unsigned)tiles), t = j - n * tiles;
         Tile x;
         x.e = e;
         x.n = n;
@@ -87,7 +86,7 @@ __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int
     for (int e = first; e < last; ++e) before[e] += base;
     if (t == 0) before[E] = total;
     __syncthreads();
-    return {before, row0, E, T, x.p.n_tiles, (int64_t)total * x.p.n_tiles};
+    return {before, row0, E, T, x.p.n_tiles, total * x.p.n_tiles};
 }
 
 // The kernel of CTA pairs (gnq_expert_linear_pair.cu): out_type as in the ABI.

@@ -5,15 +5,24 @@
 // both SMs and the sums of a tile leave tensor memory while the next tile's
 // come in.  Here the weight takes the M side (256 rows, 128 per CTA) and the
 // expert's rows the N side, as many as there are (rounded up to 32): a ragged
-// last tile costs what its rows take in, not a whole tile.  Tensor memory (512
-// columns): sums of even tiles in columns 0-255, of odd tiles in 192-447, the
-// scales behind; neighbours share 64 columns, which the epilogue takes first.
+// last tile costs what its rows take in, not a whole tile.
 //
-// A lane holds one weight row, so a warp's store is 64 bytes of each of two
-// rows of y (128 of one in fp32): whole sectors straight from registers.
+// Tensor memory (512 columns) does not hold the sums of two tiles of 256 rows
+// and the scales.  So it has a place for 256 rows (columns 0-255) and one for
+// 192 (256-447), and the rows of an expert are taken 448 at a time, as 256 and
+// the rest: a tile starts while the one before is on its way out of the other
+// place.  A tile of at most 192 rows takes whichever place the one before it
+// did not; two tiles of more in a row, and only those, wait for each other.
+//
+// A lane holds one weight row.  16-bit sums go through shared memory, where two
+// warps lay out 32 rows of y by 64 outputs (128 bytes), and leave as a tile
+// store of whole lines, or row by row at an expert's end (stores straight from
+// the registers, 64 bytes of a row each: 258 us for 8192 tokens to 8 of 64
+// experts, N = 4096, K = 2048).  Rows that a tile store cannot take, and 4-byte
+// sums, whose rows are 128 bytes of a warp anyway, leave straight from registers.
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA), 2-9
-// take sums out: two warps for each 32 weight rows, chunks of 64 rows in turn.
+// take sums out: two warps for each 32 weight rows, 64 rows in turn.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -22,16 +31,19 @@
 namespace gnq {
 namespace {
 
-constexpr int kRows = 256;        // rows of an expert, and weight rows, of a tile
+constexpr int kOutputs = 256;                 // weight rows of a tile
+constexpr int kFirst = 256, kSecond = 192;    // rows of the two tiles that one entry of the list stands for
+constexpr int kRows = kFirst + kSecond;
 constexpr int kStages = 5;
 constexpr int kPairWarps = 10;
-constexpr uint32_t kHalf = 128 * kStageK / 2;              // 128 rows of codes of one stage
-constexpr uint32_t kStage = 2 * kHalf + 3 * kBytesSf;      // per CTA: weight, rows, scales of both
-constexpr uint32_t kAccCols = 192, kSfwCol = 448, kSfxCol = 464;  // second tile, scales
+constexpr uint32_t kHalf = 128 * kStageK / 2;          // 128 rows of codes of one stage
+constexpr uint32_t kStage = 2 * kHalf + 4 * kBytesSf;  // per CTA: weight, rows, weight scales, three tiles of row scales
+constexpr uint32_t kBox = 32 * 128;                     // 32 rows x 128 bytes of y
+constexpr uint32_t kPlaceCol = 256, kSfwCol = 448, kSfxCol = 464;  // tensor memory: second place, scales
 
-// y of up to 64 rows (columns of `acc`) x this lane's weight row n.
+// y of up to 32 rows (columns of `acc`) x this lane's weight row n.
 template <typename O>
-__device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, int live, const uint32_t (*acc)[32],
+__device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, int live, const uint32_t (&acc)[32],
                                            float alpha, float bias, int lane) {
     auto result = [&](uint32_t v) { return fmaf(__uint_as_float(v), alpha, bias); };
     // Two 16-bit columns per lane: neighbouring lanes exchange, the even one
@@ -39,14 +51,13 @@ __device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, i
     if constexpr (sizeof(O) == 2) {
         if (N % 2 == 0) {
             const int odd = lane & 1;
+            const uint32_t halves = odd ? 0x3276 : 0x5410;
             O *o = y + n + (odd ? stride - 1 : 0);
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const uint32_t own = Act<O>::pack2(result(acc[i / 32][i % 32]), result(acc[i / 32][i % 32 + 1]));
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-                if (n < N && i + odd < live)
-                    *reinterpret_cast<uint32_t *>(o) =
-                        odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            for (int i = 0; i < 32; i += 2) {
+                const uint32_t own = Act<O>::pack2(result(acc[i]), result(acc[i + 1]));
+                const uint32_t w = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), halves);
+                if (n < N && i + odd < live) *reinterpret_cast<uint32_t *>(o) = w;
                 o += 2 * stride;
             }
             return;
@@ -55,23 +66,83 @@ __device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, i
     if (n < N) {
         O *o = y + n;
 #pragma unroll
-        for (int i = 0; i < 64; ++i, o += stride)
+        for (int i = 0; i < 32; ++i, o += stride)
             if (i < live) {
-                const float v = result(acc[i / 32][i % 32]);
+                const float v = result(acc[i]);
                 if constexpr (std::is_same<O, float>::value) *o = v;
                 else *o = OutType<O>::round(v);
             }
     }
 }
 
+// Arrival that a product waits for: the sums are in registers (the tensor
+// memory fence before it says so) and nothing else has to be seen.  A release
+// would wait for the stores of y that are under way, two or three microseconds
+// in which the warp takes no sums out (258 us against 202 in the case above).
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Barrier `id` of two warps; with a vote, which both get.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_all(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.pred.aligned q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// Where a pair is in its work: the list's entries that it takes, each as one
+// or two tiles, and the place in tensor memory of each tile.
+struct Walk {
+    int item, step, e;      // entry, entries from one to the next, its expert
+    TileList::Tile entry;
+    int at;                 // first row of the tile in its entry
+    int row, rows;          // first row and rows of the tile
+    int place;              // 0: columns 0-255, 1: 256-447
+    int use0, use1;         // tiles that have taken each place before this one
+
+    __device__ __forceinline__ Walk(int first, int step) : item(first - step), step(step), e(0), at(0), row(0), rows(0), place(1), use0(0), use1(-1) {
+        entry.rows = 0;
+    }
+    // The next tile, by a converged warp; false behind the last.
+    __device__ __forceinline__ bool next(const TileList &list, int lane) {
+        (place ? use1 : use0) += 1;
+        at += kFirst;
+        if (at >= entry.rows) {
+            item += step;
+            if (item >= list.count) return false;
+            entry = list.at(item, e, lane);
+            e = entry.e;
+            at = 0;
+        }
+        row = entry.row + at;
+        rows = min(kFirst, entry.rows - at);
+        place = rows > kSecond ? 0 : place ^ 1;
+        return true;
+    }
+    __device__ __forceinline__ int use() const { return place ? use1 : use0; }
+    // Rows of each CTA of the pair: half, rounded up to 16.
+    __device__ __forceinline__ int half() const { return (rows + 31) / 32 * 16; }
+    // 32-row groups of the tile's first scale tile before its first row, and
+    // the scale tiles that it touches.
+    __device__ __forceinline__ int shift() const { return ((row - entry.start) & 127) >> 5; }
+    __device__ __forceinline__ int scale_tiles() const { return (shift() + (rows + 31) / 32 + 3) / 4; }
+};
+
 // map_x: boxes of 128 rows, map_x32: of 32.
 template <typename O, typename B>
 __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
     const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_ws,
-    const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ ExpertLinearParams x) {
+    const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ CUtensorMap map_y,
+    const __grid_constant__ ExpertLinearParams x, bool tiled) {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ __align__(16) uint4 topup[kStages];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
@@ -83,17 +154,19 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
     const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };               // first CTA's: both halves landed
     auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };  // each CTA's: products done with it
-    const uint32_t acc_full = bar0 + 8u * (2 * kStages);            // each CTA's: a tile's sums are ready
-    const uint32_t shared_free = acc_full + 8;                      // first CTA's: the shared columns are out
-    const uint32_t done = acc_full + 16;
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };      // each CTA's: a tile's sums are ready
+    auto acc_free = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };  // first CTA's: they are out
+    const uint32_t done = bar0 + 8u * (2 * kStages + 4);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(shared_free, 16);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_free(b), 16);
+        }
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         failed = 0;
@@ -111,34 +184,27 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
 
     pdl_wait();  // inputs may come from the preceding grid, outputs may still be read by it
     pdl_trigger();
-    const TileList list = build_tiles(x, kRows, reinterpret_cast<int *>(dyn + (base - dyn0) + kStages * kStage), kPairWarps);
+    const TileList list = build_tiles(x, kRows, reinterpret_cast<int *>(dyn + (base - dyn0) + kStages * kStage + 4 * kBox), kPairWarps);
 
     const int KT = (p.K64 + 3) / 4;
-    const int64_t first = blockIdx.x / 2, G = gridDim.x / 2;
     auto gave_up = [&] { return *(volatile int *)&failed != 0; };
     auto give_up = [&] {
         atomicOr(p.err, (unsigned)DEVERR_WAIT_TIMEOUT);
         *(volatile int *)&failed = 1;
     };
-    // Rows that each CTA of the pair holds of a tile: half of them, rounded up
-    // to 16.
-    auto half_rows = [](int rows) { return (rows + 31) / 32 * 16; };
-
     if (warp == 0) {
         // ---- copies ----
-        int it = 0, s = 0, e = 0;
+        int it = 0, s = 0;
         uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         const int sf_rows = (p.N + 127) / 128;
-        for (int64_t i = first; i < list.count && !__any_sync(0xffffffffu, gave_up()); i += G) {
-            const TileList::Tile tile = list.at(i, e, lane);
-            e = tile.e;
-            const int half = half_rows(tile.rows), x0 = tile.row + half * rank;
+        Walk w(blockIdx.x / 2, gridDim.x / 2);
+        while (!__any_sync(0xffffffffu, gave_up()) && w.next(list, lane)) {
+            const int half = w.half(), x0 = w.row + half * rank, sf_tiles = w.scale_tiles();
             const int boxes = half > 64 ? 0 : (half + 31) / 32;  // 0: one of 128 rows
-            const bool second = tile.rows > 128;                 // rows of a second scale tile
-            const uint32_t bytes = kHalf + (boxes ? 4096u * boxes : kHalf) + (second ? 3 : 2) * kBytesSf;
-            const int w0 = tile.e * p.N + tile.n * kRows + 128 * rank;
-            const int ws = (tile.e * sf_rows + 2 * tile.n + rank) * p.K64;
-            const int xs = ((tile.start >> 7) + tile.e + ((tile.row - tile.start) >> 7)) * p.K64;
+            const uint32_t bytes = kHalf + (boxes ? 4096u * boxes : kHalf) + (1 + sf_tiles) * kBytesSf;
+            const int w0 = w.e * p.N + w.entry.n * kOutputs + 128 * rank;
+            const int ws = (w.e * sf_rows + 2 * w.entry.n + rank) * p.K64;
+            const int xs = ((w.entry.start >> 7) + w.e + ((w.row - w.entry.start) >> 7)) * p.K64;
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 if (!warp_wait_bounded(empty(s), parity, p.wait_limit)) {
                     give_up();
@@ -155,8 +221,8 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                         if (boxes == 2) tma_load_pair(at + kHalf + 4096, &map_x32, kt * 128, x0 + 32, bar);
                     }
                     tma_load_pair(at + 2 * kHalf, &map_ws, 0, ws + 4 * kt, bar);
-                    tma_load_pair(at + 2 * kHalf + kBytesSf, &map_xs, 0, xs + 4 * kt, bar);
-                    if (second) tma_load_pair(at + 2 * kHalf + 2 * kBytesSf, &map_xs, 0, xs + p.K64 + 4 * kt, bar);
+                    for (int i = 0; i < sf_tiles; ++i)
+                        tma_load_pair(at + 2 * kHalf + (1 + i) * kBytesSf, &map_xs, 0, xs + i * p.K64 + 4 * kt, bar);
                 }
                 __syncwarp();
                 if (++s == kStages) s = 0, parity ^= 1;
@@ -174,20 +240,19 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
             }
     } else if (warp == 1 && rank == 0) {
         // ---- products ----
-        int j = 0, s = 0, e = 0;
+        int s = 0;
         uint32_t parity = 0;
         bool good = true;
-        for (int64_t i = first; good && i < list.count; i += G, ++j) {
-            const TileList::Tile tile = list.at(i, e, lane);
-            e = tile.e;
-            const uint32_t idesc = idesc_nvfp4(256, 2 * half_rows(tile.rows));
-            const bool second = tile.rows > 128;
-            if (j > 0 && !warp_wait_bounded(shared_free, (j - 1) & 1, p.wait_limit)) {
-                give_up();
-                break;
-            }
-            tc_fence_after();
-            const uint32_t acc = tmem + kAccCols * (j & 1);
+        Walk w(blockIdx.x / 2, gridDim.x / 2);
+        // One tile with SF scale tiles of its rows: the loop that limits a
+        // pair, so nothing in it branches or is worked out twice.
+        auto tile = [&](auto sf) {
+            constexpr int SF = decltype(sf)::value;
+            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_nvfp4(256, 2 * w.half()), 0);
+            const uint32_t acc = __shfl_sync(0xffffffffu, tmem + (w.place ? kPlaceCol : 0u), 0);
+            const uint32_t sfw = __shfl_sync(0xffffffffu, tmem + kSfwCol, 0);
+            const uint32_t sfx = __shfl_sync(0xffffffffu, tmem + kSfxCol, 0);
+            const uint32_t shift = __shfl_sync(0xffffffffu, w.shift(), 0);
             for (int kt = 0; kt < KT; ++kt) {
                 // (under the test hook a stage may complete late, by the copy
                 // that makes up for the announcement)
@@ -202,13 +267,13 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                 if (elect_one()) {
                     const uint32_t at = (base >> 4) + (kStage >> 4) * s;
                     auto step = [&](int k) {
-                        cp_scales<2>(tmem + kSfwCol + 4 * k, desc_scales(at + (2 * kHalf + 512 * k) / 16));
-                        cp_scales<2>(tmem + kSfxCol + 8 * k, desc_scales(at + (2 * kHalf + kBytesSf + 512 * k) / 16));
-                        if (second)
-                            cp_scales<2>(tmem + kSfxCol + 8 * k + 4,
-                                         desc_scales(at + (2 * kHalf + 2 * kBytesSf + 512 * k) / 16));
-                        mma_nvfp4<2>(acc, desc_sw128(at + 2 * k), desc_sw128(at + kHalf / 16 + 2 * k), idesc,
-                                     tmem + kSfwCol + 4 * k, tmem + kSfxCol + 8 * k, kt > 0 || k > 0);
+                        cp_scales<2>(sfw + 4 * k, desc_scales(at + (2 * kHalf + 512 * k) / 16));
+#pragma unroll
+                        for (int i = 0; i < SF; ++i)
+                            cp_scales<2>(sfx + 12 * k + 4 * i,
+                                         desc_scales(at + (2 * kHalf + (1 + i) * kBytesSf + 512 * k) / 16));
+                        mma_nvfp4<2>(acc, desc_sw128(at + 2 * k), desc_sw128(at + kHalf / 16 + 2 * k), idesc, sfw + 4 * k,
+                                     sfx + 12 * k + shift, kt > 0 || k > 0);
                     };
                     if (nk >= 4) {
 #pragma unroll
@@ -217,11 +282,22 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                         for (int k = 0; k < nk; ++k) step(k);
                     }
                     tc_commit_pair(empty(s));
-                    if (kt == KT - 1) tc_commit_pair(acc_full);
+                    if (kt == KT - 1) tc_commit_pair(acc_full(w.place));
                 }
                 __syncwarp();
                 if (++s == kStages) s = 0, parity ^= 1;
             }
+        };
+        while (good && w.next(list, lane)) {
+            if (!warp_wait_bounded(acc_free(w.place), (w.use() & 1) ^ 1, p.wait_limit)) {
+                give_up();
+                break;
+            }
+            tc_fence_after();
+            const int sf_tiles = w.scale_tiles();
+            if (sf_tiles == 1) tile(std::integral_constant<int, 1>{});
+            else if (sf_tiles == 2) tile(std::integral_constant<int, 2>{});
+            else tile(std::integral_constant<int, 3>{});
         }
         // every product is done before tensor memory goes away
         if (elect_one()) tc_commit_pair(done);
@@ -229,54 +305,89 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
         if (!mbar_wait_bounded(done, 0, p.wait_limit)) give_up();
     } else if (warp >= 2) {
         // ---- sums out ----
-        // Warps 2-5 take the shared columns of a tile first and then the
-        // third chunk of 64, warps 6-9 the second and the fourth.
+        // Warps 2-5 take rows 0-63 and 128-191 of a tile, warps 6-9 the
+        // others, 32 at a time.  Two warps share a box of 32 rows x 64 outputs.
         const int quad = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
-        const uint32_t free_bar = map_to_cta(shared_free, 0);
-        int j = 0, e = 0;
-        for (int64_t i = first; i < list.count; i += G, ++j) {
-            const TileList::Tile tile = list.at(i, e, lane);
-            e = tile.e;
-            const int n = tile.n * kRows + 128 * rank + 32 * quad + lane;
-            const float alpha = ld_f32(p.alpha + e * x.alpha_stride);
-            const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + (int64_t)e * p.N + n)) : 0.f;
-            const bool ok = mbar_wait_bounded(acc_full, j & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
-            if (!__all_sync(0xffffffffu, ok)) {
+        const int id = 1 + 2 * set + (quad >> 1);     // of the two warps' barrier
+        const bool lead = (quad & 1) == 0;
+        const uint32_t box = base + kStages * kStage + kBox * (id - 1);
+        Walk w(blockIdx.x / 2, gridDim.x / 2);
+        while (w.next(list, lane)) {
+            const int n0 = w.entry.n * kOutputs + 128 * rank + 32 * quad, n = n0 + lane, box_n = n0 & ~63;
+            const float alpha = ld_f32(p.alpha + w.e * x.alpha_stride);
+            const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + (int64_t)w.e * p.N + n)) : 0.f;
+            const bool ok = mbar_wait_bounded(acc_full(w.place), w.use() & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
+            __syncwarp();
+            if (!pair_all(id, ok)) {  // both go on, or neither
                 give_up();
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem + kAccCols * (j & 1) + lanes;
-            // the next tile may start once the shared columns of this one are
-            // out (first set) and all of the one before, whose place it takes
-            // (second set: it has come here)
-            if (set == 1 && lane == 0) arrive_remote(free_bar);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int turn = 2 * h + set;  // chunk in the order of taking: the shared one is the first
-                const int c = j & 1 ? 64 * turn : 64 * ((turn + 3) & 3);
-                const int live = tile.rows - c;
-                uint32_t v[2][32];
+            const uint32_t acc = tmem + lanes + (w.place ? kPlaceCol : 0u);
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+                const int c = 64 * (h & 2) + 64 * set + 32 * (h & 1), live = w.rows - c;  // rows of this chunk and behind
+                uint32_t v[32];
                 if (live > 0) {
-                    tmem_ld32(acc + c, v[0]);
-                    tmem_ld32(acc + c + 32, v[1]);
-                    tmem_wait(v[0]);
-                    tmem_wait(v[1]);
+                    tmem_ld32(acc + c, v);
+                    tmem_wait(v);
                 }
-                if (turn == 0) {
+                if (h == 3) {  // all that this warp takes is in registers
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_remote(free_bar);
+                    if (lane == 0) arrive_relaxed(map_to_cta(acc_free(w.place), 0));
                 }
-                if (live > 0)
-                    store_rows<O>(static_cast<O *>(p.y) + (int64_t)(tile.row + c) * p.N, p.N, n, p.N, live, v, alpha, bias,
-                                  lane);
+                if (live <= 0) continue;
+                O *const y = static_cast<O *>(p.y) + (int64_t)(w.row + c) * p.N;
+                if constexpr (sizeof(O) == 2) {
+                    if (tiled) {
+                        if (lead && lane == 0) tma_store_wait<0>();
+                        __syncwarp();
+                        pair_sync(id);  // the box is free
+                        const uint32_t at = box + 2u * (lane & 7);
+                        const int unit = 4 * (quad & 1) + (lane >> 3);  // 16-byte unit of the row, before the swizzle
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint32_t two = Act<O>::pack2(fmaf(__uint_as_float(v[i]), alpha, bias),
+                                                               fmaf(__uint_as_float(v[i + 1]), alpha, bias));
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 128u * i + 16u * (unit ^ (i & 7))),
+                                         "h"((uint16_t)two)
+                                         : "memory");
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 128u * (i + 1) + 16u * (unit ^ ((i + 1) & 7))),
+                                         "h"((uint16_t)(two >> 16))
+                                         : "memory");
+                        }
+                        if (live >= 32) fence_async_shared();
+                        __syncwarp();
+                        pair_sync(id);  // all of it is written
+                        if (live >= 32) {
+                            if (lead && lane == 0) {
+                                if (box_n < p.N) tma_store_2d(&map_y, box_n, w.row + c, box);
+                                tma_store_commit();
+                            }
+                        } else {
+                            // rows of the next expert stay: each row in one go of a warp
+                            const int col = box_n + 2 * lane;
+                            O *const o = y + col;
+                            if (col < p.N)
+                                for (int r = quad & 1; r < live; r += 2) {
+                                    uint32_t two;
+                                    asm volatile("ld.shared.u32 %0, [%1];"
+                                                 : "=r"(two)
+                                                 : "r"(box + 128u * r + 16u * ((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+                                    *reinterpret_cast<uint32_t *>(o + (int64_t)r * p.N) = two;
+                                }
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                }
+                store_rows<O>(y, p.N, n, p.N, live, v, alpha, bias, lane);
                 __syncwarp();
             }
-            tc_fence_before();  // this tile's reads are done before the arrival at the next
-            __syncwarp();
         }
+        if (lane == 0) tma_store_wait<0>();  // shared memory is read before it goes away
     }
     __syncwarp();
     tc_fence_before();
@@ -290,11 +401,12 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
 }
 
 template <typename O, typename B>
-cudaError_t launch_pair(const CUtensorMap (&m)[5], const ExpertLinearParams &x, int64_t grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_pair(const CUtensorMap (&m)[6], const ExpertLinearParams &x, bool tiled, int64_t grid, size_t smem,
+                        cudaStream_t s) {
     auto fn = expert_linear_pair_kernel<O, B>;
     const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
-    return launch(fn, grid, 32 * kPairWarps, smem, 2, s, m[0], m[1], m[2], m[3], m[4], x);
+    return launch(fn, grid, 32 * kPairWarps, smem, 2, s, m[0], m[1], m[2], m[3], m[4], m[5], x, tiled);
 }
 
 }  // namespace
@@ -302,21 +414,23 @@ cudaError_t launch_pair(const CUtensorMap (&m)[5], const ExpertLinearParams &x, 
 cudaError_t launch_expert_linear_pair(ExpertLinearParams x, const void *q, const void *w_q, int out_type, int bias_type,
                                       int sms, cudaStream_t s) {
     LinearParams &p = x.p;
-    p.n_tiles = (p.N + kRows - 1) / kRows;
+    p.n_tiles = (p.N + kOutputs - 1) / kOutputs;
     const int64_t K = (int64_t)p.K64 * 64, E = x.E, R = p.M;
     const int64_t x_rows = (R / 128 + E) * p.K64, w_rows = E * ((p.N + 127) / 128) * p.K64;
-    if (x_rows > 0x7FFFFFFF || w_rows > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    CUtensorMap m[5] = {};
-    if (!encode_codes(&m[0], w_q, E * p.N, K, 128) || !encode_codes(&m[1], q, R, K, 128) ||
-        !encode_codes(&m[2], q, R, K, 32) || !encode_scales(&m[3], p.w_sf, w_rows) || !encode_scales(&m[4], p.x_sf, x_rows))
-        return cudaErrorInvalidValue;
     const int64_t tiles = (R / kRows + std::min(E, R)) * p.n_tiles;  // at most
+    if (tiles > 0x3FFFFFFF || x_rows > 0x7FFFFFFF || w_rows > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const bool tiled = out_type != GNQ_FP32 && p.N % 8 == 0;  // rows of y are 16-byte aligned
+    CUtensorMap m[6] = {};
+    if (!encode_codes(&m[0], w_q, E * p.N, K, 128) || !encode_codes(&m[1], q, R, K, 128) ||
+        !encode_codes(&m[2], q, R, K, 32) || !encode_scales(&m[3], p.w_sf, w_rows) || !encode_scales(&m[4], p.x_sf, x_rows) ||
+        (tiled && !encode_output(&m[5], p.y, R, p.N, 2)))
+        return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(tiles, sms / 2);
-    const size_t smem = 1024 + kStages * kStage + TileList::bytes(x.E, kPairWarps);
-    if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, x, grid, smem, s);
-    if (out_type == GNQ_FP16) return launch_pair<__half, __half>(m, x, grid, smem, s);
-    if (bias_type == GNQ_FP16) return launch_pair<float, __half>(m, x, grid, smem, s);
-    return launch_pair<float, __nv_bfloat16>(m, x, grid, smem, s);
+    const size_t smem = 1024 + kStages * kStage + 4 * kBox + TileList::bytes(x.E, kPairWarps);
+    if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, x, tiled, grid, smem, s);
+    if (out_type == GNQ_FP16) return launch_pair<__half, __half>(m, x, tiled, grid, smem, s);
+    if (bias_type == GNQ_FP16) return launch_pair<float, __half>(m, x, tiled, grid, smem, s);
+    return launch_pair<float, __nv_bfloat16>(m, x, tiled, grid, smem, s);
 }
 
 }  // namespace gnq

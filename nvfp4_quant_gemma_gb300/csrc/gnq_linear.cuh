@@ -64,6 +64,18 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Tile store of a chunk in shared memory; clipped at the edges of y.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most the last `N` of this thread's committed groups still read shared memory.
+template <int N> __device__ __forceinline__ void tma_store_wait() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // Map of a row-major (rows, K) matrix of packed codes, loaded in tiles of
 // `box` rows x 128 bytes; what lies outside reads as 0.
 bool encode_codes(CUtensorMap *map, const void *codes, int64_t rows, int64_t K, int box);

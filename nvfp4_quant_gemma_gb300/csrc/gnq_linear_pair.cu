@@ -52,18 +52,6 @@ struct PairParams {
     bool bias16;    // the bias is 16-byte aligned
 };
 
-// Tile store of this warp's chunk; clipped at the edges of y.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
-                 "r"(y), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// At most the last `N` of this thread's committed groups still read shared memory.
-template <int N> __device__ __forceinline__ void tma_store_wait() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // Result of 32 sums of one row at columns n .. n + 31: alpha and bias.
 template <typename B>
 __device__ __forceinline__ void scale_bias32(const PairParams &pp, int n, const uint32_t (&acc)[32], float alpha,
