@@ -134,13 +134,26 @@ struct Walk {
     __device__ __forceinline__ int scale_tiles() const { return (shift() + (rows + 31) / 32 + 3) / 4; }
 };
 
-// map_x: boxes of 128 rows, map_x32: of 32.
+struct Maps {
+    CUtensorMap w, ws, y;  // weight codes and scales, output
+    CUtensorMap x[3];      // row codes in boxes of 32, 64 and 128 rows
+    CUtensorMap xs[3];     // row scales in boxes of 1, 2 and 3 tiles
+};
+
+// Load of whole scale tiles into this CTA, completing on a barrier of the
+// pair's first CTA.
+__device__ __forceinline__ void tma_load_tiles(uint32_t dst, const CUtensorMap *map, int k64, int tile, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(k64), "r"(tile), "r"(bar)
+        : "memory");
+}
+
 template <typename O, typename B>
-__global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
-    const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-    const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_ws,
-    const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ CUtensorMap map_y,
-    const __grid_constant__ ExpertLinearParams x, bool tiled) {
+__global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(const __grid_constant__ Maps maps,
+                                                                             const __grid_constant__ ExpertLinearParams x,
+                                                                             bool tiled) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ __align__(16) uint4 topup[kStages];
@@ -152,8 +165,8 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
     const uint32_t rank = cluster_rank();
     const uint32_t dyn0 = (uint32_t)__cvta_generic_to_shared(dyn), base = (dyn0 + 1023u) & ~1023u;
     const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };               // first CTA's: both halves landed
-    auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };  // each CTA's: products done with it
+    auto full = [&](int s) { return bar0 + 8u * s; };                          // first CTA's: both halves landed
+    auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };             // each CTA's: products done with it
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };      // each CTA's: a tile's sums are ready
     auto acc_free = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };  // first CTA's: they are out
     const uint32_t done = bar0 + 8u * (2 * kStages + 4);
@@ -200,11 +213,12 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
         Walk w(blockIdx.x / 2, gridDim.x / 2);
         while (!__any_sync(0xffffffffu, gave_up()) && w.next(list, lane)) {
             const int half = w.half(), x0 = w.row + half * rank, sf_tiles = w.scale_tiles();
-            const int boxes = half > 64 ? 0 : (half + 31) / 32;  // 0: one of 128 rows
-            const uint32_t bytes = kHalf + (boxes ? 4096u * boxes : kHalf) + (1 + sf_tiles) * kBytesSf;
+            const int box = half > 64 ? 2 : half > 32 ? 1 : 0;
+            const CUtensorMap *const map_x = &maps.x[box], *const map_xs = &maps.xs[sf_tiles - 1];
+            const uint32_t bytes = kHalf + (4096u << box) + (1 + sf_tiles) * kBytesSf;
             const int w0 = w.e * p.N + w.entry.n * kOutputs + 128 * rank;
             const int ws = (w.e * sf_rows + 2 * w.entry.n + rank) * p.K64;
-            const int xs = ((w.entry.start >> 7) + w.e + ((w.row - w.entry.start) >> 7)) * p.K64;
+            const int xs = (w.entry.start >> 7) + w.e + ((w.row - w.entry.start) >> 7);
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 if (!warp_wait_bounded(empty(s), parity, p.wait_limit)) {
                     give_up();
@@ -213,16 +227,10 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                 if (elect_one()) {
                     const uint32_t at = base + kStage * s, bar = map_to_cta(full(s), 0);
                     if (rank == 0) mbar_expect_tx(full(s), 2 * bytes + p.tx_extra);
-                    tma_load_pair(at, &map_w, kt * 128, w0, bar);
-                    if (boxes == 0) {
-                        tma_load_pair(at + kHalf, &map_x, kt * 128, x0, bar);
-                    } else {
-                        tma_load_pair(at + kHalf, &map_x32, kt * 128, x0, bar);
-                        if (boxes == 2) tma_load_pair(at + kHalf + 4096, &map_x32, kt * 128, x0 + 32, bar);
-                    }
-                    tma_load_pair(at + 2 * kHalf, &map_ws, 0, ws + 4 * kt, bar);
-                    for (int i = 0; i < sf_tiles; ++i)
-                        tma_load_pair(at + 2 * kHalf + (1 + i) * kBytesSf, &map_xs, 0, xs + i * p.K64 + 4 * kt, bar);
+                    tma_load_pair(at, &maps.w, kt * 128, w0, bar);
+                    tma_load_pair(at + kHalf, map_x, kt * 128, x0, bar);
+                    tma_load_pair(at + 2 * kHalf, &maps.ws, 0, ws + 4 * kt, bar);
+                    tma_load_tiles(at + 2 * kHalf + kBytesSf, map_xs, 4 * kt, xs, bar);
                 }
                 __syncwarp();
                 if (++s == kStages) s = 0, parity ^= 1;
@@ -235,7 +243,8 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                 const int s = j % kStages;
                 if (mbar_wait_bounded(full(s), (j / kStages) & 1, p.wait_limit)) continue;
                 give_up();
-                if (p.tx_extra) bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, p.tx_extra, full(s));
+                if (p.tx_extra)
+                    bulk_g2s((uint32_t)__cvta_generic_to_shared(&topup[s]), p.w_sf, p.tx_extra, full(s));
                 mbar_wait_bounded(full(s), (j / kStages) & 1, p.wait_limit);
             }
     } else if (warp == 1 && rank == 0) {
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
                         pair_sync(id);  // all of it is written
                         if (live >= 32) {
                             if (lead && lane == 0) {
-                                if (box_n < p.N) tma_store_2d(&map_y, box_n, w.row + c, box);
+                                if (box_n < p.N) tma_store_2d(&maps.y, box_n, w.row + c, box);
                                 tma_store_commit();
                             }
                         } else {
@@ -401,12 +410,12 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(
 }
 
 template <typename O, typename B>
-cudaError_t launch_pair(const CUtensorMap (&m)[6], const ExpertLinearParams &x, bool tiled, int64_t grid, size_t smem,
+cudaError_t launch_pair(const Maps &m, const ExpertLinearParams &x, bool tiled, int64_t grid, size_t smem,
                         cudaStream_t s) {
     auto fn = expert_linear_pair_kernel<O, B>;
     const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
-    return launch(fn, grid, 32 * kPairWarps, smem, 2, s, m[0], m[1], m[2], m[3], m[4], m[5], x, tiled);
+    return launch(fn, grid, 32 * kPairWarps, smem, 2, s, m, x, tiled);
 }
 
 }  // namespace
@@ -416,15 +425,16 @@ cudaError_t launch_expert_linear_pair(ExpertLinearParams x, const void *q, const
     LinearParams &p = x.p;
     p.n_tiles = (p.N + kOutputs - 1) / kOutputs;
     const int64_t K = (int64_t)p.K64 * 64, E = x.E, R = p.M;
-    const int64_t x_rows = (R / 128 + E) * p.K64, w_rows = E * ((p.N + 127) / 128) * p.K64;
+    const int64_t w_rows = E * ((p.N + 127) / 128) * p.K64;
     const int64_t tiles = (R / kRows + std::min(E, R)) * p.n_tiles;  // at most
-    if (tiles > 0x3FFFFFFF || x_rows > 0x7FFFFFFF || w_rows > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (tiles > 0x3FFFFFFF || w_rows > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const bool tiled = out_type != GNQ_FP32 && p.N % 8 == 0;  // rows of y are 16-byte aligned
-    CUtensorMap m[6] = {};
-    if (!encode_codes(&m[0], w_q, E * p.N, K, 128) || !encode_codes(&m[1], q, R, K, 128) ||
-        !encode_codes(&m[2], q, R, K, 32) || !encode_scales(&m[3], p.w_sf, w_rows) || !encode_scales(&m[4], p.x_sf, x_rows) ||
-        (tiled && !encode_output(&m[5], p.y, R, p.N, 2)))
-        return cudaErrorInvalidValue;
+    Maps m = {};
+    bool ok = encode_codes(&m.w, w_q, E * p.N, K, 128) && encode_scales(&m.ws, p.w_sf, w_rows) &&
+              (!tiled || encode_output(&m.y, p.y, R, p.N, 2));
+    for (int i = 0; i < 3; ++i)
+        ok = ok && encode_codes(&m.x[i], q, R, K, 32 << i) && encode_scale_tiles(&m.xs[i], p.x_sf, R / 128 + E, p.K64, i + 1);
+    if (!ok) return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(tiles, sms / 2);
     const size_t smem = 1024 + kStages * kStage + 4 * kBox + TileList::bytes(x.E, kPairWarps);
     if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, x, tiled, grid, smem, s);

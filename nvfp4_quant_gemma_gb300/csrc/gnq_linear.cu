@@ -339,6 +339,15 @@ bool encode_scales(CUtensorMap *map, const void *scales, int64_t rows) {
                         CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool encode_scale_tiles(CUtensorMap *map, const void *scales, int64_t tiles, int64_t K64, int box) {
+    const EncodeFn f = encode_fn();
+    const cuuint64_t dims[3] = {128, (cuuint64_t)K64, (cuuint64_t)tiles}, strides[2] = {512, (cuuint64_t)K64 * 512};
+    const cuuint32_t boxes[3] = {128, 4, (cuuint32_t)box}, step[3] = {1, 1, 1};
+    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(scales), dims, strides, boxes, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size) {
     return encode_tiles(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, y,
                         {(cuuint64_t)N, (cuuint64_t)M}, (cuuint64_t)N * size, {(cuuint32_t)(128 / size), 32},

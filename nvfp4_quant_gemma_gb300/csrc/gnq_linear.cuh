@@ -83,6 +83,10 @@ bool encode_codes(CUtensorMap *map, const void *codes, int64_t rows, int64_t K, 
 // of K), `rows` of them, loaded four at a time.
 bool encode_scales(CUtensorMap *map, const void *scales, int64_t rows);
 
+// Map of the same as tiles of K64 such rows, `tiles` of them, loaded as four
+// rows of `box` neighbouring tiles.
+bool encode_scale_tiles(CUtensorMap *map, const void *scales, int64_t tiles, int64_t K64, int box);
+
 // Map of a row-major (M, N) output of 2- or 4-byte values, stored in tiles of
 // 32 rows x 128 bytes.
 bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size);
