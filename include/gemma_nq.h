@@ -307,7 +307,7 @@ int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
  *   offsets     (E + 1) int32, written; offsets[E] is the number of rows.
  *   slots       (M, k) int32: the row of (t, j).  An expert's rows are in
  *               token order.
- * M may be 0 (the offsets are then 0); k <= E; M * k < 2^31.
+ * M may be 0 (the offsets are then 0); k <= E; M * k <= 2^31 - 2^16.
  */
 int gnq_expert_route(const void *logits, int64_t row_stride, int logits_type,
                      int64_t M, int64_t E, int k, int renormalize, float scale,
@@ -371,7 +371,7 @@ int nvfp4_expert_linear(const void *q, const void *block_scale, const void *w_q,
  *
  *     out[t] = type(sum_j weights[t, j] * y[slots[t, j]] + add[t])
  *
- * in fp32, in the order of j, `add` last, rounded once.  Slots below 0 add
+ * in fp32, in a fixed order, `add` last, rounded once.  Slots below 0 add
  * nothing; a slot of R or more is reported as above and adds nothing.
  *   y        (R, H) of y_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
  *   weights  (M, k) fp32.

@@ -671,6 +671,12 @@ def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
     return experts, weights, offsets, slots
 
 
+def _expert_buffers(R: int, rows: int, H: int, like):
+    kw = {"device": like.device} if like.is_cuda else {"pin_memory": True}
+    return (torch.empty((R, H // 2), dtype=_U8, **kw),
+            torch.empty((rows, H // 16), dtype=_U8, **kw).view(_E4M3))
+
+
 def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=None, stream=None):
     """Rows to NVFP4 in expert order, with the global scale of each row's
     expert (``scale``: one fp32 per expert, or one).  With ``slots`` and
@@ -688,22 +694,41 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
         H //= 2
     if (slots is None) != (experts is None):
         raise ValueError("slots and experts come together")
-    E = _expert_count(offsets)
+    dev = x.get_device()
     k, R = 0, M
-    if slots is not None:
-        k = _choices(slots, "slots", M)[1]
-        if _choices(experts, "experts", M)[1] != k:
-            raise ValueError("slots and experts must have the same shape")
-        R = M * k
-    rows = expert_scale_rows(R, E)
-    if out is None:
-        kw = {"device": x.device} if x.is_cuda else {"pin_memory": True}
-        out = (torch.empty((R, H // 2), dtype=_U8, **kw), torch.empty((rows, H // 16), dtype=_U8, **kw).view(_E4M3))
-    q, bs = out
-    per_expert = _expert_values(scale, "scale", E)
-    _need(q, "q", R * H // 2, (_U8,))
-    _need(bs, "block_scale", rows * (H // 16), (_E4M3, _U8))
-    dev = _place((x, offsets, scale, slots, experts, q, bs))
+    try:
+        E = offsets.numel() - 1
+        if slots is not None:
+            k = slots.shape[1]
+            R = M * k
+        rows = (R // 128 + E) * 128
+        if out is None and dev >= 0:
+            out = _expert_buffers(R, rows, H, x)
+        q, bs = out
+        g = scale.numel()
+        ok = (dev >= 0 and dev == _current_device() and offsets.dim() == 1 and _ints_ok(dev, offsets, 2)
+              and (g == E or g == 1) and _floats_ok(dev, scale, 1)
+              and (slots is None or (slots.shape == (M, k) and experts.shape == (M, k) and _ints_ok(dev, slots, R)
+                                     and _ints_ok(dev, experts, R)))
+              and q.dtype is _U8 and q.is_contiguous() and q.nbytes >= R * H // 2 and q.get_device() == dev
+              and bs.dtype in (_E4M3, _U8) and bs.is_contiguous() and bs.nbytes >= rows * (H // 16)
+              and bs.get_device() == dev)
+        per_expert = 1 if g == E else 0
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        E = _expert_count(offsets)
+        if slots is not None:
+            k = _choices(slots, "slots", M)[1]
+            if _choices(experts, "experts", M)[1] != k:
+                raise ValueError("slots and experts must have the same shape")
+            R = M * k
+        rows = expert_scale_rows(R, E)
+        q, bs = out if out is not None else _expert_buffers(R, rows, H, x)
+        per_expert = _expert_values(scale, "scale", E)
+        _need(q, "q", R * H // 2, (_U8,))
+        _need(bs, "block_scale", rows * (H // 16), (_E4M3, _U8))
+        dev = _place((x, offsets, scale, slots, experts, q, bs))
     st = (_lib or load()).gnq_expert_quantize(
         x.data_ptr(), stride, 0 if act is None else _ACTS[act], offsets.data_ptr(), E,
         None if slots is None else slots.data_ptr(), None if experts is None else experts.data_ptr(), k,
@@ -724,19 +749,41 @@ def _expert_packed(q, block_scale, E: int):
     return R, 2 * half
 
 
+def _expert_packed_ok(dev: int, E: int, q, sf) -> bool:
+    R, half = q.shape
+    return (q.dtype is _U8 and q.is_contiguous() and q.get_device() == dev and sf.dtype in (_E4M3, _U8)
+            and sf.is_contiguous() and sf.nbytes >= (R // 128 + E) * 16 * half and sf.get_device() == dev)
+
+
 def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None, stream=None):
     """NVFP4 rows in expert order back to values, code * (block scale / scale
     of the row's expert), as bf16 (default), fp16, fp32 or E4M3."""
-    E = _expert_count(offsets)
-    R, K = _expert_packed(q, block_scale, E)
-    if out is None:
-        kw = {"device": q.device} if q.is_cuda else {"pin_memory": True}
-        out = torch.empty((R, K), dtype=dtype or torch.bfloat16, **kw)
-    if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
-        raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
-    _need(out, "out", R * K * out.element_size(), (out.dtype,))
-    per_expert = 0 if scale is None else _expert_values(scale, "scale", E)
-    dev = _place((q, block_scale, offsets, scale, out))
+    try:
+        dev = q.get_device()
+        E = offsets.numel() - 1
+        R, half = q.shape
+        K = 2 * half
+        if out is None and dev >= 0:
+            out = torch.empty((R, K), dtype=dtype or torch.bfloat16, device=q.device)
+        g = 1 if scale is None else scale.numel()
+        ok = (dev >= 0 and dev == _current_device() and offsets.dim() == 1 and _ints_ok(dev, offsets, 2)
+              and (g == E or g == 1) and (scale is None or _floats_ok(dev, scale, 1))
+              and _expert_packed_ok(dev, E, q, block_scale) and out.dtype in _OUT_TYPE
+              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.numel() >= R * K
+              and out.get_device() == dev)
+        per_expert = 1 if scale is not None and g == E else 0
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        E = _expert_count(offsets)
+        R, K = _expert_packed(q, block_scale, E)
+        if out is None:
+            out = torch.empty((R, K), dtype=dtype or torch.bfloat16, pin_memory=True)
+        if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
+            raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
+        _need(out, "out", R * K * out.element_size(), (out.dtype,))
+        per_expert = 0 if scale is None else _expert_values(scale, "scale", E)
+        dev = _place((q, block_scale, offsets, scale, out))
     st = (_lib or load()).gnq_expert_dequantize(
         q.data_ptr(), block_scale.data_ptr(), offsets.data_ptr(), E, None if scale is None else scale.data_ptr(),
         per_expert, out.data_ptr(), R, K, _OUT_TYPE[out.dtype],
@@ -755,25 +802,47 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
     ``quantize`` returns it; ``alpha`` one fp32 per expert, or one; ``bias``
     (E, N).  The output (R, N) is bf16 (default), fp16 or fp32; rows behind the
     last used one are left as they were."""
-    E = _expert_count(offsets)
-    R, K = _expert_packed(q, block_scale, E)
-    if not isinstance(weight_q, torch.Tensor) or weight_q.dim() != 3 or weight_q.shape[0] != E:
-        raise ValueError(f"weight_q must be a 3-D tensor of packed codes, one matrix for each of {E} experts")
-    N = weight_q.shape[1]
-    _need(weight_q, "weight_q", 0, (_U8,))
-    if 2 * weight_q.shape[2] != K:
-        raise ValueError(f"the activation has K = {K}, the weight {2 * weight_q.shape[2]}")
-    _need(weight_block_scale, "weight_q's block scales", E * round_up(N, 128) * (K // 16), (_E4M3, _U8))
-    per_expert = _expert_values(alpha, "alpha", E)
-    if out is None:
-        out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
-    ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
-    if ot == 3 or (dtype is not None and out.dtype != dtype):
-        raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
-    _need(out, "out", R * N * out.element_size(), (out.dtype,))
-    if bias is not None:
-        _need(bias, "bias", E * N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
-    dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias, out), pinned=False)
+    try:
+        dev = q.get_device()
+        E, N, half = weight_q.shape
+        R, K = q.shape[0], 2 * half
+        if out is None and dev >= 0:
+            out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
+        ot = _OUT_TYPE.get(out.dtype, 3)
+        g = alpha.numel()
+        ok = (ot < 3 and q.shape[1] == half and dev >= 0 and dev == _current_device()
+              and (dtype is None or out.dtype is dtype) and _expert_packed_ok(dev, E, q, block_scale)
+              and offsets.dim() == 1 and offsets.numel() == E + 1 and _ints_ok(dev, offsets, E + 1)
+              and weight_q.dtype is _U8 and weight_q.is_contiguous() and weight_q.get_device() == dev
+              and weight_block_scale.dtype in (_E4M3, _U8) and weight_block_scale.is_contiguous()
+              and weight_block_scale.nbytes >= E * ((N + 127) // 128) * 16 * half
+              and weight_block_scale.get_device() == dev and (g == E or g == 1) and _floats_ok(dev, alpha, 1)
+              and out.is_contiguous() and out.numel() >= R * N and out.get_device() == dev
+              and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous()
+                                    and bias.numel() >= E * N and bias.get_device() == dev)))
+        per_expert = 1 if g == E else 0
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        E = _expert_count(offsets)
+        R, K = _expert_packed(q, block_scale, E)
+        if not isinstance(weight_q, torch.Tensor) or weight_q.dim() != 3 or weight_q.shape[0] != E:
+            raise ValueError(f"weight_q must be a 3-D tensor of packed codes, one matrix for each of {E} experts")
+        N = weight_q.shape[1]
+        _need(weight_q, "weight_q", 0, (_U8,))
+        if 2 * weight_q.shape[2] != K:
+            raise ValueError(f"the activation has K = {K}, the weight {2 * weight_q.shape[2]}")
+        _need(weight_block_scale, "weight_q's block scales", E * round_up(N, 128) * (K // 16), (_E4M3, _U8))
+        per_expert = _expert_values(alpha, "alpha", E)
+        if out is None:
+            out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
+        ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
+        if ot == 3 or (dtype is not None and out.dtype != dtype):
+            raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
+        _need(out, "out", R * N * out.element_size(), (out.dtype,))
+        if bias is not None:
+            _need(bias, "bias", E * N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
+        dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias, out), pinned=False)
     st = (_lib or load()).nvfp4_expert_linear(
         q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(), weight_block_scale.data_ptr(), alpha.data_ptr(),
         per_expert, None if bias is None else bias.data_ptr(), offsets.data_ptr(), E, out.data_ptr(), R, N, K, ot,
@@ -788,21 +857,36 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
     y[slots[t, j]] + add[t], in fp32, rounded once; slots below 0 add nothing.
     y (R, H) is bf16, fp16 or fp32; ``out`` (M, H) of y's type, or of any of the
     three where y is fp32; ``add`` of out's type (``out`` itself, too)."""
-    if not isinstance(y, torch.Tensor) or y.dim() != 2 or _OUT_TYPE.get(y.dtype, 3) > 2:
-        raise ValueError("y must be a 2-D bf16, fp16 or fp32 tensor")
-    _need(y, "y", 0, (y.dtype,))
-    R, H = y.shape
-    M, k = _choices(slots, "slots")
-    if out is None:
-        kw = {"device": y.device} if y.is_cuda else {"pin_memory": True}
-        out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, **kw)
-    if not isinstance(out, torch.Tensor) or _OUT_TYPE.get(out.dtype, 3) > 2:
-        raise ValueError("the output must be bf16, fp16 or fp32")
-    _need(weights, "weights", 4 * M * k, (_F32,))
-    _need(out, "out", M * H * out.element_size(), (out.dtype,) if y.dtype is _F32 else (y.dtype,))
-    if add is not None:
-        _need(add, "add", M * H * out.element_size(), (out.dtype,))
-    dev = _place((y, slots, weights, add, out))
+    try:
+        dev = y.get_device()
+        R, H = y.shape
+        M, k = slots.shape
+        if out is None and dev >= 0:
+            out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, device=y.device)
+        ok = (dev >= 0 and dev == _current_device() and y.is_contiguous() and out.dtype in _OUT_TYPE
+              and (out.dtype is y.dtype or y.dtype is _F32) and _OUT_TYPE[out.dtype] < 3 and _OUT_TYPE.get(y.dtype, 3) < 3
+              and _ints_ok(dev, slots, M * k) and _floats_ok(dev, weights, M * k)
+              and out.is_contiguous() and out.numel() >= M * H and out.get_device() == dev
+              and (add is None or (add.dtype is out.dtype and add.is_contiguous() and add.numel() >= M * H
+                                   and add.get_device() == dev)))
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        if not isinstance(y, torch.Tensor) or y.dim() != 2 or _OUT_TYPE.get(y.dtype, 3) > 2:
+            raise ValueError("y must be a 2-D bf16, fp16 or fp32 tensor")
+        _need(y, "y", 0, (y.dtype,))
+        R, H = y.shape
+        M, k = _choices(slots, "slots")
+        if out is None:
+            kw = {"device": y.device} if y.is_cuda else {"pin_memory": True}
+            out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, **kw)
+        if not isinstance(out, torch.Tensor) or _OUT_TYPE.get(out.dtype, 3) > 2:
+            raise ValueError("the output must be bf16, fp16 or fp32")
+        _need(weights, "weights", 4 * M * k, (_F32,))
+        _need(out, "out", M * H * out.element_size(), (out.dtype,) if y.dtype is _F32 else (y.dtype,))
+        if add is not None:
+            _need(add, "add", M * H * out.element_size(), (out.dtype,))
+        dev = _place((y, slots, weights, add, out))
     st = (_lib or load()).gnq_expert_combine(
         y.data_ptr(), slots.data_ptr(), weights.data_ptr(), None if add is None else add.data_ptr(), out.data_ptr(),
         R, M, H, k, _OUT_TYPE[y.dtype], _OUT_TYPE[out.dtype],

@@ -250,9 +250,7 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
 }
 
 // Whether CTA pairs take the call.
-bool pairs_take(int64_t E, int64_t R, int64_t N) {
-    return R > 64 && std::min(E, R) * ((N + 255) / 256) >= 152;
-}
+bool pairs_take(int64_t E, int64_t R, int64_t K) { return R >= 80 * E && K >= 1024; }
 
 }  // namespace
 }  // namespace gnq
@@ -302,7 +300,7 @@ extern "C" int nvfp4_expert_linear(const void *q, const void *block_scale, const
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int forced = linear_policy();
-    if (forced ? forced == 2 : pairs_take(E, R, N)) return status_of(launch_expert_linear_pair(x, q, w_q, out_type, bias_type, d->sms, s));
+    if (forced ? forced == 2 : pairs_take(E, R, K)) return status_of(launch_expert_linear_pair(x, q, w_q, out_type, bias_type, d->sms, s));
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
     p.T = R <= 32 ? 32 : R <= 64 ? 64 : 128;
     p.tmem_cols = p.T == 32 ? 128 : p.T == 64 ? 256 : 512;  // two tiles' sums and the scales

@@ -8,12 +8,17 @@
 //   slots[t, j]    row of (t, j) in expert order: by expert, then by token
 //   offsets[e]     first row of expert e
 //
-// Two steps.  A warp per token picks and weighs.  Then the M k choices are
-// placed by counting: each warp counts a contiguous stretch of them in its own
-// histogram, a prefix over warps, CTAs of a cluster and experts gives every
-// warp the first row of its choices of each expert, and a second pass over
-// the same stretch places them.  No atomics: the rows of an expert are in
-// token order whatever the timing.
+// A warp per token picks and weighs.  The M k choices are then placed by
+// counting, without atomics on memory: an expert's rows are in token order
+// whatever the timing.  Up to 4096 choices one CTA does it: each warp counts a
+// contiguous stretch in a histogram of its own, a prefix over warps and
+// experts gives its first row of each expert.  More are cut into chunks of
+// tokens: the CTA that picks a chunk leaves its counts in the slots that the
+// chunk will have (it has at least as many choices as there are experts), a
+// cluster turns them into first rows, an expert's slice per CTA, and a CTA per
+// chunk places its choices as above.
+#include <algorithm>
+
 #include "gemma_nq.h"
 #include "gnq_expert.cuh"
 #include "gnq_host.cuh"
@@ -33,209 +38,428 @@ struct RouteParams {
     float *weights;
 };
 
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order_key(-inf)
-
-// Unsigned order of fp32 values: equal zeros, NaN above all.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);  // -0 -> +0
-    if (v != v) return 0xFFFFFFFFu;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(uint32_t key) {  // of a key that is not NaN's
-    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
-}
-
-template <typename L> __device__ __forceinline__ float load_logit(const void *p, int64_t i);
-template <> __device__ __forceinline__ float load_logit<float>(const void *p, int64_t i) {
-    return ld_f32(static_cast<const float *>(p) + i);
-}
-template <> __device__ __forceinline__ float load_logit<__nv_bfloat16>(const void *p, int64_t i) {
-    return __uint_as_float((uint32_t)ld_u16(static_cast<const uint16_t *>(p) + i) << 16);
-}
-template <> __device__ __forceinline__ float load_logit<__half>(const void *p, int64_t i) {
-    return __half2float(__ushort_as_half(ld_u16(static_cast<const uint16_t *>(p) + i)));
-}
-
-// One token by one warp; lane l holds the logits of experts l, l + 32, ...
-template <typename L, int NV> __device__ __forceinline__ void pick_token(const RouteParams &p, int t, int lane) {
-    uint32_t key[NV];
-    const int64_t row = (int64_t)t * p.row_stride;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = 32 * i + lane;
-        key[i] = e < p.E ? order_key(load_logit<L>(p.logits, row + e)) : 0u;
+// Unsigned order of a type's values, in the upper bits of a word: equal zeros,
+// NaN above all.  The inverse gives a NaN for NaN's key.
+template <typename L> struct Logit;
+template <> struct Logit<float> {
+    static constexpr uint32_t kNegInf = 0x007FFFFFu;
+    static __device__ __forceinline__ uint32_t key(uint32_t b) {
+        const float v = __uint_as_float(b) + 0.f;  // -0 -> +0
+        if (v != v) return 0xFFFFFFFFu;
+        b = __float_as_uint(v);
+        return b & 0x80000000u ? ~b : b | 0x80000000u;
     }
-    auto value = [&](uint32_t u) { return u == 0xFFFFFFFFu ? __int_as_float(0x7FC00000) : key_value(u); };
-    uint32_t all[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) all[i] = key[i];
+    static __device__ __forceinline__ float value(uint32_t key) {
+        return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+    }
+};
+template <typename L, uint32_t INF> struct Logit16 {
+    static constexpr uint32_t kNegInf = (0xFFFFu - (INF | 0x8000u)) << 16;
+    static __device__ __forceinline__ uint32_t key(uint32_t b) {
+        if ((b & 0x7FFFu) > INF) return 0xFFFF0000u;
+        if (b == 0x8000u) b = 0;
+        return (b & 0x8000u ? 0xFFFFu - b : b | 0x8000u) << 16;
+    }
+    static __device__ __forceinline__ uint16_t bits(uint32_t key) {
+        key >>= 16;
+        return (uint16_t)(key & 0x8000u ? key & 0x7FFFu : 0xFFFFu - key);
+    }
+};
+template <> struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16, 0x7F80u> {
+    static __device__ __forceinline__ float value(uint32_t key) { return __uint_as_float((uint32_t)bits(key) << 16); }
+};
+template <> struct Logit<__half> : Logit16<__half, 0x7C00u> {
+    static __device__ __forceinline__ float value(uint32_t key) { return __half2float(__ushort_as_half(bits(key))); }
+};
 
+// A logit's key and its expert.  16-bit logits carry the expert in the low half
+// of the word (all ones less its index: ties go to the lowest), so that one
+// comparison orders both and a maximum names the expert; fp32 ones beside it.
+template <typename L> struct Ranked {
+    uint32_t v;
+    static constexpr uint32_t kNone = Logit<L>::kNegInf | 0xFFFFu;  // up to here: -inf, or no expert
+    __device__ __forceinline__ void set(uint32_t key, int e) { v = key | (0xFFFFu - e); }
+    __device__ __forceinline__ void clear() { v = 0; }
+    __device__ __forceinline__ bool is(uint32_t top, int) const { return v == top; }
+    static __device__ __forceinline__ void order(Ranked &a, Ranked &b) {
+        const uint32_t m = max(a.v, b.v);
+        b.v = min(a.v, b.v);
+        a.v = m;
+    }
+    __device__ __forceinline__ int expert(uint32_t top) const { return 0xFFFF - (int)(top & 0xFFFFu); }
+};
+template <> struct Ranked<float> {
+    uint32_t v;
+    uint32_t e;
+    static constexpr uint32_t kNone = Logit<float>::kNegInf;
+    __device__ __forceinline__ void set(uint32_t key, int expert) { v = key, e = expert; }
+    __device__ __forceinline__ void clear() { v = 0, e = 0x7FFFFFFF; }
+    __device__ __forceinline__ bool is(uint32_t top, int expert) const { return v == top && e == (uint32_t)expert; }
+    static __device__ __forceinline__ void order(Ranked &a, Ranked &b) {
+        const bool swap = b.v > a.v || (b.v == a.v && b.e < a.e);
+        const Ranked t = a;
+        a.v = swap ? b.v : a.v, a.e = swap ? b.e : a.e;
+        b.v = swap ? t.v : b.v, b.e = swap ? t.e : b.e;
+    }
+    __device__ __forceinline__ int expert(uint32_t top) const {
+        return (int)__reduce_min_sync(0xffffffffu, v == top ? e : 0x7FFFFFFFu);
+    }
+};
+
+// Bits of a lane's logits: experts lane * NV + i in wide loads (WIDE: E = 32 NV,
+// rows 16-byte aligned), else 32 i + lane, 0 behind the last.
+template <typename L, int NV, bool WIDE>
+__device__ __forceinline__ void load_logits(const RouteParams &p, int t, int lane, uint32_t (&b)[NV]) {
+    constexpr int S = sizeof(L), BYTES = NV * S;
+    const uint8_t *row = static_cast<const uint8_t *>(p.logits) + (int64_t)t * p.row_stride * S;
+    if constexpr (WIDE && BYTES >= 4) {
+        uint32_t w[BYTES / 4];
+        const uint8_t *at = row + lane * BYTES;
+        if constexpr (BYTES >= 16) {
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i) {
+                const uint4 v = ld_stream(at + 16 * i);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < BYTES / 4; ++i) w[i] = __float_as_uint(ld_f32(reinterpret_cast<const float *>(at) + i));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) b[i] = S == 4 ? w[i] : (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = WIDE ? lane * NV + i : 32 * i + lane;
+            b[i] = 0;
+            if (e < p.E) {
+                if constexpr (S == 4) b[i] = __float_as_uint(ld_f32(reinterpret_cast<const float *>(row) + e));
+                else b[i] = ld_u16(row + 2 * e);
+            }
+        }
+    }
+}
+
+// One token by one warp.  Up to eight logits a lane are put in falling order
+// (Batcher's merge exchange), so that a choice is a maximum over the lanes'
+// first ones and a step in one lane; more are searched at each choice.  Returns
+// the lane-th choice (-1: none).
+template <typename L, int NV, bool WIDE> __device__ __forceinline__ int pick_token(const RouteParams &p, int t, int lane) {
+    constexpr bool SORT = NV <= 8;
+    Ranked<L> r[NV];
+    {
+        uint32_t b[NV];
+        load_logits<L, NV, WIDE>(p, t, lane, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = WIDE ? lane * NV + i : 32 * i + lane;
+            if (WIDE || e < p.E) r[i].set(Logit<L>::key(b[i]), e);
+            else r[i].clear();
+        }
+    }
+    if constexpr (SORT) {
+#pragma unroll
+        for (int q = 1; q < NV; q *= 2)
+#pragma unroll
+            for (int d = q; d >= 1; d /= 2)
+#pragma unroll
+                for (int i = d % q; i + d < NV; i += 2 * d)
+#pragma unroll
+                    for (int c = 0; c < d; ++c)
+                        if (i + c + d < NV && (i + c) / (2 * q) == (i + c + d) / (2 * q))
+                            Ranked<L>::order(r[i + c], r[i + c + d]);
+    }
+    auto first = [&] {
+        Ranked<L> h = r[0];
+        if constexpr (!SORT) {
+#pragma unroll
+            for (int i = 1; i < NV; ++i) {
+                Ranked<L> o = r[i];
+                Ranked<L>::order(h, o);
+            }
+        }
+        return h;
+    };
+
+    Ranked<L> head = first();
+    uint32_t top = __reduce_max_sync(0xffffffffu, head.v);
+    const float peak = Logit<L>::value(top);
+    float part = 0.f;
+    if (!p.renormalize && top > Ranked<L>::kNone) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (r[i].v != 0) part += expf(Logit<L>::value(r[i].v) - peak);
+    }
     // lane j keeps the j-th choice
     uint32_t mine = 0;
     int choice = -1;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > best) best = key[i], at = i;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top <= kKeyNegInf) break;
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(32 * at + lane) : 0x7FFFFFFFu);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (e == 32 * i + lane) key[i] = 0;
+    for (int j = 0; top > Ranked<L>::kNone;) {
+        const int e = head.expert(top);
         if (lane == j) mine = top, choice = e;
-    }
-    const uint32_t first = __shfl_sync(0xffffffffu, mine, 0);
-    float w = 0.f;
-    if (first != 0) {  // (warp-uniform)
-        const float peak = value(first);
-        w = choice >= 0 ? expf(value(mine) - peak) : 0.f;
-        float part = w;
-        if (!p.renormalize) {
-            part = 0.f;
+        if (++j == p.k) break;
+        if constexpr (SORT) {
+            const bool step = head.is(top, e);
+#pragma unroll
+            for (int i = 0; i + 1 < NV; ++i)
+                if (step) r[i] = r[i + 1];
+            if (step) r[NV - 1].clear();
+        } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (all[i] > 0) part += expf(value(all[i]) - peak);
+                if (r[i].is(top, e)) r[i].clear();
         }
-        const float total = warp_sum(part);
-        if (choice >= 0) w = __fmul_rn(__fdiv_rn(w, total), p.scale);
+        head = first();
+        top = __reduce_max_sync(0xffffffffu, head.v);
     }
+    float w = choice >= 0 ? expf(Logit<L>::value(mine) - peak) : 0.f;
+    const float total = warp_sum(p.renormalize ? w : part);
+    if (choice >= 0) w = __fmul_rn(__fdiv_rn(w, total), p.scale);
     if (lane < p.k) {
         const int64_t at = (int64_t)t * p.k + lane;
         p.experts[at] = choice;
         p.weights[at] = w;
     }
+    return choice;
 }
 
-// Rows of the M k choices, by a cluster of CTAs (or one) of 1024 threads.
-// hist: per warp and expert; totals: per CTA and expert.
-__device__ __forceinline__ void place_choices(const RouteParams &p, int32_t *hist, int32_t *totals, int32_t *sums) {
-    constexpr int W = 32;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const uint32_t C = cluster_size(), rank = C > 1 ? cluster_rank() : 0;
-    const int64_t n = (int64_t)p.M * p.k;
-    const int64_t per = ((n + C * W - 1) / (C * W) + 31) / 32 * 32;
-    const int64_t begin = min(n, (int64_t)(rank * W + warp) * per), end = min(n, begin + per);
-    int32_t *const h = hist + warp * p.E;
+constexpr int kKeep = 4;        // groups of 32 choices whose place a warp keeps in registers
+constexpr int kSmallTokens = 64;       // up to here one launch
+constexpr int kOneCta = 32 * 32 * kKeep;  // choices that one CTA places
+constexpr int kScanCtas = 8;
 
-    for (int i = t; i < W * p.E; i += 1024) hist[i] = 0;
+// Choices begin .. end - 1 by one CTA: the place of each among those of its
+// expert, plus first(expert).  hist: E words per warp.  `first` is called by
+// thread e for expert e (at least E threads) with the expert's count, by all
+// threads together.
+template <typename First>
+__device__ __forceinline__ void place_choices(const RouteParams &p, int begin, int end, int32_t *hist, const First &first) {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, W = blockDim.x >> 5;
+    const int per = ((end - begin + W - 1) / W + 31) / 32 * 32;  // choices of a warp
+    const int busy = per ? (end - begin + per - 1) / per : 0;    // warps that have some
+    const int from = min(end, begin + warp * per), to = min(end, from + per);
+    int32_t *const h = hist + warp * p.E;
+    for (int i = t; i < busy * p.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     const uint32_t below = (1u << lane) - 1;
-    // place < 0: counts; else hands out rows
-    auto pass = [&](bool place) {
-        for (int64_t i = begin + lane; i - lane < end; i += 32) {
-            const int e = i < end ? p.experts[i] : -1;
-            const uint32_t peers = __match_any_sync(0xffffffffu, e);
-            const int before = __popc(peers & below);
-            int row = -1;
-            if (e >= 0) row = h[e] + before;
-            __syncwarp();
-            if (e >= 0 && before == 0) h[e] += __popc(peers);
-            __syncwarp();
-            if (place && i < end) p.slots[i] = row;
+    int e[kKeep], at[kKeep];
+    auto read = [&](int base) {
+#pragma unroll
+        for (int g = 0; g < kKeep; ++g) {
+            const int i = base + 32 * g + lane;
+            e[g] = i < to ? p.experts[i] : -1;
         }
     };
-    pass(false);
+    const bool kept = per <= 32 * kKeep;  // else the places wait in the slots
+    for (int base = from; base < to; base += 32 * kKeep) {
+        read(base);
+#pragma unroll
+        for (int g = 0; g < kKeep; ++g) {
+            if (base + 32 * g >= to) break;
+            const uint32_t peers = __match_any_sync(0xffffffffu, e[g]);
+            const int before = __popc(peers & below);
+            at[g] = e[g] >= 0 ? h[e[g]] + before : 0;
+            __syncwarp();
+            if (e[g] >= 0 && before == 0) h[e[g]] = at[g] + __popc(peers);
+            __syncwarp();
+            if (!kept && base + 32 * g + lane < to) p.slots[base + 32 * g + lane] = at[g];
+        }
+    }
     __syncthreads();
     // counts -> prefix over the warps; one expert per thread
     int total = 0;
     if (t < p.E)
-        for (int w = 0; w < W; ++w) {
+        for (int w = 0; w < busy; ++w) {
             const int c = hist[w * p.E + t];
             hist[w * p.E + t] = total;
             total += c;
         }
-    int before = 0;
-    if (C > 1) {
-        cluster_wait();  // every CTA exists
-        if (t < p.E)
-            for (uint32_t r = 0; r < C; ++r)
-                st_cluster_u32(map_to_cta((uint32_t)__cvta_generic_to_shared(totals + rank * p.E + t), r), (uint32_t)total);
-        cluster_arrive_release();
-        cluster_wait();
-        if (t < p.E) {
-            total = 0;
-            for (uint32_t r = 0; r < C; ++r) {
-                const int c = totals[r * p.E + t];
-                if (r < rank) before += c;
-                total += c;
-            }
+    const int row = first(total);
+    if (t < p.E)
+        for (int w = 0; w < busy; ++w) hist[w * p.E + t] += row;
+    __syncthreads();
+    for (int base = from; base < to; base += 32 * kKeep) {
+        if (!kept) read(base);
+#pragma unroll
+        for (int g = 0; g < kKeep; ++g) {
+            const int i = base + 32 * g + lane;
+            if (i < to) p.slots[i] = e[g] < 0 ? -1 : h[e[g]] + (kept ? at[g] : p.slots[i]);
         }
     }
-    // prefix over the experts
-    int sum = total;
+}
+
+// Sum of `v` over the threads before this one (of at most 1024), and over all.
+__device__ __forceinline__ int prefix(int v, int32_t *sums, int &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    int sum = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += sums[w];
-    const int offset = base + sum - total;
-    if (t < p.E) {
-        for (int w = 0; w < W; ++w) hist[w * p.E + t] += offset + before;
-        if (rank == 0) {
-            p.offsets[t] = offset;
-            if (t == p.E - 1) p.offsets[p.E] = offset + total;
+    const int u = lane < W ? sums[lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, u);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? u : 0) + sum - v;
+}
+
+// All choices by one CTA, offsets included.
+__device__ __forceinline__ void place_all(const RouteParams &p, int32_t *hist, int32_t *sums) {
+    place_choices(p, 0, p.M * p.k, hist, [&](int total) {
+        int all;
+        const int row = prefix(total, sums, all), t = threadIdx.x;
+        if (t < p.E) p.offsets[t] = row;
+        if (t == 0) p.offsets[p.E] = all;
+        return row;
+    });
+}
+
+// Few tokens: everything in one CTA.
+template <typename L, int NV, bool WIDE>
+__global__ void __launch_bounds__(1024) route_small_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ int32_t counts[];
+    __shared__ int32_t sums[32];
+    pdl_wait();
+    pdl_trigger();
+    const int W = blockDim.x >> 5;
+    for (int t = threadIdx.x >> 5; t < p.M; t += W) pick_token<L, NV, WIDE>(p, t, threadIdx.x & 31);
+    __syncthreads();
+    place_all(p, counts, sums);
+}
+
+__global__ void __launch_bounds__(1024) route_place_all_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ int32_t counts[];
+    __shared__ int32_t sums[32];
+    pdl_wait();
+    pdl_trigger();
+    place_all(p, counts, sums);
+}
+
+// The choices of `chunk` tokens (the last chunk: of what is left, less than
+// twice as many), and their counts where the chunk's slots will be (chunks > 0).
+template <typename L, int NV, bool WIDE>
+__global__ void __launch_bounds__(1024) route_pick_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks) {
+    extern __shared__ int32_t counts[];
+    pdl_wait();
+    pdl_trigger();
+    const int t = threadIdx.x, lane = t & 31, W = blockDim.x >> 5;
+    const int begin = blockIdx.x * chunk, end = (int)blockIdx.x + 1 < (int)gridDim.x ? begin + chunk : p.M;
+    if (chunks) {
+        for (int i = t; i < p.E; i += blockDim.x) counts[i] = 0;
+        __syncthreads();
+    }
+    for (int m = begin + (t >> 5); m < end; m += W) {
+        const int choice = pick_token<L, NV, WIDE>(p, m, lane);
+        if (chunks && choice >= 0) atomicAdd(&counts[choice], 1);
+    }
+    if (!chunks) return;
+    __syncthreads();
+    for (int i = t; i < p.E; i += blockDim.x) p.slots[(int64_t)begin * p.k + i] = counts[i];
+}
+
+// Counts of the chunks -> first row of each chunk and expert, and the offsets.
+// A cluster: each CTA takes a slice of the experts, `slice` of them (a power of
+// two up to 128), its threads the slice side by side and the chunks in
+// stretches.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks, int slice) {
+    __shared__ int32_t part[1024], sums[32];
+    __shared__ int32_t totals[kScanCtas];
+    const int rank = (int)cluster_rank(), t = threadIdx.x;
+    cluster_arrive_relaxed();
+    pdl_wait();
+    pdl_trigger();
+    const int e = rank * slice + t % slice, stretch = t / slice, stretches = min(32, 1024 / slice);
+    const int per = (chunks + stretches - 1) / stretches;
+    const int from = min(chunks, stretch * per), to = min(chunks, from + per);
+    int32_t *const table = p.slots + e;
+    const int64_t step = (int64_t)chunk * p.k;
+    int sum = 0;
+    if (e < p.E)
+        for (int c = from; c < to; ++c) sum += table[c * step];
+    part[t] = sum;
+    __syncthreads();
+    // first stretch: the expert's total; every stretch: what comes before it
+    int total = 0, before = 0;
+    for (int i = 0; i < stretches; ++i) {
+        const int v = part[i * slice + t % slice];
+        if (i < stretch) before += v;
+        total += v;
+    }
+    int all;
+    const int within = prefix(t < slice ? total : 0, sums, all);
+    cluster_wait();  // every CTA exists
+    if (t < kScanCtas) st_cluster_u32(map_to_cta((uint32_t)__cvta_generic_to_shared(&totals[rank]), t), (uint32_t)all);
+    if (t < slice) part[t] = within;
+    cluster_arrive_release();
+    cluster_wait();
+    int slices = 0, rows = 0;
+    for (int i = 0; i < kScanCtas; ++i) {
+        if (i < rank) slices += totals[i];
+        rows += totals[i];
+    }
+    const int first = slices + part[t % slice];
+    if (t < slice && e < p.E) p.offsets[e] = first;
+    if (rank == 0 && t == 0) p.offsets[p.E] = rows;
+    if (e < p.E) {
+        int row = first + before;
+        for (int c = from; c < to; ++c) {
+            const int v = table[c * step];
+            table[c * step] = row;
+            row += v;
         }
     }
-    __syncthreads();
-    pass(true);
 }
 
-template <typename L, int NV> __global__ void __launch_bounds__(256) route_pick_kernel(const __grid_constant__ RouteParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (t < p.M) pick_token<L, NV>(p, t, threadIdx.x & 31);
-}
-
-__global__ void __launch_bounds__(1024) route_place_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(1024) route_place_kernel(const __grid_constant__ RouteParams p, int chunk) {
     extern __shared__ int32_t counts[];
-    __shared__ int32_t sums[32];
-    if (cluster_size() > 1) cluster_arrive_relaxed();
     pdl_wait();
     pdl_trigger();
-    place_choices(p, counts, counts + 32 * p.E, sums);
-}
-
-// Both steps in one CTA.
-template <typename L, int NV> __global__ void __launch_bounds__(1024) route_small_kernel(const __grid_constant__ RouteParams p) {
-    extern __shared__ int32_t counts[];
-    __shared__ int32_t sums[32];
-    pdl_wait();
-    pdl_trigger();
-    for (int t = threadIdx.x >> 5; t < p.M; t += 32) pick_token<L, NV>(p, t, threadIdx.x & 31);
+    const int begin = blockIdx.x * chunk, end = (int)blockIdx.x + 1 < (int)gridDim.x ? begin + chunk : p.M;
+    // read before any of the chunk's slots is written (place_choices writes
+    // them behind its barriers, or provisional places behind the one here)
+    const int row = (int)threadIdx.x < p.E ? p.slots[(int64_t)begin * p.k + threadIdx.x] : 0;
     __syncthreads();
-    place_choices(p, counts, nullptr, sums);
+    place_choices(p, begin * p.k, end * p.k, counts, [&](int) { return row; });
 }
 
-constexpr int kPlaceCluster = 8;
-
-template <typename L, int NV> cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
-    const size_t hist = (size_t)32 * p.E * 4;
-    if (p.M <= 64) {
-        auto fn = route_small_kernel<L, NV>;
+template <typename L, int NV, bool WIDE> cudaError_t launch_route_form(const RouteParams &p, int sms, cudaStream_t s) {
+    const int hist = (p.E + 31) / 32;  // warps that hold a thread per expert
+    auto one_cta = [&](auto fn, int warps) {
         const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
-        return e != cudaSuccess ? e : launch(fn, 1, 1024, hist, 1, s, p);
+        return e != cudaSuccess ? e : launch(fn, 1, 32 * warps, (size_t)warps * p.E * 4, 1, s, p);
+    };
+    if (p.M <= kSmallTokens) return one_cta(route_small_kernel<L, NV, WIDE>, std::max(hist, std::min(p.M, 32)));
+    const int n = p.M * p.k;
+    cudaError_t e;
+    auto pick = route_pick_kernel<L, NV, WIDE>;
+    if (n <= kOneCta) {
+        if ((e = launch(pick, (p.M + 7) / 8, 256, 0, 1, s, p, 8, 0)) != cudaSuccess) return e;
+        return one_cta(route_place_all_kernel, 32);
     }
-    cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(route_place_kernel));
-    if (e != cudaSuccess) return e;
-    if ((e = launch(route_pick_kernel<L, NV>, (p.M + 7) / 8, 256, 0, 1, s, p)) != cudaSuccess) return e;
-    return launch(route_place_kernel, kPlaceCluster, 1024, hist + (size_t)kPlaceCluster * p.E * 4, kPlaceCluster, s, p);
+    // two chunks per SM; a chunk has a choice at least for every expert
+    const int chunk = std::max((p.E + p.k - 1) / p.k, (p.M + 2 * sms - 1) / (2 * sms)), chunks = p.M / chunk;
+    int slice = 1;
+    while (slice * kScanCtas < p.E) slice *= 2;
+    if ((e = launch(pick, chunks, 1024, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
+    if ((e = launch(route_scan_kernel, kScanCtas, 1024, 0, kScanCtas, s, p, chunk, chunks, slice)) != cudaSuccess) return e;
+    const int warps = std::max(hist, 8);
+    if ((e = opt_in_dynamic_smem(reinterpret_cast<const void *>(route_place_kernel))) != cudaSuccess) return e;
+    return launch(route_place_kernel, chunks, 32 * warps, (size_t)warps * p.E * 4, 1, s, p, chunk);
 }
 
-template <typename L> cudaError_t launch_route_experts(const RouteParams &p, cudaStream_t s) {
-    if (p.E <= 32) return launch_route<L, 1>(p, s);
-    if (p.E <= 64) return launch_route<L, 2>(p, s);
-    if (p.E <= 128) return launch_route<L, 4>(p, s);
-    if (p.E <= 256) return launch_route<L, 8>(p, s);
-    if (p.E <= 512) return launch_route<L, 16>(p, s);
-    return launch_route<L, 32>(p, s);
+template <typename L, int NV> cudaError_t launch_route(const RouteParams &p, int sms, cudaStream_t s) {
+    if (p.E == 32 * NV && aligned(p.logits, 16) && p.row_stride * sizeof(L) % 16 == 0)
+        return launch_route_form<L, NV, true>(p, sms, s);
+    return launch_route_form<L, NV, false>(p, sms, s);
+}
+
+template <typename L> cudaError_t launch_route_experts(const RouteParams &p, int sms, cudaStream_t s) {
+    if (p.E <= 32) return launch_route<L, 1>(p, sms, s);
+    if (p.E <= 64) return launch_route<L, 2>(p, sms, s);
+    if (p.E <= 128) return launch_route<L, 4>(p, sms, s);
+    if (p.E <= 256) return launch_route<L, 8>(p, sms, s);
+    if (p.E <= 512) return launch_route<L, 16>(p, sms, s);
+    return launch_route<L, 32>(p, sms, s);
 }
 
 }  // namespace
@@ -247,7 +471,7 @@ extern "C" int gnq_expert_route(const void *logits, int64_t row_stride, int logi
     using namespace gnq;
     if (logits_type < GNQ_BF16 || logits_type > GNQ_FP32) return GNQ_ERR_DTYPE;
     if (E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK || k > E) return GNQ_ERR_SHAPE;
-    if (M < 0 || M > kMaxM || M * k > 0x7FFFFFFF) return GNQ_ERR_SHAPE;
+    if (M < 0 || M > kMaxM || M * k > 0x7FFF0000) return GNQ_ERR_SHAPE;
     const int64_t size = logits_type == GNQ_FP32 ? 4 : 2;
     if (row_stride < E || row_stride > (int64_t)1 << 32) return GNQ_ERR_ALIGN;
     if (!offsets || (M > 0 && (!logits || !experts || !weights || !slots))) return GNQ_ERR_NULL;
@@ -257,6 +481,8 @@ extern "C" int gnq_expert_route(const void *logits, int64_t row_stride, int logi
                               extent(offsets, 4 * (E + 1))};
     const Extent read[] = {{logits, M, size * row_stride, size * E}};
     if (outputs_meet(written, read)) return GNQ_ERR_ALIAS;
+    const DevInfo *d = dev_info();
+    if (!d) return GNQ_ERR_CUDA;
     RouteParams p = {};
     p.logits = logits;
     p.row_stride = row_stride;
@@ -270,7 +496,7 @@ extern "C" int gnq_expert_route(const void *logits, int64_t row_stride, int logi
     p.offsets = offsets;
     p.slots = slots;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (logits_type == GNQ_BF16) return status_of(launch_route_experts<__nv_bfloat16>(p, s));
-    if (logits_type == GNQ_FP16) return status_of(launch_route_experts<__half>(p, s));
-    return status_of(launch_route_experts<float>(p, s));
+    if (logits_type == GNQ_BF16) return status_of(launch_route_experts<__nv_bfloat16>(p, d->sms, s));
+    if (logits_type == GNQ_FP16) return status_of(launch_route_experts<__half>(p, d->sms, s));
+    return status_of(launch_route_experts<float>(p, d->sms, s));
 }

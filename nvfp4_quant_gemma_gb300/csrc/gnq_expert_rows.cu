@@ -61,26 +61,49 @@ struct ExpertQuantParams {
     int H, upr;     // elements and units of a row
 };
 
-// The block's codes and scale byte for global scale g: the steps of
-// epilogue_unit.
-template <typename T>
-__device__ __forceinline__ void nvfp4_block(const uint4 (&y)[2], float sixth, float g, uint32_t &lo, uint32_t &hi,
-                                            uint32_t &sf) {
-    float v[16];
+// RN(g / v) for the value v of a block scale, from v and RN(1 / v) of a table in
+// shared memory (0 for v = 0: then 1 / v counts as 0): the correction step of
+// div_fma, exact for these g; other g divide.
+__device__ __forceinline__ bool quotient_table_serves(float g) { return g >= 0x1p-100f && g <= 0x1p100f; }
+__device__ __forceinline__ void fill_reciprocals(float2 (&tab)[128], int t) {
+    if (t < 128) {
+        const float v = e4m3_value(t);
+        tab[t] = make_float2(v, t ? __frcp_rn(v) : 0.f);
+    }
+    __syncthreads();
+}
+
+// The codes and scale byte of a block `v` with amax / 6 = sixth for global
+// scale g: the steps of epilogue_unit.  TABLE: worth its filling where a thread
+// takes several quotients (SiLU of 16384 x 2048 in expert order, one each: 31.4
+// us without, 34.0 with it).
+template <bool TABLE>
+__device__ __forceinline__ void nvfp4_block(const float (&v)[16], float sixth, float g, const float2 *tab, uint32_t &lo,
+                                            uint32_t &hi, uint32_t &sf) {
     sf = e4m3x2(__fmul_rn(g, sixth), 0.f) & 0xFF;
-    Act<T>::unpack(y[0], &v[0]);
-    Act<T>::unpack(y[1], &v[8]);
-    mul_arr_s<16>(v, element_scale(g, sf));
-    lo = e2m1x8(&v[0]);
-    hi = e2m1x8(&v[8]);
+    float es, q0;
+    if (TABLE && quotient_table_serves(g)) {
+        const float2 r = tab[sf & 0x7F];
+        es = div_fma(g, r.x, r.y, q0);
+    } else {
+        es = element_scale(g, sf);
+    }
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = v[i];
+    mul_arr_s<16>(x, es);
+    lo = e2m1x8(&x[0]);
+    hi = e2m1x8(&x[8]);
 }
 
 template <typename T, int ACT, bool FAN, bool V8>
 __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant__ ExpertQuantParams p) {
+    __shared__ float2 tab[128];
     const int lane = threadIdx.x & 31;
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
     const bool ok = at < p.units;
     const int m = ok ? (int)(at / p.upr) : 0, col = ok ? (int)(at - (int64_t)m * p.upr) * 16 : 0;
+    if (FAN) fill_reciprocals(tab, threadIdx.x);
     pdl_wait();
     pdl_trigger();
     const uint16_t *src = p.in + m * p.row_stride + col;
@@ -104,26 +127,50 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
         }
     }
     const float sixth = div6(absmax16<T>(y[0], y[1]));
+    float v[16];
+    Act<T>::unpack(y[0], &v[0]);
+    Act<T>::unpack(y[1], &v[8]);
     const int Kp4 = p.upr >> 2;
+    uint8_t *const codes = p.q + (col >> 1), *const scales = p.block_scale + sf_col_offset(col);
     uint32_t lo, hi, sf;
-    auto store = [&](int row, int e, int o) {
-        st_v2(p.q + (int64_t)row * (p.H >> 1) + (col >> 1), lo, hi);
-        st_u8(p.block_scale + expert_scale_row(e, o, row - o, Kp4) + sf_col_offset(col), sf);
-    };
     if constexpr (FAN) {
-        if (!ok) return;
-        if (p.x.scale_stride == 0) nvfp4_block<T>(y, sixth, ld_f32(p.x.scale), lo, hi, sf);
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t tj = (int64_t)m * p.k + j;
-            const int row = ld_i32(p.slots + tj), e = ld_i32(p.experts + tj);
-            if (row < 0) continue;
-            const int o = (unsigned)e < (unsigned)p.x.E ? row_bound(p.x.offsets, e, p.x.R) : p.x.R;
-            if (row < o || row >= row_bound(p.x.offsets, min(max(e, 0), p.x.E - 1) + 1, p.x.R)) {
-                atomicOr(p.x.err, (unsigned)DEVERR_BAD_ROW);
-                continue;
+        // The choices of a token by the lanes of the warp, one each, so that
+        // their reads run side by side; then all units of the token in this
+        // warp take them in turn.  A warp holds one token, or parts of a few.
+        const bool shared = p.x.scale_stride == 0;
+        if (shared) nvfp4_block<true>(v, sixth, ld_f32(p.x.scale), tab, lo, hi, sf);
+        uint32_t left = __ballot_sync(0xffffffffu, ok);
+        while (left) {
+            const int token = __shfl_sync(0xffffffffu, m, __ffs(left) - 1);
+            int row = -1;
+            float g = 0.f;
+            int64_t sf_row = 0;
+            if (lane < p.k) {
+                const int64_t tj = (int64_t)token * p.k + lane;
+                const int e = ld_i32(p.experts + tj);
+                row = ld_i32(p.slots + tj);
+                const bool known = (unsigned)e < (unsigned)p.x.E;
+                const int at = known ? e : 0;
+                const int o = row_bound(p.x.offsets, at, p.x.R), to = row_bound(p.x.offsets, at + 1, p.x.R);
+                if (!shared) g = ld_f32(p.x.scale + at);
+                if (row >= 0 && (!known || row < o || row >= to)) {
+                    atomicOr(p.x.err, (unsigned)DEVERR_BAD_ROW);
+                    row = -1;
+                }
+                sf_row = expert_scale_row(at, o, row - o, Kp4);
             }
-            if (p.x.scale_stride) nvfp4_block<T>(y, sixth, ld_f32(p.x.scale + e), lo, hi, sf);
-            store(row, e, o);
+            const bool mine = ok && m == token;
+            for (uint32_t live = __ballot_sync(0xffffffffu, row >= 0); live; live &= live - 1) {
+                const int j = __ffs(live) - 1;
+                const int rj = __shfl_sync(0xffffffffu, row, j);
+                const int64_t sj = __shfl_sync(0xffffffffu, sf_row, j);
+                const float gj = __shfl_sync(0xffffffffu, g, j);
+                if (!mine) continue;
+                if (!shared) nvfp4_block<true>(v, sixth, gj, tab, lo, hi, sf);
+                st_v2(codes + (int64_t)rj * (p.H >> 1), lo, hi);
+                st_u8(scales + sj, sf);
+            }
+            left &= ~__ballot_sync(0xffffffffu, mine);
         }
     } else {
         // one search for the warp, from there each lane by itself
@@ -131,8 +178,9 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
         if (!ok) return;
         e = expert_from(p.x, e, m, o);
         if (e == p.x.E) return;
-        nvfp4_block<T>(y, sixth, ld_f32(p.x.scale + e * p.x.scale_stride), lo, hi, sf);
-        store(m, e, o);
+        nvfp4_block<false>(v, sixth, ld_f32(p.x.scale + e * p.x.scale_stride), tab, lo, hi, sf);
+        st_v2(codes + (int64_t)m * (p.H >> 1), lo, hi);
+        st_u8(scales + expert_scale_row(e, o, m - o, Kp4), sf);
     }
 }
 
@@ -229,9 +277,10 @@ template <> struct Row8<float> {
     }
 };
 
-// Y: type of the rows, O: of `add` and the result.  Sums in fp32, in the order
-// of j, `add` last, one rounding.
-template <typename Y, typename O>
+// Y: type of the rows, O: of `add` and the result.  Sums in fp32, `add` last,
+// one rounding.
+// G: rows on their way at a time.
+template <typename Y, typename O, int G>
 __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constant__ CombineParams p) {
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
     if (at >= p.units) return;
@@ -240,18 +289,46 @@ __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constan
     pdl_wait();
     pdl_trigger();
     float acc[8] = {};
-    for (int j = 0; j < p.k; ++j) {
-        const int row = ld_i32(p.slots + t * p.k + j);
-        if (row < 0) continue;
-        if (row >= p.R) {
-            atomicOr(p.err, (unsigned)DEVERR_BAD_ROW);
-            continue;
-        }
-        const float w = ld_f32(p.weights + t * p.k + j);
-        float f[8];
-        Row8<Y>::unpack(Row8<Y>::load(p.y, (int64_t)row * p.H + col), f);
+    const int32_t *const slots = p.slots + t * p.k;
+    const float *const weights = p.weights + t * p.k;
+    for (int j0 = 0; j0 < p.k; j0 += G) {
+        // G rows on their way at a time, added as a tree: fewer roundings of
+        // large sums than one by one, and a shorter chain.
+        int row[G];
+        float w[G];
+        typename Row8<Y>::Raw raw[G];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+        for (int j = 0; j < G; ++j) {
+            row[j] = j0 + j < p.k ? ld_i32(slots + j0 + j) : -1;
+            w[j] = j0 + j < p.k ? ld_f32(weights + j0 + j) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            if (row[j] >= p.R) {
+                atomicOr(p.err, (unsigned)DEVERR_BAD_ROW);
+                row[j] = -1;
+            }
+            raw[j] = typename Row8<Y>::Raw{};
+            if (row[j] >= 0) raw[j] = Row8<Y>::load(p.y, (int64_t)row[j] * p.H + col);
+        }
+        float s[G / 2][8];
+#pragma unroll
+        for (int j = 0; j < G; j += 2) {
+            float a[8], b[8];
+            Row8<Y>::unpack(raw[j], a);
+            Row8<Y>::unpack(raw[j + 1], b);
+            const float wa = row[j] < 0 ? 0.f : w[j], wb = row[j + 1] < 0 ? 0.f : w[j + 1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[j / 2][i] = fmaf(wb, b[i], wa * a[i]);
+        }
+#pragma unroll
+        for (int d = 1; d < G / 2; d *= 2)
+#pragma unroll
+            for (int j = 0; j + d < G / 2; j += 2 * d)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[j][i] += s[j + d][i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += s[0][i];
     }
     if (p.add) {
         float f[8];
@@ -262,10 +339,15 @@ __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constan
     Row8<O>::store(p.out, t * p.H + col, acc);
 }
 
-template <typename Y, typename O> cudaError_t launch_combine(const CombineParams &p, cudaStream_t s) {
+template <typename Y, typename O> cudaError_t launch_combine(const CombineParams &p, int sms, cudaStream_t s) {
     const int64_t grid = (p.units + NT - 1) / NT;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch(expert_combine_kernel<Y, O>, grid, NT, 0, 1, s, p);
+    // Eight where the batch is a part of one wave, for latency (one token of 8
+    // rows x 2048: 2.4, 2.2, 1.8 us with 2, 4, 8); two in larger ones, whose
+    // occupancy keeps more on their way (8192 tokens of 8 x 4096: 102.5, 110.5,
+    // 117.7 us).
+    if (p.units <= (int64_t)sms * 1024) return launch(expert_combine_kernel<Y, O, 8>, grid, NT, 0, 1, s, p);
+    return launch(expert_combine_kernel<Y, O, 2>, grid, NT, 0, 1, s, p);
 }
 
 }  // namespace
@@ -380,11 +462,11 @@ int gnq_expert_combine(const void *y, const int32_t *slots, const float *weights
     p.H = (int)H;
     p.err = d->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (y_type == GNQ_BF16) return status_of(launch_combine<__nv_bfloat16, __nv_bfloat16>(p, s));
-    if (y_type == GNQ_FP16) return status_of(launch_combine<__half, __half>(p, s));
-    if (out_type == GNQ_BF16) return status_of(launch_combine<float, __nv_bfloat16>(p, s));
-    if (out_type == GNQ_FP16) return status_of(launch_combine<float, __half>(p, s));
-    return status_of(launch_combine<float, float>(p, s));
+    if (y_type == GNQ_BF16) return status_of(launch_combine<__nv_bfloat16, __nv_bfloat16>(p, d->sms, s));
+    if (y_type == GNQ_FP16) return status_of(launch_combine<__half, __half>(p, d->sms, s));
+    if (out_type == GNQ_BF16) return status_of(launch_combine<float, __nv_bfloat16>(p, d->sms, s));
+    if (out_type == GNQ_FP16) return status_of(launch_combine<float, __half>(p, d->sms, s));
+    return status_of(launch_combine<float, float>(p, d->sms, s));
 }
 
 }  // extern "C"

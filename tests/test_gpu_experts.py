@@ -79,7 +79,8 @@ def _logits(M, E, dtype, seed, ties=False):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("M,E,k", [(0, 8, 2), (1, 1, 1), (1, 128, 8), (2, 33, 32), (3, 1024, 32), (64, 60, 4),
-                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6)])
+                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6), (700, 8, 8), (4200, 1, 1), (6000, 1024, 2),
+                                   (9001, 100, 3)])
 def test_route(gnq, M, E, k, dtype):
     for ties in (False, True):
         _check_route(gnq, _logits(M, E, dtype, M + E, ties), k, renormalize=not ties, scale=2.5 if ties else 1.0)
@@ -214,6 +215,29 @@ def test_quantize_in_expert_order(gnq, counts, H, act, dtype):
     G.check()
     _check_packed(q, bs, y, scales, offsets, dtype)
     assert gnq.read_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quantize_extreme_scales(gnq, dtype):
+    """Global scales in and outside the range of the tabled quotient, block
+    scales of every code: bit for bit the oracle's."""
+    scales = [1e-38, 2e-30, 7.9e-31, 0.013, 3.0, 447.3, 1e4, 1.2e30, 1.3e30, 3e38]
+    counts = [40] * len(scales)
+    offsets = offsets_of(counts)
+    R, H = offsets[-1], 256
+    g = torch.Generator().manual_seed(8)
+    x = (torch.randn(R, H, generator=g) * torch.exp2(torch.randint(-14, 12, (R, H // 16, 1), generator=g).float())
+         .expand(R, H // 16, 16).reshape(R, H)).to(DTYPES[dtype])
+    G = Guarded()
+    bufs = [(G((R, H // 2), torch.uint8), G((scale_rows(R, len(counts)), H // 16), torch.float8_e4m3fn)) for _ in range(2)]
+    gnq.expert_quantize(x.cuda(), ints(offsets), fp32(scales), out=bufs[0])
+    slots = torch.arange(R).reshape(R, 1)
+    experts = torch.repeat_interleave(torch.arange(len(counts)), 40).reshape(R, 1)
+    gnq.expert_quantize(x.cuda(), ints(offsets), fp32(scales), slots=slots.int().cuda(), experts=experts.int().cuda(), out=bufs[1])
+    torch.cuda.synchronize()
+    G.check()
+    for q, bs in bufs:
+        _check_packed(q, bs, x, fp32(scales).cpu().tolist(), offsets, dtype)
 
 
 @pytest.mark.parametrize("act", [None, "silu"])
