@@ -72,37 +72,11 @@ template <> struct Logit<__half> : Logit16<__half, 0x7C00u> {
     static __device__ __forceinline__ float value(uint32_t key) { return __half2float(__ushort_as_half(bits(key))); }
 };
 
-// A logit's key and its expert.  16-bit logits carry the expert in the low half
-// of the word (all ones less its index: ties go to the lowest), so that one
-// comparison orders both and a maximum names the expert; fp32 ones beside it.
-template <typename L> struct Ranked {
-    uint32_t v;
-    static constexpr uint32_t kNone = Logit<L>::kNegInf | 0xFFFFu;  // up to here: -inf, or no expert
-    __device__ __forceinline__ void set(uint32_t key, int e) { v = key | (0xFFFFu - e); }
-    __device__ __forceinline__ void clear() { v = 0; }
-    __device__ __forceinline__ bool is(uint32_t top, int) const { return v == top; }
-    static __device__ __forceinline__ void order(Ranked &a, Ranked &b) {
-        const uint32_t m = max(a.v, b.v);
-        b.v = min(a.v, b.v);
-        a.v = m;
-    }
-    __device__ __forceinline__ int expert(uint32_t top) const { return 0xFFFF - (int)(top & 0xFFFFu); }
-};
-template <> struct Ranked<float> {
-    uint32_t v;
-    uint32_t e;
-    static constexpr uint32_t kNone = Logit<float>::kNegInf;
-    __device__ __forceinline__ void set(uint32_t key, int expert) { v = key, e = expert; }
-    __device__ __forceinline__ void clear() { v = 0, e = 0x7FFFFFFF; }
-    __device__ __forceinline__ bool is(uint32_t top, int expert) const { return v == top && e == (uint32_t)expert; }
-    static __device__ __forceinline__ void order(Ranked &a, Ranked &b) {
-        const bool swap = b.v > a.v || (b.v == a.v && b.e < a.e);
-        const Ranked t = a;
-        a.v = swap ? b.v : a.v, a.e = swap ? b.e : a.e;
-        b.v = swap ? t.v : b.v, b.e = swap ? t.e : b.e;
-    }
-    __device__ __forceinline__ int expert(uint32_t top) const {
-        return (int)__reduce_min_sync(0xffffffffu, v == top ? e : 0x7FFFFFFFu);
+// A logit's key and its expert, in order: by key, equal keys by falling index.
+struct Ranked {
+    uint32_t v, e;
+    static __device__ __forceinline__ bool less(const Ranked &a, const Ranked &b) {
+        return a.v < b.v || (a.v == b.v && a.e > b.e);
     }
 };
 
@@ -140,23 +114,58 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, int t, int lan
     }
 }
 
-// One token by one warp.  Up to eight logits a lane are put in falling order
-// (Batcher's merge exchange), so that a choice is a maximum over the lanes'
-// first ones and a step in one lane; more are searched at each choice.  Returns
-// the lane-th choice (-1: none).
-template <typename L, int NV, bool WIDE> __device__ __forceinline__ int pick_token(const RouteParams &p, int t, int lane) {
-    constexpr bool SORT = NV <= 8;
-    Ranked<L> r[NV];
-    {
-        uint32_t b[NV];
-        load_logits<L, NV, WIDE>(p, t, lane, b);
+// The choices of a token from exact keys, the lane-th to each lane: a search
+// through all of them for each.
+template <int NV>
+__device__ __noinline__ int pick_exact(const uint32_t (&key)[NV], int e0, int de, int k, uint32_t none, int lane) {
+    uint32_t taken = 0;
+    int choice = -1;
+    for (int j = 0; j < k; ++j) {
+        Ranked h = {0, 0x7FFFFFFFu};
+        int at = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = WIDE ? lane * NV + i : 32 * i + lane;
-            if (WIDE || e < p.E) r[i].set(Logit<L>::key(b[i]), e);
-            else r[i].clear();
+            const Ranked o = {taken >> i & 1 ? 0u : key[i], (uint32_t)(e0 + de * i)};
+            if (Ranked::less(h, o)) h = o, at = i;
         }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, h.v);
+        if (top <= none) break;
+        const uint32_t e = __reduce_min_sync(0xffffffffu, h.v == top ? h.e : 0x7FFFFFFFu);
+        if (h.v == top && h.e == e) taken |= 1u << at;
+        if (lane == j) choice = (int)e;
     }
+    return choice;
+}
+
+// One token by one warp.  A logit's key and all ones less its index share a
+// word, the index in the low bits, so that one comparison orders both, ties by
+// index, and a maximum names the expert.  16-bit keys fit beside the index;
+// fp32 ones lose their low 8 bits (10 from 512 experts on): if two neighbours
+// in the order, down to the first that is not chosen, are equal in what is
+// left, the token is picked again from exact keys (16384 x 256 fp32 logits:
+// 15.5 us with exact keys throughout, all instruction issue).
+// `b` holds the lane's logits.  Up to eight a lane are put in falling order (Batcher's merge
+// exchange), so that a choice is a maximum over the lanes' first ones and a
+// step in one lane; more are searched at each choice.  Returns the lane-th
+// choice (-1: none).
+template <typename L, int NV, bool WIDE>
+__device__ __forceinline__ int pick_token(const RouteParams &p, int t, int lane, const uint32_t (&b)[NV]) {
+    constexpr bool SORT = NV <= 8, EXACT = sizeof(L) == 2;
+    constexpr uint32_t MASK = EXACT ? 0xFFFFu : NV <= 8 ? 0xFFu : 0x3FFu;
+    constexpr uint32_t NONE = Logit<L>::kNegInf | MASK;  // up to here: -inf, or no expert
+    const int e0 = WIDE ? lane * NV : lane;
+    constexpr int DE = WIDE ? 1 : 32;
+    uint32_t r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = e0 + DE * i;
+        r[i] = WIDE || e < p.E ? (Logit<L>::key(b[i]) & ~MASK) | (MASK - e) : 0u;
+    }
+    auto order = [&](uint32_t &x, uint32_t &y) {
+        const uint32_t m = max(x, y);
+        y = min(x, y);
+        x = m;
+    };
     if constexpr (SORT) {
 #pragma unroll
         for (int q = 1; q < NV; q *= 2)
@@ -166,53 +175,59 @@ template <typename L, int NV, bool WIDE> __device__ __forceinline__ int pick_tok
                 for (int i = d % q; i + d < NV; i += 2 * d)
 #pragma unroll
                     for (int c = 0; c < d; ++c)
-                        if (i + c + d < NV && (i + c) / (2 * q) == (i + c + d) / (2 * q))
-                            Ranked<L>::order(r[i + c], r[i + c + d]);
+                        if (i + c + d < NV && (i + c) / (2 * q) == (i + c + d) / (2 * q)) order(r[i + c], r[i + c + d]);
     }
     auto first = [&] {
-        Ranked<L> h = r[0];
+        uint32_t h = r[0];
         if constexpr (!SORT) {
 #pragma unroll
-            for (int i = 1; i < NV; ++i) {
-                Ranked<L> o = r[i];
-                Ranked<L>::order(h, o);
-            }
+            for (int i = 1; i < NV; ++i) h = max(h, r[i]);
         }
-        return h;
+        return __reduce_max_sync(0xffffffffu, h);
     };
-
-    Ranked<L> head = first();
-    uint32_t top = __reduce_max_sync(0xffffffffu, head.v);
-    const float peak = Logit<L>::value(top);
-    float part = 0.f;
-    if (!p.renormalize && top > Ranked<L>::kNone) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (r[i].v != 0) part += expf(Logit<L>::value(r[i].v) - peak);
-    }
-    // lane j keeps the j-th choice
-    uint32_t mine = 0;
-    int choice = -1;
-    for (int j = 0; top > Ranked<L>::kNone;) {
-        const int e = head.expert(top);
-        if (lane == j) mine = top, choice = e;
-        if (++j == p.k) break;
+    uint32_t mine = 0, last = 0;  // lane j keeps the j-th choice
+    bool again = false;
+    for (int j = 0;; ++j) {
+        const uint32_t top = first();
+        again |= !EXACT && ((top ^ last) & ~MASK) == 0;
+        if (top <= NONE || j == p.k) break;
+        last = top;
+        if (lane == j) mine = top;
+        if (EXACT && j + 1 == p.k) break;
         if constexpr (SORT) {
-            const bool step = head.is(top, e);
+            const bool step = r[0] == top;
 #pragma unroll
-            for (int i = 0; i + 1 < NV; ++i)
-                if (step) r[i] = r[i + 1];
-            if (step) r[NV - 1].clear();
+            for (int i = 0; i + 1 < NV; ++i) r[i] = step ? r[i + 1] : r[i];
+            r[NV - 1] = step ? 0u : r[NV - 1];
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (r[i].is(top, e)) r[i].clear();
+            for (int i = 0; i < NV; ++i) r[i] = r[i] == top ? 0u : r[i];
         }
-        head = first();
-        top = __reduce_max_sync(0xffffffffu, head.v);
     }
-    float w = choice >= 0 ? expf(Logit<L>::value(mine) - peak) : 0.f;
-    const float total = warp_sum(p.renormalize ? w : part);
+    int choice = mine ? (int)(MASK - (mine & MASK)) : -1;
+    if constexpr (!EXACT) {
+        if (again) {  // (the same for the whole warp)
+            uint32_t key[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) key[i] = WIDE || e0 + DE * i < p.E ? Logit<L>::key(b[i]) : 0u;
+            choice = pick_exact<NV>(key, e0, DE, p.k, Logit<L>::kNegInf, lane);
+        }
+    }
+    float v = 0.f;
+    if (choice >= 0) {
+        if constexpr (EXACT) v = Logit<L>::value(mine);
+        else v = ld_f32(static_cast<const float *>(p.logits) + (int64_t)t * p.row_stride + choice);
+    }
+    const float peak = __shfl_sync(0xffffffffu, v, 0);
+    float w = choice >= 0 ? expf(v - peak) : 0.f;
+    float part = w;
+    if (!p.renormalize) {
+        part = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (WIDE || e0 + DE * i < p.E) part += expf(Logit<L>::value(Logit<L>::key(b[i])) - peak);
+    }
+    const float total = warp_sum(part);
     if (choice >= 0) w = __fmul_rn(__fdiv_rn(w, total), p.scale);
     if (lane < p.k) {
         const int64_t at = (int64_t)t * p.k + lane;
@@ -220,6 +235,22 @@ template <typename L, int NV, bool WIDE> __device__ __forceinline__ int pick_tok
         p.weights[at] = w;
     }
     return choice;
+}
+
+// Tokens first, first + step, ... before `end` by one warp, the next one's
+// logits on their way meanwhile; `done` gets the lane-th choice of each.
+template <typename L, int NV, bool WIDE, typename Done>
+__device__ __forceinline__ void pick_tokens(const RouteParams &p, int first, int end, int step, int lane, const Done &done) {
+    if (first >= end) return;
+    uint32_t b[NV];
+    load_logits<L, NV, WIDE>(p, first, lane, b);
+    for (int t = first; t < end; t += step) {
+        uint32_t next[NV];
+        if (t + step < end) load_logits<L, NV, WIDE>(p, t + step, lane, next);
+        done(pick_token<L, NV, WIDE>(p, t, lane, b));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) b[i] = next[i];
+    }
 }
 
 constexpr int kKeep = 4;        // groups of 32 choices whose place a warp keeps in registers
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(1024) route_small_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
     const int W = blockDim.x >> 5;
-    for (int t = threadIdx.x >> 5; t < p.M; t += W) pick_token<L, NV, WIDE>(p, t, threadIdx.x & 31);
+    pick_tokens<L, NV, WIDE>(p, threadIdx.x >> 5, p.M, W, threadIdx.x & 31, [](int) {});
     __syncthreads();
     place_all(p, counts, sums);
 }
@@ -338,7 +369,7 @@ __global__ void __launch_bounds__(1024) route_place_all_kernel(const __grid_cons
 // The choices of `chunk` tokens (the last chunk: of what is left, less than
 // twice as many), and their counts where the chunk's slots will be (chunks > 0).
 template <typename L, int NV, bool WIDE>
-__global__ void __launch_bounds__(1024) route_pick_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks) {
+__global__ void __launch_bounds__(512) route_pick_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks) {
     extern __shared__ int32_t counts[];
     pdl_wait();
     pdl_trigger();
@@ -348,10 +379,9 @@ __global__ void __launch_bounds__(1024) route_pick_kernel(const __grid_constant_
         for (int i = t; i < p.E; i += blockDim.x) counts[i] = 0;
         __syncthreads();
     }
-    for (int m = begin + (t >> 5); m < end; m += W) {
-        const int choice = pick_token<L, NV, WIDE>(p, m, lane);
+    pick_tokens<L, NV, WIDE>(p, begin + (t >> 5), end, W, lane, [&](int choice) {
         if (chunks && choice >= 0) atomicAdd(&counts[choice], 1);
-    }
+    });
     if (!chunks) return;
     __syncthreads();
     for (int i = t; i < p.E; i += blockDim.x) p.slots[(int64_t)begin * p.k + i] = counts[i];
@@ -373,9 +403,18 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const __grid_constant_
     const int from = min(chunks, stretch * per), to = min(chunks, from + per);
     int32_t *const table = p.slots + e;
     const int64_t step = (int64_t)chunk * p.k;
+    // eight reads on their way at a time
+    auto read = [&](int c0, int (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = e < p.E && c0 + i < to ? table[(c0 + i) * step] : 0;
+    };
     int sum = 0;
-    if (e < p.E)
-        for (int c = from; c < to; ++c) sum += table[c * step];
+    for (int c = from; c < to; c += 8) {
+        int v[8];
+        read(c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += v[i];
+    }
     part[t] = sum;
     __syncthreads();
     // first stretch: the expert's total; every stretch: what comes before it
@@ -400,12 +439,14 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const __grid_constant_
     const int first = slices + part[t % slice];
     if (t < slice && e < p.E) p.offsets[e] = first;
     if (rank == 0 && t == 0) p.offsets[p.E] = rows;
-    if (e < p.E) {
-        int row = first + before;
-        for (int c = from; c < to; ++c) {
-            const int v = table[c * step];
-            table[c * step] = row;
-            row += v;
+    int row = first + before;
+    for (int c = from; c < to; c += 8) {
+        int v[8];
+        read(c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (e < p.E && c + i < to) table[(c + i) * step] = row;
+            row += v[i];
         }
     }
 }
@@ -440,7 +481,7 @@ template <typename L, int NV, bool WIDE> cudaError_t launch_route_form(const Rou
     const int chunk = std::max((p.E + p.k - 1) / p.k, (p.M + 2 * sms - 1) / (2 * sms)), chunks = p.M / chunk;
     int slice = 1;
     while (slice * kScanCtas < p.E) slice *= 2;
-    if ((e = launch(pick, chunks, 1024, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
+    if ((e = launch(pick, chunks, 512, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
     if ((e = launch(route_scan_kernel, kScanCtas, 1024, 0, kScanCtas, s, p, chunk, chunks, slice)) != cudaSuccess) return e;
     const int warps = std::max(hist, 8);
     if ((e = opt_in_dynamic_smem(reinterpret_cast<const void *>(route_place_kernel))) != cudaSuccess) return e;
