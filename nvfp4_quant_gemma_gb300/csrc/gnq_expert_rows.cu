@@ -59,6 +59,9 @@ struct ExpertQuantParams {
     uint8_t *q, *block_scale;
     int64_t units;  // 16-element blocks in all rows of `in`
     int H, upr;     // elements and units of a row
+    int M;          // rows of `in`
+    int wave;       // CTAs of the first wave, which prefetch before the wait
+    int rows_ahead; // rows from a unit to the one prefetched in its place
 };
 
 // RN(g / v) for the value v of a block scale, from v and RN(1 / v) of a table in
@@ -104,13 +107,21 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
     const bool ok = at < p.units;
     const int m = ok ? (int)(at / p.upr) : 0, col = ok ? (int)(at - (int64_t)m * p.upr) * 16 : 0;
     if (FAN) fill_reciprocals(tab, threadIdx.x);
+    const uint16_t *src = p.in + m * p.row_stride + col;
+    auto prefetch = [&](const uint16_t *at, bool last) {
+        prefetch_l2_line(at, last);
+        if (ACT != ACT_NONE) prefetch_l2_line(at + p.H, last);
+    };
+    // The first wave's units into L2 while the preceding grid drains, and later
+    // the units that take this place three quarters of a round from now: hints.
+    if ((int)blockIdx.x < p.wave && ok) prefetch(src, false);
     pdl_wait();
     pdl_trigger();
-    const uint16_t *src = p.in + m * p.row_stride + col;
     uint4 y[2], u[2];
     load_unit<T, V8>(src, y);
+    if constexpr (ACT != ACT_NONE) load_unit<T, V8>(src + p.H, u);
+    if (ok && m + p.rows_ahead < p.M) prefetch(src + p.rows_ahead * p.row_stride, true);
     if constexpr (ACT != ACT_NONE) {
-        load_unit<T, V8>(src + p.H, u);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float g[8], f[8];
@@ -184,17 +195,20 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
     }
 }
 
-template <typename T, int ACT> cudaError_t launch_expert_quant(const ExpertQuantParams &p, bool v8, cudaStream_t s) {
+template <typename T, int ACT> cudaError_t launch_expert_quant(ExpertQuantParams &p, bool v8, cudaStream_t s) {
     const int64_t grid = (p.units + NT - 1) / NT;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    auto start = [&](auto fn) {
+        p.wave = one_wave_ctas(reinterpret_cast<const void *>(fn), NT);
+        p.rows_ahead = (int)(((int64_t)p.wave * 3 / 4 * NT + p.upr - 1) / p.upr);
+        return launch(fn, grid, NT, 0, 1, s, p);
+    };
     if (p.slots)
-        return v8 ? launch(expert_quant_kernel<T, ACT, true, true>, grid, NT, 0, 1, s, p)
-                  : launch(expert_quant_kernel<T, ACT, true, false>, grid, NT, 0, 1, s, p);
-    return v8 ? launch(expert_quant_kernel<T, ACT, false, true>, grid, NT, 0, 1, s, p)
-              : launch(expert_quant_kernel<T, ACT, false, false>, grid, NT, 0, 1, s, p);
+        return v8 ? start(expert_quant_kernel<T, ACT, true, true>) : start(expert_quant_kernel<T, ACT, true, false>);
+    return v8 ? start(expert_quant_kernel<T, ACT, false, true>) : start(expert_quant_kernel<T, ACT, false, false>);
 }
 
-template <typename T> cudaError_t launch_expert_quant_act(const ExpertQuantParams &p, int act, bool v8, cudaStream_t s) {
+template <typename T> cudaError_t launch_expert_quant_act(ExpertQuantParams &p, int act, bool v8, cudaStream_t s) {
     if (act == ACT_SILU) return launch_expert_quant<T, ACT_SILU>(p, v8, s);
     if (act == ACT_GELU_TANH) return launch_expert_quant<T, ACT_GELU_TANH>(p, v8, s);
     return launch_expert_quant<T, ACT_NONE>(p, v8, s);
@@ -390,6 +404,7 @@ int gnq_expert_quantize(const void *x, int64_t row_stride, int act, const int32_
     p.H = (int)H;
     p.upr = (int)(H / 16);
     p.units = M * p.upr;
+    p.M = (int)M;
     const bool v8 = aligned(x, 32) && row_stride % 16 == 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return status_of(dtype == GNQ_BF16 ? launch_expert_quant_act<__nv_bfloat16>(p, act, v8, s)
