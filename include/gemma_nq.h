@@ -426,10 +426,11 @@ int gnq_query_launch(int64_t M, int64_t H, int k, int has_residual, int write_y,
                      int *form);
 
 /*
- * Tuning hook: force the kernel of later nvfp4_linear calls in this process.
- * kernel 0 = automatic; 1 = tiles of one CTA, K split over a cluster where
- * that fills the device; 2 = CTA pairs on 256 x 256 tiles.  (More tiles than a
- * grid holds go to pairs all the same.)  A split adds its parts last, so y may
+ * Tuning hook: force the kernel of later nvfp4_linear and nvfp4_expert_linear
+ * calls in this process.  kernel 0 = automatic; 1 = tiles of one CTA
+ * (nvfp4_linear: K split over a cluster where that fills the device); 2 = CTA
+ * pairs on 256 x 256 tiles.  (More tiles of nvfp4_linear than a grid holds go to
+ * pairs all the same.)  A split adds its parts last, so y may
  * move by a rounding step of the fp32 sum.  Not synchronised with calls in
  * flight on other host threads.  Returns GNQ_ERR_SHAPE for other values.
  */

@@ -917,8 +917,8 @@ def query_launch(M: int, H: int, mode, dtype: str = "bf16", k: int = 1, residual
 
 
 def set_linear_policy(kernel: int = 0) -> None:
-    """Force the kernel of later nvfp4_linear calls (0 = automatic): 1 = tiles
-    of one CTA with a split K, 2 = CTA pairs on 256 x 256 tiles."""
+    """Force the kernel of later nvfp4_linear and nvfp4_expert_linear calls (0 =
+    automatic): 1 = tiles of one CTA, 2 = CTA pairs on 256 x 256 tiles."""
     _check(load().gnq_set_linear_policy(int(kernel)), "gnq_set_linear_policy")
 
 

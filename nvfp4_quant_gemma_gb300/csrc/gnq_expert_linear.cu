@@ -21,7 +21,16 @@
 namespace gnq {
 namespace {
 
+// 64 rows a tile leave tensor memory (twice 64 sums and the scales) and shared
+// memory (three stages) for two CTAs on an SM, one of which computes while the
+// other starts or ends a tile: 77.1 us for 64 tokens to 8 of 128 experts, N = 4096,
+// K = 2048 (79.2 with one CTA and 128 rows); 128 experts of 200 rows, N = 2048, K =
+// 512: 40.9 (51.0); of 16 rows, N = 4096, K = 2048: 89.8 (94.0).
+constexpr int kTileRows = 64;
+constexpr int kPerSm = 2;
+constexpr uint32_t kTmemCols = 256;
 constexpr int kRowBox = 32;  // rows of one tile copy of activations
+constexpr uint32_t kBytesX = kTileRows * 128, kStage = kBytesW + kBytesX + 2 * kBytesSf;
 constexpr int kWarps = 6;
 
 
@@ -44,9 +53,6 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
     const uint32_t done = bar0 + 8u * (2 * kMaxStages + 4);
-    const uint32_t bytes_x = (uint32_t)p.T * 128;
-    const uint32_t stage_bytes = kBytesW + bytes_x + 2 * kBytesSf;
-
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
@@ -61,18 +67,18 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
         failed = 0;
     }
     if (warp == 1) {
-        tmem_alloc<1>((uint32_t)__cvta_generic_to_shared(&tmem_slot), p.tmem_cols);
+        tmem_alloc<1>((uint32_t)__cvta_generic_to_shared(&tmem_slot), kTmemCols);
         tmem_relinquish<1>();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t sfw_col = tmem + 2 * p.T, sfx_col = sfw_col + 16;
+    const uint32_t sfw_col = tmem + 2 * kTileRows, sfx_col = sfw_col + 16;
 
     pdl_wait();  // inputs may come from the preceding grid, outputs may still be read by it
     pdl_trigger();
-    const TileList list = build_tiles(x, p.T, reinterpret_cast<int *>(dyn + (base - dyn0) + stage_bytes * p.stages), kWarps);
+    const TileList list = build_tiles(x, kTileRows, reinterpret_cast<int *>(dyn + (base - dyn0) + kStage * p.stages), kWarps);
 
     const int KT = (p.K64 + 3) / 4;
     auto give_up = [&] {
@@ -100,13 +106,13 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t at = base + stage_bytes * s, sf_bytes = 512u * min(4, p.K64 - 4 * kt);
+                    const uint32_t at = base + kStage * s, sf_bytes = 512u * min(4, p.K64 - 4 * kt);
                     mbar_expect_tx(full(s), kBytesW + boxes * (kRowBox * 128) + 2 * sf_bytes + p.tx_extra);
                     tma_load_2d(at, &map_w, kt * 128, w0, full(s));
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(at + kBytesW + b * (kRowBox * 128), &map_x, kt * 128, tile.row + b * kRowBox, full(s));
-                    bulk_g2s(at + kBytesW + bytes_x, w_sf + kt * 2048, sf_bytes, full(s));
-                    bulk_g2s(at + kBytesW + bytes_x + kBytesSf, x_sf + kt * 2048, sf_bytes, full(s));
+                    bulk_g2s(at + kBytesW + kBytesX, w_sf + kt * 2048, sf_bytes, full(s));
+                    bulk_g2s(at + kBytesW + kBytesX + kBytesSf, x_sf + kt * 2048, sf_bytes, full(s));
                 }
                 __syncwarp();
                 if (++s == p.stages) s = 0, parity ^= 1;
@@ -132,8 +138,9 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
             const TileList::Tile tile = list.at(i, e, lane);
             e = tile.e;
             const uint32_t idesc = idesc_nvfp4(kTileN, (tile.rows + 15) & ~15);
-            // 32 rows of a scale tile are one column of tensor memory
-            const uint32_t acc = tmem + p.T * (j & 1), sfx = sfx_col + (((tile.row - tile.start) & 127) >> 5);
+            // 32 rows of a scale tile are one column of tensor memory.  A tile
+            // starts 0 or 64 rows into it: the column has to be even.
+            const uint32_t acc = tmem + kTileRows * (j & 1), sfx = sfx_col + (((tile.row - tile.start) & 127) >> 5);
             if (!warp_wait_bounded(acc_empty(j & 1), ((j >> 1) & 1) ^ 1, p.wait_limit)) {
                 give_up();
                 break;
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
                 tc_fence_after();
                 const int nk = min(4, p.K64 - 4 * kt);
                 if (elect_one()) {
-                    const uint32_t at = (base + stage_bytes * s) >> 4, sf = at + ((kBytesW + bytes_x) >> 4);
+                    const uint32_t at = (base + kStage * s) >> 4, sf = at + ((kBytesW + kBytesX) >> 4);
                     auto step = [&](int k) {
                         cp_scales<1>(sfw_col + 4 * k, desc_scales(sf + 32 * k));
                         cp_scales<1>(sfx_col + 4 * k, desc_scales(sf + kBytesSf / 16 + 32 * k));
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem + p.T * (j & 1) + lanes;
+            const uint32_t acc = tmem + kTileRows * (j & 1) + lanes;
             auto result = [&](uint32_t v) { return fmaf(__uint_as_float(v), alpha, bias); };
             // Two 16-bit columns per lane: neighbouring lanes exchange, the
             // even one stores row c + i, the odd one c + i + 1.
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc<1>(tmem, p.tmem_cols);
+    if (warp == 1) tmem_dealloc<1>(tmem, kTmemCols);
 }
 
 template <typename O, typename B>
@@ -249,8 +256,19 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
     return launch(fn, grid, 32 * kWarps, smem, 1, s, mw, mx, x);
 }
 
-// Whether CTA pairs take the call.
-bool pairs_take(int64_t E, int64_t R, int64_t K) { return R >= 80 * E && K >= 1024; }
+// Whether CTA pairs take the call.  Their tile is eight times the other
+// kernel's and pays from about 120 rows an expert on, where there are enough of
+// them to go round and K is deep enough for the hand-over between tiles.  Of 668
+// shapes timed in both kernels (2 to 128 experts, 64 to 1000 rows each, N of 512 to
+// 8192, K of 512 to 4096) the choice loses 0.5 % on average against the faster
+// one, and more than 10 % on 6 (64 experts of 100 rows, N = K = 4096: 125 us on
+// single CTAs, 114 on pairs; of 160 rows, N = 512, K = 4096: 28.3 and 31.1; of 256
+// rows, N = K = 2048: 80 and 72; 8 of 64 rows, N = K = 4096: 21.4 and 19.3).
+bool pairs_take(int64_t E, int64_t R, int64_t N, int64_t K) {
+    if (R < 120 * E || K < 768) return false;
+    const int64_t tiles = (N + 255) / 256 * std::max(E, R / 224);
+    return K >= 1536 ? tiles >= 64 : R >= 250 * E && tiles >= 1000;
+}
 
 }  // namespace
 }  // namespace gnq
@@ -300,16 +318,16 @@ extern "C" int nvfp4_expert_linear(const void *q, const void *block_scale, const
     p.tx_extra = inject_timeout_on() ? 16u : 0u;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int forced = linear_policy();
-    if (forced ? forced == 2 : pairs_take(E, R, K)) return status_of(launch_expert_linear_pair(x, q, w_q, out_type, bias_type, d->sms, s));
+    if (forced ? forced == 2 : pairs_take(E, R, N, K)) return status_of(launch_expert_linear_pair(x, q, w_q, out_type, bias_type, d->sms, s));
     p.n_tiles = (int)((N + kTileN - 1) / kTileN);
-    p.T = R <= 32 ? 32 : R <= 64 ? 64 : 128;
-    p.tmem_cols = p.T == 32 ? 128 : p.T == 64 ? 256 : 512;  // two tiles' sums and the scales
-    const int64_t tiles = (R / p.T + std::min(E, R)) * p.n_tiles;  // at most
+    const int64_t tiles = (R / kTileRows + std::min(E, R)) * p.n_tiles;  // at most
     if (tiles > 0x3FFFFFFF) return GNQ_ERR_SHAPE;
-    const int64_t stage = kBytesW + p.T * 128 + 2 * kBytesSf, lists = TileList::bytes((int)E, kWarps);
-    p.stages = (int)std::min<int64_t>(kMaxStages, (d->smem_optin - 1024 - 1024 - lists) / stage);
-    const size_t smem = (size_t)(1024 + p.stages * stage + lists);
-    const int64_t grid = std::min<int64_t>(tiles, d->sms);
+    const int64_t lists = TileList::bytes((int)E, kWarps);
+    // (each CTA: 1 KB of the system's, its static part, and what alignment takes)
+    const int64_t room = (tiles <= d->sms ? d->smem_optin : d->smem_sm / kPerSm - 1024) - 1024 - 1024 - lists;
+    p.stages = (int)std::min<int64_t>(kMaxStages, room / kStage);
+    const size_t smem = (size_t)(1024 + p.stages * kStage + lists);
+    const int64_t grid = std::min<int64_t>(tiles, kPerSm * d->sms);
     CUtensorMap mw, mx;
     if (!encode_codes(&mw, w_q, E * N, K, kTileN) || !encode_codes(&mx, q, R, K, kRowBox)) return GNQ_ERR_CUDA;
     if (out_type == GNQ_BF16) return status_of(launch_expert_linear<__nv_bfloat16, __nv_bfloat16>(mw, mx, x, grid, smem, s));

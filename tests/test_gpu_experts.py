@@ -387,6 +387,13 @@ def test_linear_wait_timeout_in_both_kernels(gnq):
             _run_linear(gnq, counts, 384, 1024, torch.bfloat16)
 
 
+@pytest.mark.parametrize("N,K", [(136, 64), (256, 1088)])
+@pytest.mark.parametrize("counts", [[150, 3] + [0] * 14, [1, 0, 65, 190, 64] + [0] * 20, [0, 63, 129] * 12])
+def test_linear_few_rows_but_many_for_one(gnq, counts, N, K):
+    """Batches that go to tiles of 64 rows, some of which start inside a scale tile."""
+    _run_linear(gnq, counts, N, K, torch.bfloat16, bias=torch.bfloat16, seed=N)
+
+
 @pytest.mark.parametrize("extra", [0, 200])
 def test_linear_without_rows(gnq, extra):
     """No expert has a row: nothing is written."""
