@@ -33,7 +33,6 @@ constexpr int kRowBox = 32;  // rows of one tile copy of activations
 constexpr uint32_t kBytesX = kTileRows * 128, kStage = kBytesW + kBytesX + 2 * kBytesSf;
 constexpr int kWarps = 6;
 
-
 template <typename O, typename B>
 __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                     const __grid_constant__ CUtensorMap map_x,
@@ -262,8 +261,8 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
 // shapes timed in both kernels (2 to 128 experts, 64 to 1000 rows each, N of 512 to
 // 8192, K of 512 to 4096) the choice loses 0.5 % on average against the faster
 // one, and more than 10 % on 6 (64 experts of 100 rows, N = K = 4096: 125 us on
-// single CTAs, 114 on pairs; of 160 rows, N = 512, K = 4096: 28.3 and 31.1; of 256
-// rows, N = K = 2048: 80 and 72; 8 of 64 rows, N = K = 4096: 21.4 and 19.3).
+// single CTAs, 114 on pairs; of 160 rows, N = 512, K = 4096: 28.3 and 31.1; 8 of 64
+// rows, N = K = 4096: 21.4 and 19.3).
 bool pairs_take(int64_t E, int64_t R, int64_t N, int64_t K) {
     if (R < 120 * E || K < 768) return false;
     const int64_t tiles = (N + 255) / 256 * std::max(E, R / 224);

@@ -45,9 +45,11 @@ template <> struct Logit<float> {
     static constexpr uint32_t kNegInf = 0x007FFFFFu;
     static __device__ __forceinline__ uint32_t key(uint32_t b) {
         const float v = __uint_as_float(b) + 0.f;  // -0 -> +0
-        if (v != v) return 0xFFFFFFFFu;
-        b = __float_as_uint(v);
-        return b & 0x80000000u ? ~b : b | 0x80000000u;
+        return v != v ? 0xFFFFFFFFu : number_key(v);
+    }
+    static __device__ __forceinline__ uint32_t number_key(float v) {
+        const uint32_t b = __float_as_uint(v);
+        return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
     }
     static __device__ __forceinline__ float value(uint32_t key) {
         return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
@@ -143,7 +145,8 @@ __device__ __noinline__ int pick_exact(const uint32_t (&key)[NV], int e0, int de
 // fp32 ones lose their low 8 bits (10 from 512 experts on): if two neighbours
 // in the order, down to the first that is not chosen, are equal in what is
 // left, the token is picked again from exact keys (16384 x 256 fp32 logits:
-// 15.5 us with exact keys throughout, all instruction issue).
+// 15.5 us with exact keys throughout, all instruction issue).  So is one with a
+// NaN, whose key the first look does not make (their sum is one, too).
 // `b` holds the lane's logits.  Up to eight a lane are put in falling order (Batcher's merge
 // exchange), so that a choice is a maximum over the lanes' first ones and a
 // step in one lane; more are searched at each choice.  Returns the lane-th
@@ -156,10 +159,19 @@ __device__ __forceinline__ int pick_token(const RouteParams &p, int t, int lane,
     const int e0 = WIDE ? lane * NV : lane;
     constexpr int DE = WIDE ? 1 : 32;
     uint32_t r[NV];
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = e0 + DE * i;
-        r[i] = WIDE || e < p.E ? (Logit<L>::key(b[i]) & ~MASK) | (MASK - e) : 0u;
+        uint32_t key;
+        if constexpr (EXACT) {
+            key = Logit<L>::key(b[i]);
+        } else {
+            const float v = __uint_as_float(b[i]) + 0.f;  // -0 -> +0
+            sum += v;
+            key = Logit<float>::number_key(v);
+        }
+        r[i] = WIDE || e < p.E ? (key & ~MASK) | (MASK - e) : 0u;
     }
     auto order = [&](uint32_t &x, uint32_t &y) {
         const uint32_t m = max(x, y);
@@ -186,7 +198,7 @@ __device__ __forceinline__ int pick_token(const RouteParams &p, int t, int lane,
         return __reduce_max_sync(0xffffffffu, h);
     };
     uint32_t mine = 0, last = 0;  // lane j keeps the j-th choice
-    bool again = false;
+    bool again = !EXACT && __any_sync(0xffffffffu, sum != sum);
     for (int j = 0;; ++j) {
         const uint32_t top = first();
         again |= !EXACT && ((top ^ last) & ~MASK) == 0;
@@ -257,6 +269,7 @@ constexpr int kKeep = 4;        // groups of 32 choices whose place a warp keeps
 constexpr int kSmallTokens = 64;       // up to here one launch
 constexpr int kOneCta = 32 * 32 * kKeep;  // choices that one CTA places
 constexpr int kScanCtas = 8;
+constexpr int kPickWarps = 18;
 
 // Choices begin .. end - 1 by one CTA: the place of each among those of its
 // expert, plus first(expert).  hist: E words per warp.  `first` is called by
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(1024) route_place_all_kernel(const __grid_cons
 // The choices of `chunk` tokens (the last chunk: of what is left, less than
 // twice as many), and their counts where the chunk's slots will be (chunks > 0).
 template <typename L, int NV, bool WIDE>
-__global__ void __launch_bounds__(512) route_pick_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks) {
+__global__ void __launch_bounds__(32 * kPickWarps) route_pick_kernel(const __grid_constant__ RouteParams p, int chunk, int chunks) {
     extern __shared__ int32_t counts[];
     pdl_wait();
     pdl_trigger();
@@ -401,15 +414,15 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const __grid_constant_
     const int e = rank * slice + t % slice, stretch = t / slice, stretches = min(32, 1024 / slice);
     const int per = (chunks + stretches - 1) / stretches;
     const int from = min(chunks, stretch * per), to = min(chunks, from + per);
-    int32_t *const table = p.slots + e;
-    const int64_t step = (int64_t)chunk * p.k;
+    const int step = chunk * p.k, mine = e < p.E ? to - from : 0;
+    int32_t *const table = p.slots + (int64_t)from * step + e;
     // eight reads on their way at a time
-    auto read = [&](int c0, int (&v)[8]) {
+    auto read = [&](int c, int (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = e < p.E && c0 + i < to ? table[(c0 + i) * step] : 0;
+        for (int i = 0; i < 8; ++i) v[i] = c + i < mine ? table[(c + i) * step] : 0;
     };
     int sum = 0;
-    for (int c = from; c < to; c += 8) {
+    for (int c = 0; c < mine; c += 8) {
         int v[8];
         read(c, v);
 #pragma unroll
@@ -440,12 +453,12 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const __grid_constant_
     if (t < slice && e < p.E) p.offsets[e] = first;
     if (rank == 0 && t == 0) p.offsets[p.E] = rows;
     int row = first + before;
-    for (int c = from; c < to; c += 8) {
+    for (int c = 0; c < mine; c += 8) {
         int v[8];
         read(c, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (e < p.E && c + i < to) table[(c + i) * step] = row;
+            if (c + i < mine) table[(c + i) * step] = row;
             row += v[i];
         }
     }
@@ -481,7 +494,8 @@ template <typename L, int NV, bool WIDE> cudaError_t launch_route_form(const Rou
     const int chunk = std::max((p.E + p.k - 1) / p.k, (p.M + 2 * sms - 1) / (2 * sms)), chunks = p.M / chunk;
     int slice = 1;
     while (slice * kScanCtas < p.E) slice *= 2;
-    if ((e = launch(pick, chunks, 512, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
+    const int rounds = (chunk + kPickWarps - 1) / kPickWarps, pickers = (chunk + rounds - 1) / rounds;
+    if ((e = launch(pick, chunks, 32 * pickers, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
     if ((e = launch(route_scan_kernel, kScanCtas, 1024, 0, kScanCtas, s, p, chunk, chunks, slice)) != cudaSuccess) return e;
     const int warps = std::max(hist, 8);
     if ((e = opt_in_dynamic_smem(reinterpret_cast<const void *>(route_place_kernel))) != cudaSuccess) return e;
