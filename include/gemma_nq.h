@@ -286,8 +286,8 @@ int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
  * fp32 per expert, 0 for one that all share (GNQ_ERR_MODE otherwise).
  * Offsets that do not ascend within 0 .. R, and slots that are not a row of
  * their expert, are found on the device: bit 2 of the device error word is set
- * (gnq_read_device_error), what they name is left out, and nothing outside the
- * buffers is touched.
+ * (gnq_read_device_error), what they name is left out (nvfp4_expert_linear
+ * writes nothing at all), and nothing outside the buffers is touched.
  */
 
 /*

@@ -36,7 +36,7 @@ __device__ __forceinline__ int find_expert(const int32_t *offsets, int E, int ro
     if (above == 0) return E;
     const int first = (__ffs(above) - 1) * step, i = min(first + lane + 1, E);
     above = __ballot_sync(0xffffffffu, lane < step && ld_i32(offsets + i) > row);
-    return first + __ffs(above) - 1;  // the last of these bounds is the one found above
+    return above ? first + __ffs(above) - 1 : E;  // (never 0: the last of these bounds is the one found above)
 }
 
 // Byte of the scale tile row of row `r` of an expert that starts at row `o`.

@@ -51,8 +51,8 @@ struct TileList {
 };
 
 // Builds the list with the whole CTA (warps x 32 threads), after the wait on
-// the preceding grid.  Offsets that do not ascend within the R rows are
-// reported; an expert that ends before it starts has no rows.
+// the preceding grid.  Offsets that do not ascend within the R rows are reported
+// and give an empty list: with others the tiles fit an int and every search ends.
 __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int T, int *smem, int warps) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, E = x.E, R = (int)x.p.M;
     int *const before = smem, *const row0 = smem + E + 1, *const sums = row0 + E + 1;
@@ -77,7 +77,7 @@ __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int
         if (lane >= o) sum += v;
     }
     if (lane == 31) sums[warp] = sum;
-    __syncthreads();
+    const bool none = __syncthreads_or(bad) != 0;
     int base = sum - mine, total = 0;
     for (int w = 0; w < warps; ++w) {
         if (w < warp) base += sums[w];
@@ -86,7 +86,7 @@ __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int
     for (int e = first; e < last; ++e) before[e] += base;
     if (t == 0) before[E] = total;
     __syncthreads();
-    return {before, row0, E, T, x.p.n_tiles, total * x.p.n_tiles};
+    return {before, row0, E, T, x.p.n_tiles, none ? 0 : total * x.p.n_tiles};
 }
 
 // The kernel of CTA pairs (gnq_expert_linear_pair.cu): out_type as in the ABI.

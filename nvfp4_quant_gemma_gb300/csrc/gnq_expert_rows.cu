@@ -77,16 +77,16 @@ __device__ __forceinline__ void fill_reciprocals(float2 (&tab)[128], int t) {
 }
 
 // The codes and scale byte of a block `v` with amax / 6 = sixth for global
-// scale g: the steps of epilogue_unit.  TABLE: worth its filling where a thread
-// takes several quotients (SiLU of 16384 x 2048 in expert order, one each: 31.4
+// scale g: the steps of epilogue_unit.  TABLE: for g that it serves, and worth its
+// filling where a thread takes several quotients (SiLU of 16384 x 2048 in expert order, one each: 31.4
 // us without, 34.0 with it).
 template <bool TABLE>
 __device__ __forceinline__ void nvfp4_block(const float (&v)[16], float sixth, float g, const float2 *tab, uint32_t &lo,
                                             uint32_t &hi, uint32_t &sf) {
     sf = e4m3x2(__fmul_rn(g, sixth), 0.f) & 0xFF;
-    float es, q0;
-    if (TABLE && quotient_table_serves(g)) {
-        const float2 r = tab[sf & 0x7F];
+    [[maybe_unused]] float es, q0;
+    if constexpr (TABLE) {
+        const float2 r = tab[sf];  // (g and amax are not below 0: no sign)
         es = div_fma(g, r.x, r.y, q0);
     } else {
         es = element_scale(g, sf);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
         // their reads run side by side; then all units of the token in this
         // warp take them in turn.  A warp holds one token, or parts of a few.
         const bool shared = p.x.scale_stride == 0;
-        if (shared) nvfp4_block<true>(v, sixth, ld_f32(p.x.scale), tab, lo, hi, sf);
+        if (shared) nvfp4_block<false>(v, sixth, ld_f32(p.x.scale), tab, lo, hi, sf);
         uint32_t left = __ballot_sync(0xffffffffu, ok);
         while (left) {
             const int token = __shfl_sync(0xffffffffu, m, __ffs(left) - 1);
@@ -171,16 +171,23 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
                 sf_row = expert_scale_row(at, o, row - o, Kp4);
             }
             const bool mine = ok && m == token;
-            for (uint32_t live = __ballot_sync(0xffffffffu, row >= 0); live; live &= live - 1) {
-                const int j = __ffs(live) - 1;
-                const int rj = __shfl_sync(0xffffffffu, row, j);
-                const int64_t sj = __shfl_sync(0xffffffffu, sf_row, j);
-                const float gj = __shfl_sync(0xffffffffu, g, j);
-                if (!mine) continue;
-                if (!shared) nvfp4_block<true>(v, sixth, gj, tab, lo, hi, sf);
-                st_v2(codes + (int64_t)rj * (p.H >> 1), lo, hi);
-                st_u8(scales + sj, sf);
-            }
+            auto take = [&](auto whole, auto table) {
+                for (uint32_t live = __ballot_sync(0xffffffffu, row >= 0); live; live &= live - 1) {
+                    const int j = __ffs(live) - 1;
+                    const int rj = __shfl_sync(0xffffffffu, row, j);
+                    const int64_t sj = __shfl_sync(0xffffffffu, sf_row, j);
+                    const float gj = __shfl_sync(0xffffffffu, g, j);
+                    if (!decltype(whole)::value && !mine) continue;
+                    if (!shared) nvfp4_block<decltype(table)::value>(v, sixth, gj, tab, lo, hi, sf);
+                    st_v2(codes + (int64_t)rj * (p.H >> 1), lo, hi);
+                    st_u8(scales + sj, sf);
+                }
+            };
+            // (the common case apart: a warp of one token, scales that the table serves)
+            const bool served = __all_sync(0xffffffffu, row < 0 || shared || quotient_table_serves(g));
+            if (served && __all_sync(0xffffffffu, mine)) take(std::true_type{}, std::true_type{});
+            else if (served) take(std::false_type{}, std::true_type{});
+            else take(std::false_type{}, std::false_type{});
             left &= ~__ballot_sync(0xffffffffu, mine);
         }
     } else {

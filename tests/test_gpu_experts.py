@@ -79,7 +79,7 @@ def _logits(M, E, dtype, seed, ties=False):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("M,E,k", [(0, 8, 2), (1, 1, 1), (1, 128, 8), (2, 33, 32), (3, 1024, 32), (64, 60, 4),
-                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6), (700, 8, 8), (4200, 1, 1), (6000, 1024, 2),
+                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6), (700, 8, 8), (4200, 1, 1), (2200, 1024, 2),
                                    (9001, 100, 3)])
 def test_route(gnq, M, E, k, dtype):
     for ties in (False, True):
@@ -500,7 +500,8 @@ def test_offsets_that_do_not_ascend_are_reported(gnq, bad):
     gnq.read_device_error()
     gnq.nvfp4_expert_linear(q.cuda(), sf.cuda(), wq.cuda(), wsf.cuda(), fp32([1.0]), o, out=y)
     torch.cuda.synchronize()
-    assert bad[0] == 2 or gnq.read_device_error() & 2
+    if bad[0] != 2:
+        assert gnq.read_device_error() & 2 and (u8(y) == SENT).all()
     x = torch.randn(R, K, device="cuda").to(torch.bfloat16)
     out = G((R, K // 2), torch.uint8), G((scale_rows(R, 3), K // 16), torch.float8_e4m3fn)
     gnq.expert_quantize(x, o, fp32([9.0]), out=out)
