@@ -14,9 +14,9 @@
 // place.  A tile of at most 192 rows takes whichever place the one before it
 // did not; two tiles of more in a row, and only those, wait for each other.
 //
-// A lane holds one weight row.  16-bit sums go through shared memory, where two
-// warps lay out 32 rows of y by 64 outputs (128 bytes), and leave as a tile
-// store of whole lines, or row by row at an expert's end (stores straight from
+// A lane holds one weight row.  16-bit sums go through shared memory, where each
+// warp lays out 32 rows of y by its 32 outputs (64 bytes), and leave as a tile
+// store of whole sectors, or row by row at an expert's end (stores straight from
 // the registers, 64 bytes of a row each: 258 us for 8192 tokens to 8 of 64
 // experts, N = 4096, K = 2048).  Rows that a tile store cannot take, and 4-byte
 // sums, whose rows are 128 bytes of a warp anyway, leave straight from registers.
@@ -38,7 +38,7 @@ constexpr int kStages = 5;
 constexpr int kPairWarps = 10;
 constexpr uint32_t kHalf = 128 * kStageK / 2;          // 128 rows of codes of one stage
 constexpr uint32_t kStage = 2 * kHalf + 4 * kBytesSf;  // per CTA: weight, rows, weight scales, three tiles of row scales
-constexpr uint32_t kBox = 32 * 128;                     // 32 rows x 128 bytes of y
+constexpr uint32_t kBox = 32 * 64;                     // 32 rows x 64 bytes of y
 constexpr uint32_t kPlaceCol = 256, kSfwCol = 448, kSfxCol = 464;  // tensor memory: second place, scales
 
 // y of up to 32 rows (columns of `acc`) x this lane's weight row n.
@@ -81,19 +81,6 @@ __device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, i
 // in which the warp takes no sums out (258 us against 202 in the case above).
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Barrier `id` of two warps; with a vote, which both get.
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool pair_all(int id, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-        "barrier.cta.red.and.pred.aligned q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
 }
 
 // Where a pair is in its work: the list's entries that it takes, each as one
@@ -197,7 +184,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
 
     pdl_wait();  // inputs may come from the preceding grid, outputs may still be read by it
     pdl_trigger();
-    const TileList list = build_tiles(x, kRows, reinterpret_cast<int *>(dyn + (base - dyn0) + kStages * kStage + 4 * kBox), kPairWarps);
+    const TileList list = build_tiles(x, kRows, reinterpret_cast<int *>(dyn + (base - dyn0) + kStages * kStage + 8 * kBox), kPairWarps);
 
     const int KT = (p.K64 + 3) / 4;
     auto gave_up = [&] { return *(volatile int *)&failed != 0; };
@@ -315,20 +302,17 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
     } else if (warp >= 2) {
         // ---- sums out ----
         // Warps 2-5 take rows 0-63 and 128-191 of a tile, warps 6-9 the
-        // others, 32 at a time.  Two warps share a box of 32 rows x 64 outputs.
+        // others, 32 at a time.
         const int quad = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
-        const int id = 1 + 2 * set + (quad >> 1);     // of the two warps' barrier
-        const bool lead = (quad & 1) == 0;
-        const uint32_t box = base + kStages * kStage + kBox * (id - 1);
+        const uint32_t box = base + kStages * kStage + kBox * (warp - 2);
         Walk w(blockIdx.x / 2, gridDim.x / 2);
         while (w.next(list, lane)) {
-            const int n0 = w.entry.n * kOutputs + 128 * rank + 32 * quad, n = n0 + lane, box_n = n0 & ~63;
+            const int n0 = w.entry.n * kOutputs + 128 * rank + 32 * quad, n = n0 + lane;
             const float alpha = ld_f32(p.alpha + w.e * x.alpha_stride);
             const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + (int64_t)w.e * p.N + n)) : 0.f;
             const bool ok = mbar_wait_bounded(acc_full(w.place), w.use() & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
-            __syncwarp();
-            if (!pair_all(id, ok)) {  // both go on, or neither
+            if (!__all_sync(0xffffffffu, ok)) {
                 give_up();
                 break;
             }
@@ -351,40 +335,32 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
                 O *const y = static_cast<O *>(p.y) + (int64_t)(w.row + c) * p.N;
                 if constexpr (sizeof(O) == 2) {
                     if (tiled) {
-                        if (lead && lane == 0) tma_store_wait<0>();
-                        __syncwarp();
-                        pair_sync(id);  // the box is free
-                        const uint32_t at = box + 2u * (lane & 7);
-                        const int unit = 4 * (quad & 1) + (lane >> 3);  // 16-byte unit of the row, before the swizzle
+                        if (lane == 0) tma_store_wait<0>();
+                        __syncwarp();  // the box is free
+                        const uint32_t at = box + 2u * lane;
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             const uint32_t two = Act<O>::pack2(fmaf(__uint_as_float(v[i]), alpha, bias),
                                                                fmaf(__uint_as_float(v[i + 1]), alpha, bias));
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 128u * i + 16u * (unit ^ (i & 7))),
-                                         "h"((uint16_t)two)
-                                         : "memory");
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 128u * (i + 1) + 16u * (unit ^ ((i + 1) & 7))),
-                                         "h"((uint16_t)(two >> 16))
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 64u * i), "h"((uint16_t)two) : "memory");
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 64u * (i + 1)), "h"((uint16_t)(two >> 16))
                                          : "memory");
                         }
                         if (live >= 32) fence_async_shared();
-                        __syncwarp();
-                        pair_sync(id);  // all of it is written
+                        __syncwarp();  // all of it is written
                         if (live >= 32) {
-                            if (lead && lane == 0) {
-                                if (box_n < p.N) tma_store_2d(&maps.y, box_n, w.row + c, box);
+                            if (lane == 0) {
+                                if (n0 < p.N) tma_store_2d(&maps.y, n0, w.row + c, box);
                                 tma_store_commit();
                             }
                         } else {
-                            // rows of the next expert stay: each row in one go of a warp
-                            const int col = box_n + 2 * lane;
+                            // rows of the next expert stay: two rows in one go
+                            const int col = n0 + 2 * (lane & 15);
                             O *const o = y + col;
                             if (col < p.N)
-                                for (int r = quad & 1; r < live; r += 2) {
+                                for (int r = lane >> 4; r < live; r += 2) {
                                     uint32_t two;
-                                    asm volatile("ld.shared.u32 %0, [%1];"
-                                                 : "=r"(two)
-                                                 : "r"(box + 128u * r + 16u * ((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+                                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(two) : "r"(box + 64u * r + 4u * (lane & 15)));
                                     *reinterpret_cast<uint32_t *>(o + (int64_t)r * p.N) = two;
                                 }
                         }
@@ -431,12 +407,12 @@ cudaError_t launch_expert_linear_pair(ExpertLinearParams x, const void *q, const
     const bool tiled = out_type != GNQ_FP32 && p.N % 8 == 0;  // rows of y are 16-byte aligned
     Maps m = {};
     bool ok = encode_codes(&m.w, w_q, E * p.N, K, 128) && encode_scales(&m.ws, p.w_sf, w_rows) &&
-              (!tiled || encode_output(&m.y, p.y, R, p.N, 2));
+              (!tiled || encode_output_half(&m.y, p.y, R, p.N));
     for (int i = 0; i < 3; ++i)
         ok = ok && encode_codes(&m.x[i], q, R, K, 32 << i) && encode_scale_tiles(&m.xs[i], p.x_sf, R / 128 + E, p.K64, i + 1);
     if (!ok) return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(tiles, sms / 2);
-    const size_t smem = 1024 + kStages * kStage + 4 * kBox + TileList::bytes(x.E, kPairWarps);
+    const size_t smem = 1024 + kStages * kStage + 8 * kBox + TileList::bytes(x.E, kPairWarps);
     if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, x, tiled, grid, smem, s);
     if (out_type == GNQ_FP16) return launch_pair<__half, __half>(m, x, tiled, grid, smem, s);
     if (bias_type == GNQ_FP16) return launch_pair<float, __half>(m, x, tiled, grid, smem, s);

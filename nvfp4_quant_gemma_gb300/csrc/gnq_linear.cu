@@ -354,6 +354,11 @@ bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size) {
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool encode_output_half(CUtensorMap *map, void *y, int64_t R, int64_t N) {
+    return encode_tiles(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, y, {(cuuint64_t)N, (cuuint64_t)R}, (cuuint64_t)N * 2, {32, 32},
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 namespace {
 
 // Shared memory of a split: half of an SM's where two stages fit it (two CTAs

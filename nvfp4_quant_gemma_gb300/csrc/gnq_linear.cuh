@@ -91,6 +91,9 @@ bool encode_scale_tiles(CUtensorMap *map, const void *scales, int64_t tiles, int
 // 32 rows x 128 bytes.
 bool encode_output(CUtensorMap *map, void *y, int64_t M, int64_t N, int size);
 
+// Map of a row-major (R, N) 16-bit output, stored in tiles of 32 rows x 64 bytes.
+bool encode_output_half(CUtensorMap *map, void *y, int64_t R, int64_t N);
+
 // The kernel of large batches (gnq_linear_pair.cu): out_type as in the ABI.
 cudaError_t launch_linear_pair(const LinearParams &p, const void *q, const void *w_q, int out_type,
                                int bias_type, int sms, cudaStream_t s);
