@@ -53,6 +53,8 @@ __global__ void __launch_bounds__(32 * kWarps) expert_linear_kernel(const __grid
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
     const uint32_t done = bar0 + 8u * (2 * kMaxStages + 4);
     if (warp == 0 && lane == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_x);
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);

@@ -159,6 +159,10 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
     const uint32_t done = bar0 + 8u * (2 * kStages + 4);
 
     if (warp == 0 && lane == 0) {
+        prefetch_map(&maps.w);
+        prefetch_map(&maps.ws);
+        prefetch_map(&maps.x[2]);
+        prefetch_map(&maps.xs[1]);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
