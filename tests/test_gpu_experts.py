@@ -485,6 +485,26 @@ def test_combine(gnq, M, H, k, add, Y, O):
     assert_within(out, want, err + rounding(want.abs() + err, ALL[O]), "out")
 
 
+@pytest.mark.parametrize("k", [2, 9])
+def test_combine_infinities_and_nan(gnq, k):
+    """An infinite or NaN element reaches its own result alone, with its sign;
+    a sum that overflows fp32 is infinite."""
+    M, H = 20, 64
+    g = torch.Generator().manual_seed(k)
+    y = torch.randn(M * k, H, generator=g)
+    slots = torch.arange(M * k).reshape(M, k)
+    w = torch.rand(M, k, generator=g) + 0.5
+    y[0, 3], y[k + 1, 5], y[2 * k, 7] = float("inf"), -float("inf"), float("nan")
+    y[3 * k:3 * k + 2, 9] = 3e38
+    y[4 * k, 11], y[4 * k + 1, 11] = float("inf"), -float("inf")
+    out = gnq.expert_combine(y.cuda(), slots.int().cuda(), w.cuda())
+    plain = (y[slots] * w[..., None]).sum(1)
+    odd = ~torch.isfinite(plain)
+    assert odd.sum() == 5 and torch.equal(torch.isfinite(out.cpu()), ~odd)
+    assert out[0, 3] == float("inf") and out[1, 5] == -float("inf") and out[3, 9] == float("inf")
+    assert bool(torch.isnan(out[2, 7])) and bool(torch.isnan(out[4, 11]))
+
+
 # ---------------------------------------------------------------------------
 # what the device finds
 # ---------------------------------------------------------------------------
