@@ -12,7 +12,15 @@
 // wastes neither tensor time nor row copies.  CTAs are persistent; each walks
 // the list of tiles, which it builds itself from the offsets, with one warp
 // copying, one issuing products and four taking sums out while the next tile's
-// products run.
+// products run.  (K-splitting clusters for a handful of rows, as the product of
+// one weight has them, gained only below 64 tiles: one token to 8 of 128 experts,
+// N = 2048, K = 4096, 11.2 us against 10.8.)
+//
+// What bounds it: the bytes of the weights that have rows, each read once.  64
+// tokens to 8 of 128 experts, N = 4096, K = 2048: 77 us of 73.7 at the copy rate (105
+// experts have rows); one token, N = 2048, K = 4096: 10.4 us of 5.6, launch, offsets,
+// first copy and last store; 301 tokens to 4 of 60, 1000 x 1088: 11.5 of 5.8, 480
+// tiles on 304 CTAs.
 #include <algorithm>
 
 #include "gemma_nq.h"

@@ -16,10 +16,18 @@
 //
 // A lane holds one weight row.  16-bit sums go through shared memory, where each
 // warp lays out 32 rows of y by its 32 outputs (64 bytes), and leave as a tile
-// store of whole sectors, or row by row at an expert's end (stores straight from
-// the registers, 64 bytes of a row each: 258 us for 8192 tokens to 8 of 64
-// experts, N = 4096, K = 2048).  Rows that a tile store cannot take, and 4-byte
-// sums, whose rows are 128 bytes of a warp anyway, leave straight from registers.
+// store of whole sectors, or row by row at an expert's end (8192 tokens to 8 of 64
+// experts, N = 4096, K = 2048: 233 us; 243 straight from the registers; 239 with
+// boxes of 128 bytes that two warps share, 277 with boxes of 16 rows).  Rows that
+// a tile store cannot take, and 4-byte sums, whose rows are 128 bytes of a warp
+// anyway, leave straight from registers.
+//
+// What bounds it: a stage is 36 to 40 KB into each SM, 590 cycles at 64 bytes a
+// cycle, and as much for its products and the scale copies into tensor memory; the
+// two meet with jitter at about 740.  The case above: 233 us, 4.7 PFLOP/s (the
+// product of one weight on as many rows, 65536 x 4096 x 2048: 228); 2048 tokens to 8
+// of 64, N = K = 4096: 164 us, where reading the weights and writing y take 114.
+// Copies that only prefetch into L2 take from the same 64 bytes (242 us).
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA), 2-9
 // take sums out: two warps for each 32 weight rows, 64 rows in turn.
@@ -77,8 +85,8 @@ __device__ __forceinline__ void store_rows(O *y, int64_t stride, int n, int N, i
 
 // Arrival that a product waits for: the sums are in registers (the tensor
 // memory fence before it says so) and nothing else has to be seen.  A release
-// would wait for the stores of y that are under way, two or three microseconds
-// in which the warp takes no sums out (258 us against 202 in the case above).
+// would wait for the stores of y that are under way, microseconds in which the
+// warp takes no sums out (291 us against 241 in the case above).
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

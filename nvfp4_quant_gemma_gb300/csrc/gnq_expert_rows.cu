@@ -7,11 +7,18 @@
 //   dequantize out = type(code * (block scale / global scale))
 //   combine    out[t] = type(sum_j w[t, j] y[slots[t, j]] + add[t])
 //
-// One pass, a few operations per byte: bound by HBM.  A thread owns whole
-// units (a 16-element block, a pair of blocks, 8 elements) of a flat index, so
-// rows of any width keep every lane busy.  The arithmetic that decides a code
-// is that of the norm kernels, so equal 16-bit values and scales give equal
-// codes whatever produced them.
+// One pass, a few operations per byte.  A thread owns whole units (a 16-element
+// block, a pair of blocks, 8 elements) of a flat index, so rows of any width keep
+// every lane busy.  The arithmetic that decides a code is that of the norm
+// kernels, so equal 16-bit values and scales give equal codes whatever produced
+// them.
+//
+// A token that goes to k experts is read once and written k times, each time
+// with the codes of that expert's scale.  Measured: bf16 8192 x 4096 to 8 experts
+// each 51 us (32 at the copy rate: 75 instructions per block and expert, 70 % of
+// the issue slots), 49 with one scale for all; SiLU of 16384 x 2048 29 us (25),
+// tanh-GELU 30, no activation 20 (12.6); back to bf16 15.2 us (15.4), fp32 33 (25), E4M3
+// 11.6 (10.3); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
 #include "gemma_nq.h"
 #include "gnq_elementwise.cuh"
 #include "gnq_expert.cuh"
