@@ -16,7 +16,8 @@
 // tokens: the CTA that picks a chunk leaves its counts in the slots that the
 // chunk will have (it has at least as many choices as there are experts), a
 // cluster turns them into first rows, an expert's slice per CTA, and a CTA per
-// chunk places its choices as above.
+// chunk places its choices as above.  (Where that makes fewer chunks than SMs,
+// the counting is a step of its own.)
 //
 // What bounds it: picking is instruction issue (420 warp instructions a token of 256
 // fp32 logits), placing latency.  16384 tokens: 256 fp32 logits, 8 choices 20.3 us, 128
@@ -272,13 +273,17 @@ __device__ __forceinline__ void pick_tokens(const RouteParams &p, int first, int
 }
 
 constexpr int kKeep = 4;        // groups of 32 choices whose place a warp keeps in registers
-constexpr int kSmallTokens = 64;       // up to here one launch
-constexpr int kOneCta = 32 * 32 * kKeep;  // choices that one CTA places
+// One launch up to so many tokens and logits: more are picked faster by several
+// SMs (E = 128: 16 tokens 3.3 us in one launch and 3.8 in two, 64 tokens 6.3 and 4.7).
+constexpr int kSmallTokens = 32, kSmallLogits = 4096;
+// Choices that one CTA places: 4096 take 8.7 us with the picks (E = 128, k = 8), 8192
+// took 12.7, and in chunks 16384 take 9.2.
+constexpr int kOneCta = 32 * 32 * kKeep;
 constexpr int kScanCtas = 8;
 constexpr int kPickWarps = 18;
 
 // Choices begin .. end - 1 by one CTA: the place of each among those of its
-// expert, plus first(expert).  hist: E words per warp.  `first` is called by
+// expert, plus first(expert).  hist: E words per warp, and E more.  `first` is called by
 // thread e for expert e (at least E threads) with the expert's count, by all
 // threads together.
 template <typename First>
@@ -315,24 +320,30 @@ __device__ __forceinline__ void place_choices(const RouteParams &p, int begin, i
         }
     }
     __syncthreads();
-    // counts -> prefix over the warps; one expert per thread
+    // counts -> prefix over the warps; one expert per thread, eight reads on
+    // their way at a time
     int total = 0;
     if (t < p.E)
-        for (int w = 0; w < busy; ++w) {
-            const int c = hist[w * p.E + t];
-            hist[w * p.E + t] = total;
-            total += c;
+        for (int w = 0; w < busy; w += 8) {
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = w + i < busy ? hist[(w + i) * p.E + t] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w + i < busy) hist[(w + i) * p.E + t] = total;
+                total += c[i];
+            }
         }
+    int32_t *const row0 = hist + W * p.E;
     const int row = first(total);
-    if (t < p.E)
-        for (int w = 0; w < busy; ++w) hist[w * p.E + t] += row;
+    if (t < p.E) row0[t] = row;
     __syncthreads();
     for (int base = from; base < to; base += 32 * kKeep) {
         if (!kept) read(base);
 #pragma unroll
         for (int g = 0; g < kKeep; ++g) {
             const int i = base + 32 * g + lane;
-            if (i < to) p.slots[i] = e[g] < 0 ? -1 : h[e[g]] + (kept ? at[g] : p.slots[i]);
+            if (i < to) p.slots[i] = e[g] < 0 ? -1 : row0[e[g]] + h[e[g]] + (kept ? at[g] : p.slots[i]);
         }
     }
 }
@@ -404,6 +415,22 @@ __global__ void __launch_bounds__(32 * kPickWarps) route_pick_kernel(const __gri
     if (!chunks) return;
     __syncthreads();
     for (int i = t; i < p.E; i += blockDim.x) p.slots[(int64_t)begin * p.k + i] = counts[i];
+}
+
+// The same counts from choices that other CTAs have picked.
+__global__ void __launch_bounds__(256) route_count_kernel(const __grid_constant__ RouteParams p, int chunk) {
+    extern __shared__ int32_t counts[];
+    pdl_wait();
+    pdl_trigger();
+    const int begin = blockIdx.x * chunk, end = (int)blockIdx.x + 1 < (int)gridDim.x ? begin + chunk : p.M;
+    for (int i = threadIdx.x; i < p.E; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    for (int i = begin * p.k + threadIdx.x; i < end * p.k; i += blockDim.x) {
+        const int e = p.experts[i];
+        if (e >= 0) atomicAdd(&counts[e], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.E; i += blockDim.x) p.slots[(int64_t)begin * p.k + i] = counts[i];
 }
 
 // Counts of the chunks -> first row of each chunk and expert, and the offsets.
@@ -486,9 +513,9 @@ template <typename L, int NV, bool WIDE> cudaError_t launch_route_form(const Rou
     const int hist = (p.E + 31) / 32;  // warps that hold a thread per expert
     auto one_cta = [&](auto fn, int warps) {
         const cudaError_t e = opt_in_dynamic_smem(reinterpret_cast<const void *>(fn));
-        return e != cudaSuccess ? e : launch(fn, 1, 32 * warps, (size_t)warps * p.E * 4, 1, s, p);
+        return e != cudaSuccess ? e : launch(fn, 1, 32 * warps, (size_t)(warps + 1) * p.E * 4, 1, s, p);
     };
-    if (p.M <= kSmallTokens) return one_cta(route_small_kernel<L, NV, WIDE>, std::max(hist, std::min(p.M, 32)));
+    if (p.M <= kSmallTokens && p.M * p.E <= kSmallLogits) return one_cta(route_small_kernel<L, NV, WIDE>, std::max(hist, std::min(p.M, 32)));
     const int n = p.M * p.k;
     cudaError_t e;
     auto pick = route_pick_kernel<L, NV, WIDE>;
@@ -500,12 +527,17 @@ template <typename L, int NV, bool WIDE> cudaError_t launch_route_form(const Rou
     const int chunk = std::max((p.E + p.k - 1) / p.k, (p.M + 2 * sms - 1) / (2 * sms)), chunks = p.M / chunk;
     int slice = 1;
     while (slice * kScanCtas < p.E) slice *= 2;
-    const int rounds = (chunk + kPickWarps - 1) / kPickWarps, pickers = (chunk + rounds - 1) / rounds;
-    if ((e = launch(pick, chunks, 32 * pickers, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
+    if (chunks >= sms) {
+        const int rounds = (chunk + kPickWarps - 1) / kPickWarps, pickers = (chunk + rounds - 1) / rounds;
+        if ((e = launch(pick, chunks, 32 * pickers, (size_t)p.E * 4, 1, s, p, chunk, chunks)) != cudaSuccess) return e;
+    } else {  // chunks of many experts are too few to pick in (2048 tokens of 1024 experts: 45.7 us so)
+        if ((e = launch(pick, (p.M + 7) / 8, 256, 0, 1, s, p, 8, 0)) != cudaSuccess) return e;
+        if ((e = launch(route_count_kernel, chunks, 256, (size_t)p.E * 4, 1, s, p, chunk)) != cudaSuccess) return e;
+    }
     if ((e = launch(route_scan_kernel, kScanCtas, 1024, 0, kScanCtas, s, p, chunk, chunks, slice)) != cudaSuccess) return e;
     const int warps = std::max(hist, 8);
     if ((e = opt_in_dynamic_smem(reinterpret_cast<const void *>(route_place_kernel))) != cudaSuccess) return e;
-    return launch(route_place_kernel, chunks, 32 * warps, (size_t)warps * p.E * 4, 1, s, p, chunk);
+    return launch(route_place_kernel, chunks, 32 * warps, (size_t)(warps + 1) * p.E * 4, 1, s, p, chunk);
 }
 
 template <typename L, int NV> cudaError_t launch_route(const RouteParams &p, int sms, cudaStream_t s) {

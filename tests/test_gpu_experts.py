@@ -79,7 +79,7 @@ def _logits(M, E, dtype, seed, ties=False):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("M,E,k", [(0, 8, 2), (1, 1, 1), (1, 128, 8), (2, 33, 32), (3, 1024, 32), (64, 60, 4),
-                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6), (700, 8, 8), (4200, 1, 1), (2200, 1024, 2),
+                                   (65, 60, 4), (257, 256, 8), (1000, 31, 1), (130, 1000, 7), (5000, 257, 6), (700, 8, 8), (4200, 1, 1), (2200, 1024, 2), (33, 100, 3), (32, 129, 4), (1025, 256, 8),
                                    (9001, 100, 3)])
 def test_route(gnq, M, E, k, dtype):
     for ties in (False, True):
