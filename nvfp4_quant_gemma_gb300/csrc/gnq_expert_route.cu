@@ -20,8 +20,8 @@
 // the counting is a step of its own.)
 //
 // What bounds it: picking is instruction issue (420 warp instructions a token of 256
-// fp32 logits), placing latency.  16384 tokens: 256 fp32 logits, 8 choices 20.3 us, 128
-// bf16 logits 17.6, 64 and 2 choices 13.9; 65536 of the first 56 us (1.2 TB/s of logits);
+// fp32 logits), placing latency.  16384 tokens: 256 fp32 logits, 8 choices 20 us, 128
+// bf16 logits 17, 64 and 2 choices 13.9; 65536 of the first 56 us (1.2 TB/s of logits);
 // one token 2.4 us.  One CTA or cluster that places all 131072 choices took 22 us by
 // itself, the chunks' two steps take 9.
 #include <algorithm>
