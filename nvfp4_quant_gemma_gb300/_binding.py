@@ -706,14 +706,17 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
             out = _expert_buffers(R, rows, H, x)
         q, bs = out
         g = scale.numel()
-        ok = (dev >= 0 and dev == _current_device() and offsets.dim() == 1 and _ints_ok(dev, offsets, 2)
-              and (g == E or g == 1) and _floats_ok(dev, scale, 1)
-              and (slots is None or (slots.shape == (M, k) and experts.shape == (M, k) and _ints_ok(dev, slots, R)
-                                     and _ints_ok(dev, experts, R)))
+        per_expert = 1 if g == E else 0
+        ok = (dev >= 0 and dev == _current_device() and E > 0 and (g == E or g == 1)
+              and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
+              and scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev
+              and (slots is None or (slots.shape == (M, k) and slots.dtype is _I32 and slots.is_contiguous()
+                                     and slots.get_device() == dev and experts.shape == slots.shape
+                                     and experts.dtype is _I32 and experts.is_contiguous()
+                                     and experts.get_device() == dev))
               and q.dtype is _U8 and q.is_contiguous() and q.nbytes >= R * H // 2 and q.get_device() == dev
               and bs.dtype in (_E4M3, _U8) and bs.is_contiguous() and bs.nbytes >= rows * (H // 16)
               and bs.get_device() == dev)
-        per_expert = 1 if g == E else 0
     except (AttributeError, TypeError, ValueError, IndexError):
         ok = False
     if not ok:
@@ -766,12 +769,13 @@ def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None,
         if out is None and dev >= 0:
             out = torch.empty((R, K), dtype=dtype or torch.bfloat16, device=q.device)
         g = 1 if scale is None else scale.numel()
-        ok = (dev >= 0 and dev == _current_device() and offsets.dim() == 1 and _ints_ok(dev, offsets, 2)
-              and (g == E or g == 1) and (scale is None or _floats_ok(dev, scale, 1))
+        per_expert = 1 if scale is not None and g == E else 0
+        ok = (dev >= 0 and dev == _current_device() and E > 0 and (g == E or g == 1)
+              and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
+              and (scale is None or (scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev))
               and _expert_packed_ok(dev, E, q, block_scale) and out.dtype in _OUT_TYPE
               and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.numel() >= R * K
               and out.get_device() == dev)
-        per_expert = 1 if scale is not None and g == E else 0
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
