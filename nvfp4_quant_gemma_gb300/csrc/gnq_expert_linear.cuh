@@ -37,7 +37,10 @@ struct TileList {
             above = __ballot_sync(0xffffffffu, e + lane < E && tiles_before[e + lane + 1] > q);
             if (above) break;
         }
-        e += __ffs(above) - 1;
+        return of(i, e + __ffs(above) - 1);
+    }
+    // Tile `i`, which is of expert `e`.
+    __device__ __forceinline__ Tile of(int i, int e) const {
         const int before = tiles_before[e], tiles = tiles_before[e + 1] - before;
         const int j = i - before * n_tiles, n = (int)((unsigned)j / (unsigned)tiles), t = j - n * tiles;
         Tile x;

@@ -14,23 +14,33 @@
 // place.  A tile of at most 192 rows takes whichever place the one before it
 // did not; two tiles of more in a row, and only those, wait for each other.
 //
+// Pairs take entries of the list in rounds, one each, and a warp of every CTA deals
+// them: of the entries of a round the largest goes to the pair that has been dealt
+// the least, and so on.  What runs at a time stays as near together as in the
+// order of the list, and no pair ends much later than another.  (The experts'
+// rows differ widely, and of some tens of entries in plain order the fullest pair had
+// 15 to 60 % more than the average, now 2 to 10 %.  The two cases below took 235
+// and 164 us in plain order, 229 and 145 dealt out; 257 and 159 with all entries by
+// falling rows, which reads weights twice; 291 and 189 with each pair's share in
+// one piece, where pairs that run at a time share nothing.)
+//
 // A lane holds one weight row.  16-bit sums go through shared memory, where each
 // warp lays out 32 rows of y by its 32 outputs (64 bytes), and leave as a tile
 // store of whole sectors, or row by row at an expert's end (8192 tokens to 8 of 64
-// experts, N = 4096, K = 2048: 233 us; 243 straight from the registers; 239 with
-// boxes of 128 bytes that two warps share, 277 with boxes of 16 rows).  Rows that
+// experts, N = 4096, K = 2048, before the deal: 233 us; 243 straight from the registers; 239
+// with boxes of 128 bytes that two warps share, 277 with boxes of 16 rows).  Rows that
 // a tile store cannot take, and 4-byte sums, whose rows are 128 bytes of a warp
 // anyway, leave straight from registers.
 //
 // What bounds it: a stage is 36 to 40 KB into each SM, 590 cycles at 64 bytes a
 // cycle, and as much for its products and the scale copies into tensor memory; the
-// two meet with jitter at about 740.  The case above: 233 us, 4.7 PFLOP/s (the
+// two meet with jitter at about 740.  The case above: 229 us, 4.8 PFLOP/s (the
 // product of one weight on as many rows, 65536 x 4096 x 2048: 228); 2048 tokens to 8
-// of 64, N = K = 4096: 164 us, where reading the weights and writing y take 114.
+// of 64, N = K = 4096: 145 us, where reading the weights and writing y take 114.
 // Copies that only prefetch into L2 take from the same 64 bytes (242 us).
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA), 2-9
-// take sums out: two warps for each 32 weight rows, 64 rows in turn.
+// take sums out: two warps for each 32 weight rows, 64 rows in turn; 10 deals.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -43,7 +53,8 @@ constexpr int kOutputs = 256;                 // weight rows of a tile
 constexpr int kFirst = 256, kSecond = 192;    // rows of the two tiles that one entry of the list stands for
 constexpr int kRows = kFirst + kSecond;
 constexpr int kStages = 5;
-constexpr int kPairWarps = 10;
+constexpr int kPairWarps = 11;
+constexpr int kMaxPairs = 96;
 constexpr uint32_t kHalf = 128 * kStageK / 2;          // 128 rows of codes of one stage
 constexpr uint32_t kStage = 2 * kHalf + 4 * kBytesSf;  // per CTA: weight, rows, weight scales, three tiles of row scales
 constexpr uint32_t kBox = 32 * 64;                     // 32 rows x 64 bytes of y
@@ -91,32 +102,54 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Where a pair is in its work: the list's entries that it takes, each as one
-// or two tiles, and the place in tensor memory of each tile.
-struct Walk {
-    int item, step, e;      // entry, entries from one to the next, its expert
-    TileList::Tile entry;
-    int at;                 // first row of the tile in its entry
-    int row, rows;          // first row and rows of the tile
-    int place;              // 0: columns 0-255, 1: 256-447
-    int use0, use1;         // tiles that have taken each place before this one
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
-    __device__ __forceinline__ Walk(int first, int step) : item(first - step), step(step), e(0), at(0), row(0), rows(0), place(1), use0(0), use1(-1) {
-        entry.rows = 0;
-    }
+// What a tile takes, in the time that 32 rows of a stage take: the weight's side
+// of its stages counts as eight of those.
+// An entry of more than 256 rows is two tiles.
+__device__ __forceinline__ int cost_of(int rows) { return (rows > kFirst ? 16 : 8) + (rows + 31) / 32; }
+
+// What the deal hands to the other warps of its CTA: a weight tile and up to 448
+// rows of an expert; rows = 0 behind the last.
+struct __align__(16) Entry {
+    int e, n, at, rows;  // expert, weight tile, first row in the expert, rows
+};
+constexpr int kRing = 4;
+struct Ring {
+    const Entry *slots;
+    uint32_t bars;  // dealt [kRing], then taken [kRing]
+    __device__ __forceinline__ uint32_t dealt(int i) const { return bars + 8u * i; }
+    __device__ __forceinline__ uint32_t taken(int i) const { return bars + 8u * (kRing + i); }
+};
+
+// Where a pair is in its work: the entries dealt to it, each as one or two
+// tiles, and the place in tensor memory of each tile.
+struct Walk {
+    int i = -1;                   // entries taken before this one
+    Entry entry = {0, 0, 0, 0};
+    int in = 0;                   // first row of the tile in its entry
+    int at = 0, rows = 0;         // first row of the tile in its expert, rows
+    int place = 1;                // 0: columns 0-255, 1: 256-447
+    int use0 = 0, use1 = -1;      // tiles that have taken each place before this one
+
     // The next tile, by a converged warp; false behind the last.
-    __device__ __forceinline__ bool next(const TileList &list, int lane) {
+    __device__ __forceinline__ bool next(const Ring &ring, int lane, long long limit, bool &ok) {
         (place ? use1 : use0) += 1;
-        at += kFirst;
-        if (at >= entry.rows) {
-            item += step;
-            if (item >= list.count) return false;
-            entry = list.at(item, e, lane);
-            e = entry.e;
-            at = 0;
+        in += kFirst;
+        if (in >= entry.rows) {
+            ++i;
+            ok = warp_wait_bounded(ring.dealt(i % kRing), i / kRing & 1, limit);
+            if (!ok) return false;
+            entry = ring.slots[i % kRing];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ring.taken(i % kRing));
+            if (entry.rows == 0) return false;
+            in = 0;
         }
-        row = entry.row + at;
-        rows = min(kFirst, entry.rows - at);
+        at = entry.at + in;
+        rows = min(kFirst, entry.rows - in);
         place = rows > kSecond ? 0 : place ^ 1;
         return true;
     }
@@ -125,7 +158,7 @@ struct Walk {
     __device__ __forceinline__ int half() const { return (rows + 31) / 32 * 16; }
     // 32-row groups of the tile's first scale tile before its first row, and
     // the scale tiles that it touches.
-    __device__ __forceinline__ int shift() const { return ((row - entry.start) & 127) >> 5; }
+    __device__ __forceinline__ int shift() const { return (at & 127) >> 5; }
     __device__ __forceinline__ int scale_tiles() const { return (shift() + (rows + 31) / 32 + 3) / 4; }
 };
 
@@ -146,12 +179,15 @@ __device__ __forceinline__ void tma_load_tiles(uint32_t dst, const CUtensorMap *
 }
 
 template <typename O, typename B>
-__global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(const __grid_constant__ Maps maps,
+__global__ void __launch_bounds__(32 * kPairWarps, 1) expert_linear_pair_kernel(const __grid_constant__ Maps maps,
                                                                              const __grid_constant__ ExpertLinearParams x,
                                                                              bool tiled) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ __align__(16) uint4 topup[kStages];
+    __shared__ Entry slots[kRing];
+    __shared__ __align__(16) uint32_t sizes[kMaxPairs], loads[kMaxPairs], by_size[kMaxPairs];  // of the deal
+    __shared__ __align__(8) uint64_t ring_bars[2 * kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
@@ -165,6 +201,8 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };      // each CTA's: a tile's sums are ready
     auto acc_free = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };  // first CTA's: they are out
     const uint32_t done = bar0 + 8u * (2 * kStages + 4);
+
+    const Ring ring = {slots, (uint32_t)__cvta_generic_to_shared(ring_bars)};
 
     if (warp == 0 && lane == 0) {
         prefetch_map(&maps.w);
@@ -180,6 +218,10 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
             mbar_init(acc_free(b), 16);
         }
         mbar_init(done, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(ring.dealt(i), 1);
+            mbar_init(ring.taken(i), rank == 0 ? 10 : 9);  // copies, sums, the first CTA's products
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         failed = 0;
     }
@@ -204,20 +246,26 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
         atomicOr(p.err, (unsigned)DEVERR_WAIT_TIMEOUT);
         *(volatile int *)&failed = 1;
     };
+    auto next = [&](Walk &w) {
+        bool ok = true;
+        const bool more = w.next(ring, lane, 2 * p.wait_limit, ok);
+        if (!ok) give_up();
+        return more;
+    };
     if (warp == 0) {
         // ---- copies ----
         int it = 0, s = 0;
         uint32_t parity = 1;  // of the wait on `empty`: passes at once in the first round
         const int sf_rows = (p.N + 127) / 128;
-        Walk w(blockIdx.x / 2, gridDim.x / 2);
-        while (!__any_sync(0xffffffffu, gave_up()) && w.next(list, lane)) {
-            const int half = w.half(), x0 = w.row + half * rank, sf_tiles = w.scale_tiles();
+        Walk w;
+        while (!__any_sync(0xffffffffu, gave_up()) && next(w)) {
+            const int half = w.half(), x0 = list.row0[w.entry.e] + w.at + half * rank, sf_tiles = w.scale_tiles();
             const int box = half > 64 ? 2 : half > 32 ? 1 : 0;
             const CUtensorMap *const map_x = &maps.x[box], *const map_xs = &maps.xs[sf_tiles - 1];
             const uint32_t bytes = kHalf + (4096u << box) + (1 + sf_tiles) * kBytesSf;
-            const int w0 = w.e * p.N + w.entry.n * kOutputs + 128 * rank;
-            const int ws = (w.e * sf_rows + 2 * w.entry.n + rank) * p.K64;
-            const int xs = (w.entry.start >> 7) + w.e + ((w.row - w.entry.start) >> 7);
+            const int w0 = w.entry.e * p.N + w.entry.n * kOutputs + 128 * rank;
+            const int ws = (w.entry.e * sf_rows + 2 * w.entry.n + rank) * p.K64;
+            const int xs = (list.row0[w.entry.e] >> 7) + w.entry.e + (w.at >> 7);
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 if (!warp_wait_bounded(empty(s), parity, p.wait_limit)) {
                     give_up();
@@ -251,7 +299,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
         int s = 0;
         uint32_t parity = 0;
         bool good = true;
-        Walk w(blockIdx.x / 2, gridDim.x / 2);
+        Walk w;
         // One tile with SF scale tiles of its rows: the loop that limits a
         // pair, so nothing in it branches or is worked out twice.
         auto tile = [&](auto sf) {
@@ -296,7 +344,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
                 if (++s == kStages) s = 0, parity ^= 1;
             }
         };
-        while (good && w.next(list, lane)) {
+        while (good && next(w)) {
             if (!warp_wait_bounded(acc_free(w.place), (w.use() & 1) ^ 1, p.wait_limit)) {
                 give_up();
                 break;
@@ -311,6 +359,78 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
         if (elect_one()) tc_commit_pair(done);
         __syncwarp();
         if (!mbar_wait_bounded(done, 0, p.wait_limit)) give_up();
+    } else if (warp == kPairWarps - 1) {
+        // ---- deal ----
+        // Each CTA plays the whole deal by itself (about 2000 cycles a round), a
+        // lane for three pairs and for three entries of a round.
+        const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+        constexpr int per = kMaxPairs / 32;
+        uint32_t load[per];  // of pair 32 i + lane: what it has x 128, and its number
+        int e[per] = {};     // expert of the entry in the last round
+#pragma unroll
+        for (int i = 0; i < per; ++i) load[i] = 32 * i + lane < pairs ? 32 * i + lane : ~0u;
+        int put = 0;
+        for (int first = 0;; first += pairs) {
+            // entry first + 32 i + lane: its cost and number, falling (0: none)
+            Entry entry[per];
+            uint32_t size[per];
+            int low = 0x7fffffff;
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const int number = 32 * i + lane, item = first + number;
+                size[i] = number < pairs ? 127 - number : 0;
+                if (number < pairs && item < list.count) {
+                    while (list.tiles_before[e[i] + 1] * list.n_tiles <= item) ++e[i];
+                    const TileList::Tile tile = list.of(item, e[i]);
+                    entry[i] = {tile.e, tile.n, tile.row - tile.start, tile.rows};
+                    size[i] += 128 * cost_of(tile.rows);
+                }
+                sizes[number] = size[i];
+                loads[number] = load[i];
+                if (number < pairs) low = min(low, (int)(load[i] / 128));
+            }
+            low = 128 * __reduce_min_sync(0xffffffffu, low);
+            __syncwarp();
+            int of_size[per] = {}, of_load[per] = {};  // ranks
+            for (int j = 0; j < pairs; j += 4) {
+                const uint4 s = *reinterpret_cast<const uint4 *>(sizes + j), l = *reinterpret_cast<const uint4 *>(loads + j);
+#pragma unroll
+                for (int i = 0; i < per; ++i) {
+                    of_size[i] += (s.x > size[i]) + (s.y > size[i]) + (s.z > size[i]) + (s.w > size[i]);
+                    of_load[i] += (l.x < load[i]) + (l.y < load[i]) + (l.z < load[i]) + (l.w < load[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                if (32 * i + lane < pairs) by_size[of_size[i]] = size[i] & ~127u;
+            __syncwarp();
+            int mine = 0;  // rank of this pair
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                if (32 * i + lane >= pairs) continue;
+                if (32 * i + lane == pair) mine = of_load[i];
+                load[i] += by_size[of_load[i]] - low;
+            }
+            mine = __shfl_sync(0xffffffffu, mine, pair & 31);
+            const bool more = by_size[mine] > 0;
+            if (!warp_wait_bounded(ring.taken(put % kRing), (put / kRing & 1) ^ 1, 2 * p.wait_limit)) give_up();
+            if (__any_sync(0xffffffffu, gave_up())) break;
+            bool put_it = !more && lane == 0;
+            Entry own = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                if (more && 32 * i + lane < pairs && of_size[i] == mine) {
+                    own = entry[i];
+                    put_it = true;
+                }
+            if (put_it) {
+                slots[put % kRing] = own;
+                mbar_arrive(ring.dealt(put % kRing));
+            }
+            __syncwarp();
+            ++put;
+            if (!more) break;
+        }
     } else if (warp >= 2) {
         // ---- sums out ----
         // Warps 2-5 take rows 0-63 and 128-191 of a tile, warps 6-9 the
@@ -318,11 +438,12 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
         const int quad = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;  // 32 lanes per warp, lane number in bits 16-31
         const uint32_t box = base + kStages * kStage + kBox * (warp - 2);
-        Walk w(blockIdx.x / 2, gridDim.x / 2);
-        while (w.next(list, lane)) {
+        Walk w;
+        while (next(w)) {
             const int n0 = w.entry.n * kOutputs + 128 * rank + 32 * quad, n = n0 + lane;
-            const float alpha = ld_f32(p.alpha + w.e * x.alpha_stride);
-            const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + (int64_t)w.e * p.N + n)) : 0.f;
+            const float alpha = ld_f32(p.alpha + w.entry.e * x.alpha_stride);
+            const float bias = p.bias && n < p.N ? OutType<B>::bias(ld_u16(p.bias + (int64_t)w.entry.e * p.N + n)) : 0.f;
+            const int row = list.row0[w.entry.e] + w.at;
             const bool ok = mbar_wait_bounded(acc_full(w.place), w.use() & 1, 2 * p.wait_limit) && !(p.tx_extra && gave_up());
             if (!__all_sync(0xffffffffu, ok)) {
                 give_up();
@@ -344,7 +465,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
                     if (lane == 0) arrive_relaxed(map_to_cta(acc_free(w.place), 0));
                 }
                 if (live <= 0) continue;
-                O *const y = static_cast<O *>(p.y) + (int64_t)(w.row + c) * p.N;
+                O *const y = static_cast<O *>(p.y) + (int64_t)(row + c) * p.N;
                 if constexpr (sizeof(O) == 2) {
                     if (tiled) {
                         if (lane == 0) tma_store_wait<0>();
@@ -362,7 +483,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) expert_linear_pair_kernel(con
                         __syncwarp();  // all of it is written
                         if (live >= 32) {
                             if (lane == 0) {
-                                if (n0 < p.N) tma_store_2d(&maps.y, n0, w.row + c, box);
+                                if (n0 < p.N) tma_store_2d(&maps.y, n0, row + c, box);
                                 tma_store_commit();
                             }
                         } else {
@@ -423,7 +544,7 @@ cudaError_t launch_expert_linear_pair(ExpertLinearParams x, const void *q, const
     for (int i = 0; i < 3; ++i)
         ok = ok && encode_codes(&m.x[i], q, R, K, 32 << i) && encode_scale_tiles(&m.xs[i], p.x_sf, R / 128 + E, p.K64, i + 1);
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t grid = 2 * std::min<int64_t>(tiles, sms / 2);
+    const int64_t grid = 2 * std::min<int64_t>(tiles, std::min(sms / 2, kMaxPairs));
     const size_t smem = 1024 + kStages * kStage + 8 * kBox + TileList::bytes(x.E, kPairWarps);
     if (out_type == GNQ_BF16) return launch_pair<__nv_bfloat16, __nv_bfloat16>(m, x, tiled, grid, smem, s);
     if (out_type == GNQ_FP16) return launch_pair<__half, __half>(m, x, tiled, grid, smem, s);
