@@ -367,6 +367,21 @@ def test_linear_both_kernels(gnq, counts, N, K, T, bias):
     assert torch.equal(got[0][:sum(counts)], got[1][:sum(counts)])
 
 
+@pytest.mark.parametrize("counts", [[i * 7 % 5 for i in range(1024)], [450 * (i % 7 == 3) + i * 31 % 70 for i in range(100)],
+                                    [0] * 40 + [9000] + [0] * 40 + [5], [40] * 300])
+@pytest.mark.parametrize("N,K", [(264, 128), (1100, 64)])
+def test_linear_both_kernels_over_many_tiles(gnq, counts, N, K):
+    """Each CTA takes several tiles, of experts of very different sizes."""
+    got = []
+    for kernel in (1, 2):
+        gnq.set_linear_policy(kernel)
+        try:
+            got.append(_run_linear(gnq, counts, N, K, torch.bfloat16, seed=K)[3])
+        finally:
+            gnq.set_linear_policy(0)
+    assert torch.equal(got[0][:sum(counts)], got[1][:sum(counts)])
+
+
 def test_linear_wait_timeout_in_both_kernels(gnq):
     for kernel in (1, 2):
         for counts in ([3, 0, 2], [700, 0, 600]):
