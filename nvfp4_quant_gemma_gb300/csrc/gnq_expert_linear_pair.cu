@@ -14,8 +14,8 @@
 // place.  A tile of at most 192 rows takes whichever place the one before it
 // did not; two tiles of more in a row, and only those, wait for each other.
 //
-// Pairs take entries of the list in rounds, one each, and a warp of every CTA deals
-// them: of the entries of a round the largest goes to the pair that has been dealt
+// Pairs take entries of the list in rounds, one each, and three warps of every CTA
+// deal them: of the entries of a round the largest goes to the pair that has been dealt
 // the least, and so on.  What runs at a time stays as near together as in the
 // order of the list, and no pair ends much later than another.  (The experts'
 // rows differ widely, and of some tens of entries in plain order the fullest pair had
@@ -40,7 +40,8 @@
 // Copies that only prefetch into L2 take from the same 64 bytes (242 us).
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA), 2-9
-// take sums out: two warps for each 32 weight rows, 64 rows in turn; 10 deals.
+// take sums out: two warps for each 32 weight rows, 64 rows in turn; 10-12
+// deal.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -53,8 +54,8 @@ constexpr int kOutputs = 256;                 // weight rows of a tile
 constexpr int kFirst = 256, kSecond = 192;    // rows of the two tiles that one entry of the list stands for
 constexpr int kRows = kFirst + kSecond;
 constexpr int kStages = 5;
-constexpr int kPairWarps = 11;
-constexpr int kMaxPairs = 96;
+constexpr int kMaxPairs = 96;                 // (of the 76 that the machine has)
+constexpr int kDealWarp = 10, kPairWarps = kDealWarp + kMaxPairs / 32;
 constexpr uint32_t kHalf = 128 * kStageK / 2;          // 128 rows of codes of one stage
 constexpr uint32_t kStage = 2 * kHalf + 4 * kBytesSf;  // per CTA: weight, rows, weight scales, three tiles of row scales
 constexpr uint32_t kBox = 32 * 64;                     // 32 rows x 64 bytes of y
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(32 * kPairWarps, 1) expert_linear_pair_kernel(
     __shared__ __align__(16) uint4 topup[kStages];
     __shared__ Entry slots[kRing];
     __shared__ __align__(16) uint32_t sizes[kMaxPairs], loads[kMaxPairs], by_size[kMaxPairs];  // of the deal
+    __shared__ int rank_of_pair, stop;
     __shared__ __align__(8) uint64_t ring_bars[2 * kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(32 * kPairWarps, 1) expert_linear_pair_kernel(
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         failed = 0;
+        stop = 0;
     }
     if (warp == 1) {
         tmem_alloc<2>((uint32_t)__cvta_generic_to_shared(&tmem_slot), 512);
@@ -359,75 +362,62 @@ __global__ void __launch_bounds__(32 * kPairWarps, 1) expert_linear_pair_kernel(
         if (elect_one()) tc_commit_pair(done);
         __syncwarp();
         if (!mbar_wait_bounded(done, 0, p.wait_limit)) give_up();
-    } else if (warp == kPairWarps - 1) {
+    } else if (warp >= kDealWarp) {
         // ---- deal ----
-        // Each CTA plays the whole deal by itself (about 2000 cycles a round), a
-        // lane for three pairs and for three entries of a round.
-        const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-        constexpr int per = kMaxPairs / 32;
-        uint32_t load[per];  // of pair 32 i + lane: what it has x 128, and its number
-        int e[per] = {};     // expert of the entry in the last round
-#pragma unroll
-        for (int i = 0; i < per; ++i) load[i] = 32 * i + lane < pairs ? 32 * i + lane : ~0u;
+        // Each CTA plays the whole deal by itself, a thread for each pair and
+        // for each entry of a round.
+        const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, number = threadIdx.x - 32 * kDealWarp;
+        auto sync = [] {
+            __syncwarp();
+            asm volatile("bar.sync 1, %0;" ::"n"(kMaxPairs) : "memory");
+        };
+        uint32_t load = number < pairs ? number : ~0u;  // of pair `number`: what it has x 128, and its number
+        int e = 0;                                      // expert of the last round's entry
         int put = 0;
         for (int first = 0;; first += pairs) {
-            // entry first + 32 i + lane: its cost and number, falling (0: none)
-            Entry entry[per];
-            uint32_t size[per];
-            int low = 0x7fffffff;
-#pragma unroll
-            for (int i = 0; i < per; ++i) {
-                const int number = 32 * i + lane, item = first + number;
-                size[i] = number < pairs ? 127 - number : 0;
-                if (number < pairs && item < list.count) {
-                    while (list.tiles_before[e[i] + 1] * list.n_tiles <= item) ++e[i];
-                    const TileList::Tile tile = list.of(item, e[i]);
-                    entry[i] = {tile.e, tile.n, tile.row - tile.start, tile.rows};
-                    size[i] += 128 * cost_of(tile.rows);
-                }
-                sizes[number] = size[i];
-                loads[number] = load[i];
-                if (number < pairs) low = min(low, (int)(load[i] / 128));
+            // cost and number of the entry first + number, falling (cost 0: there is none)
+            Entry entry = {0, 0, 0, 0};
+            uint32_t size = number < pairs ? 127 - number : 0;
+            if (number < pairs && first + number < list.count) {
+                while (list.tiles_before[e + 1] * list.n_tiles <= first + number) ++e;
+                const TileList::Tile tile = list.of(first + number, e);
+                entry = {tile.e, tile.n, tile.row - tile.start, tile.rows};
+                size += 128 * cost_of(tile.rows);
             }
-            low = 128 * __reduce_min_sync(0xffffffffu, low);
-            __syncwarp();
-            int of_size[per] = {}, of_load[per] = {};  // ranks
-            for (int j = 0; j < pairs; j += 4) {
-                const uint4 s = *reinterpret_cast<const uint4 *>(sizes + j), l = *reinterpret_cast<const uint4 *>(loads + j);
-#pragma unroll
-                for (int i = 0; i < per; ++i) {
-                    of_size[i] += (s.x > size[i]) + (s.y > size[i]) + (s.z > size[i]) + (s.w > size[i]);
-                    of_load[i] += (l.x < load[i]) + (l.y < load[i]) + (l.z < load[i]) + (l.w < load[i]);
+            sizes[number] = size;
+            loads[number] = load;
+            sync();
+            if (stop) break;  // the same for all: it is written behind the second sync only
+            // their ranks; the first round as it comes, for an early start
+            int of_size = number, of_load = number;
+            if (first > 0) {
+                of_size = of_load = 0;
+#pragma unroll 4
+                for (int j = 0; j < pairs; j += 4) {
+                    const uint4 s = *reinterpret_cast<const uint4 *>(sizes + j), l = *reinterpret_cast<const uint4 *>(loads + j);
+                    of_size += (s.x > size) + (s.y > size) + (s.z > size) + (s.w > size);
+                    of_load += (l.x < load) + (l.y < load) + (l.z < load) + (l.w < load);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < per; ++i)
-                if (32 * i + lane < pairs) by_size[of_size[i]] = size[i] & ~127u;
-            __syncwarp();
-            int mine = 0;  // rank of this pair
-#pragma unroll
-            for (int i = 0; i < per; ++i) {
-                if (32 * i + lane >= pairs) continue;
-                if (32 * i + lane == pair) mine = of_load[i];
-                load[i] += by_size[of_load[i]] - low;
-            }
-            mine = __shfl_sync(0xffffffffu, mine, pair & 31);
+            // (no two pairs are further apart than an entry's cost, so this
+            // leaves no load below 0, and none grows out of 32 bits)
+            const uint32_t less = max((int)(loads[0] / 128) - 64, 0) * 128;
+            if (number < pairs) by_size[of_size] = size & ~127u;
+            if (number == pair) rank_of_pair = of_load;
+            sync();
+            const int mine = rank_of_pair;
             const bool more = by_size[mine] > 0;
-            if (!warp_wait_bounded(ring.taken(put % kRing), (put / kRing & 1) ^ 1, 2 * p.wait_limit)) give_up();
-            if (__any_sync(0xffffffffu, gave_up())) break;
-            bool put_it = !more && lane == 0;
-            Entry own = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < per; ++i)
-                if (more && 32 * i + lane < pairs && of_size[i] == mine) {
-                    own = entry[i];
-                    put_it = true;
+            if (number < pairs) load += by_size[of_load] - less;
+            if (more ? number < pairs && of_size == mine : number == 0) {
+                if (!mbar_wait_bounded(ring.taken(put % kRing), (put / kRing & 1) ^ 1, 2 * p.wait_limit)) give_up();
+                if (gave_up()) {
+                    stop = 1;
+                } else {
+                    if (!more) entry.rows = 0;
+                    slots[put % kRing] = entry;
+                    mbar_arrive(ring.dealt(put % kRing));
                 }
-            if (put_it) {
-                slots[put % kRing] = own;
-                mbar_arrive(ring.dealt(put % kRing));
             }
-            __syncwarp();
             ++put;
             if (!more) break;
         }
