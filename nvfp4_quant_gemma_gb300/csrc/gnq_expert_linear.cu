@@ -267,16 +267,16 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
 
 // Whether CTA pairs take the call.  Their tile is eight times the other
 // kernel's and pays from about 120 rows an expert on, where there are enough of
-// them to go round and K is deep enough for the hand-over between tiles.  Of 668
-// shapes timed in both kernels (2 to 128 experts, 64 to 1000 rows each, N of 512 to
-// 8192, K of 512 to 4096) the choice loses 0.5 % on average against the faster
-// one, and more than 10 % on 6 (64 experts of 100 rows, N = K = 4096: 125 us on
-// single CTAs, 114 on pairs; of 160 rows, N = 512, K = 4096: 28.3 and 31.1; 8 of 64
-// rows, N = K = 4096: 21.4 and 19.3).
+// them to go round and K is deep enough for the hand-over between tiles; with
+// many, from 96 rows on.  Of 668 shapes timed in both kernels (2 to 128 experts, 64
+// to 1000 rows each, N of 512 to 8192, K of 512 to 4096) the choice loses 0.4 % on
+// average against the faster one, and more than 10 % on 3 (2 experts of 380 rows,
+// N = K = 4096: 17.4 us on single CTAs, 15.8 on pairs; 16 of 200 rows, N = 1024,
+// K = 2048: 11.3 and 12.4).
 bool pairs_take(int64_t E, int64_t R, int64_t N, int64_t K) {
-    if (R < 120 * E || K < 768) return false;
+    if (K < 768) return false;
     const int64_t tiles = (N + 255) / 256 * std::max(E, R / 224);
-    return K >= 1536 ? tiles >= 64 : R >= 250 * E && tiles >= 1000;
+    return R >= 120 * E ? tiles >= (K >= 1536 ? 64 : 300) : R >= 96 * E && tiles >= 500;
 }
 
 }  // namespace

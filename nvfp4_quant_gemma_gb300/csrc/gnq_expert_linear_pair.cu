@@ -20,7 +20,7 @@
 // order of the list, and no pair ends much later than another.  (The experts'
 // rows differ widely, and of some tens of entries in plain order the fullest pair had
 // 15 to 60 % more than the average, now 2 to 10 %.  The two cases below took 235
-// and 164 us in plain order, 229 and 145 dealt out; 257 and 159 with all entries by
+// and 164 us in plain order, 225 and 143 dealt out; 257 and 159 with all entries by
 // falling rows, which reads weights twice; 291 and 189 with each pair's share in
 // one piece, where pairs that run at a time share nothing.)
 //
@@ -34,9 +34,9 @@
 //
 // What bounds it: a stage is 36 to 40 KB into each SM, 590 cycles at 64 bytes a
 // cycle, and as much for its products and the scale copies into tensor memory; the
-// two meet with jitter at about 740.  The case above: 229 us, 4.8 PFLOP/s (the
+// two meet with jitter at about 740.  The case above: 225 us, 4.9 PFLOP/s (the
 // product of one weight on as many rows, 65536 x 4096 x 2048: 228); 2048 tokens to 8
-// of 64, N = K = 4096: 145 us, where reading the weights and writing y take 114.
+// of 64, N = K = 4096: 143 us, where reading the weights and writing y take 114.
 // Copies that only prefetch into L2 take from the same 64 bytes (242 us).
 //
 // Warps of a CTA: 0 copies, 1 issues products (in the pair's first CTA), 2-9
