@@ -128,6 +128,15 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
     load_unit<T, V8>(src, y);
     if constexpr (ACT != ACT_NONE) load_unit<T, V8>(src + p.H, u);
     if (ok && m + p.rows_ahead < p.M) prefetch(src + p.rows_ahead * p.row_stride, true);
+    // in expert order: the row's expert while its values are on their way, by
+    // one search for the warp and from there each lane by itself
+    [[maybe_unused]] int o = 0, e = 0;
+    [[maybe_unused]] float own_scale = 0.f;
+    if constexpr (!FAN) {
+        e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
+        e = ok ? expert_from(p.x, e, m, o) : p.x.E;
+        if (e < p.x.E) own_scale = ld_f32(p.x.scale + e * p.x.scale_stride);
+    }
     if constexpr (ACT != ACT_NONE) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -198,12 +207,8 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
             left &= ~__ballot_sync(0xffffffffu, mine);
         }
     } else {
-        // one search for the warp, from there each lane by itself
-        int o, e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
-        if (!ok) return;
-        e = expert_from(p.x, e, m, o);
         if (e == p.x.E) return;
-        nvfp4_block<false>(v, sixth, ld_f32(p.x.scale + e * p.x.scale_stride), tab, lo, hi, sf);
+        nvfp4_block<false>(v, sixth, own_scale, tab, lo, hi, sf);
         st_v2(codes + (int64_t)m * (p.H >> 1), lo, hi);
         st_u8(scales + expert_scale_row(e, o, m - o, Kp4), sf);
     }
@@ -247,11 +252,11 @@ __global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constan
     const int m = ok ? (int)(at / p.ppr) : 0, b = ok ? 2 * (int)(at - (int64_t)m * p.ppr) : 0;
     pdl_wait();
     pdl_trigger();
+    const uint4 code = ok ? ld_stream(p.q + 16 * at) : make_uint4(0, 0, 0, 0);
     int o, e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
     if (!ok) return;
     e = expert_from(p.x, e, m, o);
     if (e == p.x.E) return;
-    const uint4 code = ld_stream(p.q + 16 * at);
     const uint32_t sf = ld_u16(p.block_scale + expert_scale_row(e, o, m - o, p.Kp4) + (b >> 2) * 512 + (b & 3));
     const float g = p.x.scale ? ld_f32(p.x.scale + e * p.x.scale_stride) : 1.f;
     nvfp4_pair_out<OUT, V8>(p.out, at * 32, code, sf, g);
