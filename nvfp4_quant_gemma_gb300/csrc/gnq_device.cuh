@@ -89,6 +89,9 @@ __device__ __forceinline__ void st_v2(void *p, uint32_t a, uint32_t b) {
 __device__ __forceinline__ void st_u32(void *p, uint32_t a) {
     asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(a) : "memory");
 }
+__device__ __forceinline__ void st_u16(void *p, uint32_t a) {
+    asm volatile("st.global.u16 [%0], %1;" ::"l"(p), "h"((uint16_t)a) : "memory");
+}
 __device__ __forceinline__ void st_u8(void *p, uint32_t a) {
     asm volatile("st.global.u8 [%0], %1;" ::"l"(p), "r"(a) : "memory");
 }

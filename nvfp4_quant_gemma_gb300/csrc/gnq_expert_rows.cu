@@ -15,10 +15,10 @@
 //
 // A token that goes to k experts is read once and written k times, each time
 // with the codes of that expert's scale.  Measured: bf16 8192 x 4096 to 8 experts
-// each 51 us (32 at the copy rate: 75 instructions per block and expert, 70 % of
-// the issue slots), 49 with one scale for all; SiLU of 16384 x 2048 29 us (25),
-// tanh-GELU 30, no activation 20 (12.6); back to bf16 15.2 us (15.4), fp32 33 (25), E4M3
-// 11.6 (10.3); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
+// each 50 us (32 at the copy rate: 75 instructions per block and expert, 70 % of
+// the issue slots), 49 with one scale for all; SiLU of 65536 x 2048 104 us (100),
+// tanh-GELU 108, no activation 52 (51); back to bf16 51 us (51), fp32 114 (90), E4M3
+// 44 (31); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
 #include "gemma_nq.h"
 #include "gnq_elementwise.cuh"
 #include "gnq_expert.cuh"
@@ -106,13 +106,18 @@ __device__ __forceinline__ void nvfp4_block(const float (&v)[16], float sixth, f
     hi = e2m1x8(&x[8]);
 }
 
-template <typename T, int ACT, bool FAN, bool V8>
+// B blocks of 16 a thread, side by side in a row.  Two in expert order without an
+// activation, where a thread's search and addresses cost as much as its codes (65536 x
+// 2048: 51 us, with one block 70, with four 59); one elsewhere: a token to its rows
+// takes 50 us, with two 51, and with an activation a block is work enough (SiLU 104
+// us, HBM).
+template <typename T, int ACT, bool FAN, bool V8, int B>
 __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant__ ExpertQuantParams p) {
     __shared__ float2 tab[128];
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, upr = p.upr / B;
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
-    const bool ok = at < p.units;
-    const int m = ok ? (int)(at / p.upr) : 0, col = ok ? (int)(at - (int64_t)m * p.upr) * 16 : 0;
+    const bool ok = at < p.units / B;
+    const int m = ok ? (int)(at / upr) : 0, col = ok ? (int)(at - (int64_t)m * upr) * 16 * B : 0;
     if (FAN) fill_reciprocals(tab, threadIdx.x);
     const uint16_t *src = p.in + m * p.row_stride + col;
     auto prefetch = [&](const uint16_t *at, bool last) {
@@ -124,10 +129,13 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
     if ((int)blockIdx.x < p.wave && ok) prefetch(src, false);
     pdl_wait();
     pdl_trigger();
-    uint4 y[2], u[2];
-    load_unit<T, V8>(src, y);
-    if constexpr (ACT != ACT_NONE) load_unit<T, V8>(src + p.H, u);
-    if (ok && m + p.rows_ahead < p.M) prefetch(src + p.rows_ahead * p.row_stride, true);
+    uint4 y[B][2], u[B][2];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        load_unit<T, V8>(src + 16 * i, y[i]);
+        if constexpr (ACT != ACT_NONE) load_unit<T, V8>(src + p.H + 16 * i, u[i]);
+    }
+    if (p.rows_ahead && ok && m + p.rows_ahead < p.M) prefetch(src + p.rows_ahead * p.row_stride, true);
     // in expert order: the row's expert while its values are on their way, by
     // one search for the warp and from there each lane by itself
     [[maybe_unused]] int o = 0, e = 0;
@@ -137,35 +145,53 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
         e = ok ? expert_from(p.x, e, m, o) : p.x.E;
         if (e < p.x.E) own_scale = ld_f32(p.x.scale + e * p.x.scale_stride);
     }
-    if constexpr (ACT != ACT_NONE) {
+    float v[B][16], sixth[B];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float g[8], f[8];
-            Act<T>::unpack(y[c], g);
-            Act<T>::unpack(u[c], f);
-            auto activate = [&](auto far) {
+    for (int i = 0; i < B; ++i) {
+        if constexpr (ACT != ACT_NONE) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2)
-                    upk2(act_mul2<T, ACT, decltype(far)::value>(pk2(g[i], g[i + 1]), pk2(f[i], f[i + 1])), g[i], g[i + 1]);
-            };
-            if (__any_sync(0xffffffffu, gates_far<T, ACT>(y[c]))) activate(std::true_type{});
-            else activate(std::false_type{});
-            y[c] = pack8<T>(g);
+            for (int c = 0; c < 2; ++c) {
+                float g[8], f[8];
+                Act<T>::unpack(y[i][c], g);
+                Act<T>::unpack(u[i][c], f);
+                auto activate = [&](auto far) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        upk2(act_mul2<T, ACT, decltype(far)::value>(pk2(g[j], g[j + 1]), pk2(f[j], f[j + 1])), g[j], g[j + 1]);
+                };
+                if (__any_sync(0xffffffffu, gates_far<T, ACT>(y[i][c]))) activate(std::true_type{});
+                else activate(std::false_type{});
+                y[i][c] = pack8<T>(g);
+            }
         }
+        sixth[i] = div6(absmax16<T>(y[i][0], y[i][1]));
+        Act<T>::unpack(y[i][0], &v[i][0]);
+        Act<T>::unpack(y[i][1], &v[i][8]);
     }
-    const float sixth = div6(absmax16<T>(y[0], y[1]));
-    float v[16];
-    Act<T>::unpack(y[0], &v[0]);
-    Act<T>::unpack(y[1], &v[8]);
     const int Kp4 = p.upr >> 2;
     uint8_t *const codes = p.q + (col >> 1), *const scales = p.block_scale + sf_col_offset(col);
-    uint32_t lo, hi, sf;
+    uint32_t code[2 * B], sf[B];
+    auto encode = [&](auto table, float g) {
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            nvfp4_block<decltype(table)::value>(v[i], sixth[i], g, tab, code[2 * i], code[2 * i + 1], sf[i]);
+    };
+    auto store = [&](int row, int64_t sf_row) {
+        uint8_t *const q = codes + (int64_t)row * (p.H >> 1);
+        if constexpr (B == 2) {
+            st_v4(q, make_uint4(code[0], code[1], code[2], code[3]));
+            st_u16(scales + sf_row, sf[0] | sf[1] << 8);
+        } else {
+            st_v2(q, code[0], code[1]);
+            st_u8(scales + sf_row, sf[0]);
+        }
+    };
     if constexpr (FAN) {
         // The choices of a token by the lanes of the warp, one each, so that
         // their reads run side by side; then all units of the token in this
         // warp take them in turn.  A warp holds one token, or parts of a few.
         const bool shared = p.x.scale_stride == 0;
-        if (shared) nvfp4_block<false>(v, sixth, ld_f32(p.x.scale), tab, lo, hi, sf);
+        if (shared) encode(std::false_type{}, ld_f32(p.x.scale));
         uint32_t left = __ballot_sync(0xffffffffu, ok);
         while (left) {
             const int token = __shfl_sync(0xffffffffu, m, __ffs(left) - 1);
@@ -194,9 +220,8 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
                     const int64_t sj = __shfl_sync(0xffffffffu, sf_row, j);
                     const float gj = __shfl_sync(0xffffffffu, g, j);
                     if (!decltype(whole)::value && !mine) continue;
-                    if (!shared) nvfp4_block<decltype(table)::value>(v, sixth, gj, tab, lo, hi, sf);
-                    st_v2(codes + (int64_t)rj * (p.H >> 1), lo, hi);
-                    st_u8(scales + sj, sf);
+                    if (!shared) encode(table, gj);
+                    store(rj, sj);
                 }
             };
             // (the common case apart: a warp of one token, scales that the table serves)
@@ -208,23 +233,26 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
         }
     } else {
         if (e == p.x.E) return;
-        nvfp4_block<false>(v, sixth, own_scale, tab, lo, hi, sf);
-        st_v2(codes + (int64_t)m * (p.H >> 1), lo, hi);
-        st_u8(scales + expert_scale_row(e, o, m - o, Kp4), sf);
+        encode(std::false_type{}, own_scale);
+        store(m, expert_scale_row(e, o, m - o, Kp4));
     }
 }
 
 template <typename T, int ACT> cudaError_t launch_expert_quant(ExpertQuantParams &p, bool v8, cudaStream_t s) {
-    const int64_t grid = (p.units + NT - 1) / NT;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    auto start = [&](auto fn) {
+    auto start = [&](auto fn, int blocks, bool ahead) {
+        const int64_t grid = (p.units / blocks + NT - 1) / NT;
+        if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
         p.wave = one_wave_ctas(reinterpret_cast<const void *>(fn), NT);
-        p.rows_ahead = (int)(((int64_t)p.wave * 3 / 4 * NT + p.upr - 1) / p.upr);
+        const int upr = p.upr / blocks;
+        p.rows_ahead = ahead ? (int)(((int64_t)p.wave * 3 / 4 * NT + upr - 1) / upr) : 0;
         return launch(fn, grid, NT, 0, 1, s, p);
     };
+    constexpr int own = ACT == ACT_NONE ? 2 : 1;
     if (p.slots)
-        return v8 ? start(expert_quant_kernel<T, ACT, true, true>) : start(expert_quant_kernel<T, ACT, true, false>);
-    return v8 ? start(expert_quant_kernel<T, ACT, false, true>) : start(expert_quant_kernel<T, ACT, false, false>);
+        return v8 ? start(expert_quant_kernel<T, ACT, true, true, 1>, 1, true)
+                  : start(expert_quant_kernel<T, ACT, true, false, 1>, 1, true);
+    return v8 ? start(expert_quant_kernel<T, ACT, false, true, own>, own, own == 1)
+              : start(expert_quant_kernel<T, ACT, false, false, own>, own, own == 1);
 }
 
 template <typename T> cudaError_t launch_expert_quant_act(ExpertQuantParams &p, int act, bool v8, cudaStream_t s) {
