@@ -18,7 +18,7 @@
 // each 50 us (32 at the copy rate: 75 instructions per block and expert, 70 % of
 // the issue slots), 49 with one scale for all; SiLU of 65536 x 2048 104 us (100),
 // tanh-GELU 108, no activation 52 (51); back to bf16 51 us (51), fp32 114 (90), E4M3
-// 44 (31); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
+// 35 (31); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
 #include "gemma_nq.h"
 #include "gnq_elementwise.cuh"
 #include "gnq_expert.cuh"
@@ -272,29 +272,36 @@ struct ExpertDequantParams {
     int ppr, Kp4;   // of a row; scale tiles per 128 rows
 };
 
-template <int OUT, bool V8>
+// P pairs a thread: two where the output is small (65536 x 2048 to E4M3: 35 us, with
+// one 44, which is the instructions of the search and the addresses), else one.
+template <int OUT, bool V8, int P>
 __global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, ppr = p.ppr / P;
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
-    const bool ok = at < p.pairs;
-    const int m = ok ? (int)(at / p.ppr) : 0, b = ok ? 2 * (int)(at - (int64_t)m * p.ppr) : 0;
+    const bool ok = at < p.pairs / P;
+    const int m = ok ? (int)(at / ppr) : 0, b = ok ? 2 * P * (int)(at - (int64_t)m * ppr) : 0;
     pdl_wait();
     pdl_trigger();
-    const uint4 code = ok ? ld_stream(p.q + 16 * at) : make_uint4(0, 0, 0, 0);
+    uint4 code[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) code[i] = ok ? ld_stream(p.q + 16 * (P * at + i)) : make_uint4(0, 0, 0, 0);
     int o, e = find_expert(p.x.offsets, p.x.E, __shfl_sync(0xffffffffu, m, 0), lane);
     if (!ok) return;
     e = expert_from(p.x, e, m, o);
     if (e == p.x.E) return;
-    const uint32_t sf = ld_u16(p.block_scale + expert_scale_row(e, o, m - o, p.Kp4) + (b >> 2) * 512 + (b & 3));
+    const uint8_t *const scales = p.block_scale + expert_scale_row(e, o, m - o, p.Kp4) + (b >> 2) * 512 + (b & 3);
+    const uint32_t sf = P == 2 ? (uint32_t)ld_i32(reinterpret_cast<const int32_t *>(scales)) : ld_u16(scales);
     const float g = p.x.scale ? ld_f32(p.x.scale + e * p.x.scale_stride) : 1.f;
-    nvfp4_pair_out<OUT, V8>(p.out, at * 32, code, sf, g);
+#pragma unroll
+    for (int i = 0; i < P; ++i) nvfp4_pair_out<OUT, V8>(p.out, (P * at + i) * 32, code[i], sf >> 16 * i, g);
 }
 
 template <int OUT> cudaError_t launch_expert_dequant(const ExpertDequantParams &p, cudaStream_t s) {
-    const int64_t grid = (p.pairs + NT - 1) / NT;
+    constexpr int P = OUT == OUT_E4M3 ? 2 : 1;
+    const int64_t grid = (p.pairs / P + NT - 1) / NT;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    if (aligned(p.out, 32)) return launch(expert_dequant_kernel<OUT, true>, grid, NT, 0, 1, s, p);
-    return launch(expert_dequant_kernel<OUT, false>, grid, NT, 0, 1, s, p);
+    if (aligned(p.out, 32)) return launch(expert_dequant_kernel<OUT, true, P>, grid, NT, 0, 1, s, p);
+    return launch(expert_dequant_kernel<OUT, false, P>, grid, NT, 0, 1, s, p);
 }
 
 // ---------------------------------------------------------------------------
