@@ -402,6 +402,27 @@ def test_linear_wait_timeout_in_both_kernels(gnq):
             _run_linear(gnq, counts, 384, 1024, torch.bfloat16)
 
 
+def test_linear_wait_timeout_with_many_tiles(gnq):
+    """Each CTA still has tiles before it when its waits run out."""
+    counts = [40, 0, 500] * 100
+    offsets, q, sf, wq, wsf = _operands(counts, 640, 256, 1)
+    args = [t.cuda() for t in (q, sf, wq, wsf)]
+    for kernel in (1, 2):
+        y = torch.full((offsets[-1], 640), 7.0, dtype=torch.bfloat16, device="cuda")
+        gnq.read_device_error()
+        gnq.set_linear_policy(kernel)
+        gnq.inject_wait_timeout(True)
+        try:
+            gnq.nvfp4_expert_linear(*args, fp32([1.0]), ints(offsets), out=y)
+            torch.cuda.synchronize()
+        finally:
+            gnq.inject_wait_timeout(False)
+            gnq.set_linear_policy(0)
+        assert gnq.read_device_error(clear=True) & 1
+        assert bool((y == 7.0).all())
+        _run_linear(gnq, counts[:30], 384, 256, torch.bfloat16)
+
+
 @pytest.mark.parametrize("N,K", [(136, 64), (256, 1088)])
 @pytest.mark.parametrize("counts", [[150, 3] + [0] * 14, [1, 0, 65, 190, 64] + [0] * 20, [0, 63, 129] * 12])
 def test_linear_few_rows_but_many_for_one(gnq, counts, N, K):
