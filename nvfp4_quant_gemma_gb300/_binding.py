@@ -602,6 +602,25 @@ def _floats_ok(dev: int, t, n: int) -> bool:
     return t.dtype is _F32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
 
 
+def _matrix_ok(t, rows: int, cols: int) -> bool:
+    """Whether the kernels, which index it with a row stride of `cols`, find a
+    (rows, cols) matrix in the contiguous `t`: in rows of that width, or flat."""
+    d = t.dim()
+    return t.shape[-1] == cols and t.numel() >= rows * cols if d > 1 else d == 1 and t.numel() == rows * cols
+
+
+def _need_matrix(t, name: str, rows: int, cols: int, dtypes) -> None:
+    size = t.element_size() if isinstance(t, torch.Tensor) else 0
+    _need(t, name, rows * cols * size, dtypes)
+    if not _matrix_ok(t, rows, cols):
+        raise ValueError(f"{name} must be ({rows}, {cols}), got {tuple(t.shape)}")
+
+
+def _weight_scales_ok(t, E: int, rows: int, cols: int) -> bool:
+    """Whether each of E experts' scales lie `rows` x `cols` bytes behind the last one's."""
+    return t.nbytes == E * rows * cols or (t.dim() == 3 and t.shape[0] >= E and t.shape[1:] == (rows, cols))
+
+
 def _expert_count(offsets) -> int:
     _need(offsets, "offsets", 8, (_I32,))
     if offsets.dim() != 1:
@@ -804,8 +823,9 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
     expert_quantize returns them; ``weight_q`` (E, N, K/2) and
     ``weight_block_scale`` (E, round_up(N, 128), K/16), each expert's as
     ``quantize`` returns it; ``alpha`` one fp32 per expert, or one; ``bias``
-    (E, N).  The output (R, N) is bf16 (default), fp16 or fp32; rows behind the
-    last used one are left as they were."""
+    (E, N): matrix by matrix and row by row as they lie in memory, so not padded
+    to more columns.  The output (R, N) is bf16 (default), fp16 or fp32; rows
+    behind the last used one are left as they were."""
     try:
         dev = q.get_device()
         E, N, half = weight_q.shape
@@ -819,11 +839,11 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
               and offsets.dim() == 1 and offsets.numel() == E + 1 and _ints_ok(dev, offsets, E + 1)
               and weight_q.dtype is _U8 and weight_q.is_contiguous() and weight_q.get_device() == dev
               and weight_block_scale.dtype in (_E4M3, _U8) and weight_block_scale.is_contiguous()
-              and weight_block_scale.nbytes >= E * ((N + 127) // 128) * 16 * half
+              and _weight_scales_ok(weight_block_scale, E, (N + 127) // 128 * 128, half // 8)
               and weight_block_scale.get_device() == dev and (g == E or g == 1) and _floats_ok(dev, alpha, 1)
               and out.is_contiguous() and out.numel() >= R * N and out.get_device() == dev
               and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous()
-                                    and bias.numel() >= E * N and bias.get_device() == dev)))
+                                    and _matrix_ok(bias, E, N) and bias.get_device() == dev)))
         per_expert = 1 if g == E else 0
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -837,6 +857,9 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
         if 2 * weight_q.shape[2] != K:
             raise ValueError(f"the activation has K = {K}, the weight {2 * weight_q.shape[2]}")
         _need(weight_block_scale, "weight_q's block scales", E * round_up(N, 128) * (K // 16), (_E4M3, _U8))
+        if not _weight_scales_ok(weight_block_scale, E, round_up(N, 128), K // 16):
+            raise ValueError(f"weight_q's block scales must be ({E}, {round_up(N, 128)}, {K // 16}), "
+                             f"got {tuple(weight_block_scale.shape)}")
         per_expert = _expert_values(alpha, "alpha", E)
         if out is None:
             out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
@@ -845,7 +868,7 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
             raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
         _need(out, "out", R * N * out.element_size(), (out.dtype,))
         if bias is not None:
-            _need(bias, "bias", E * N * 2, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
+            _need_matrix(bias, "bias", E, N, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
         dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias, out), pinned=False)
     st = (_lib or load()).nvfp4_expert_linear(
         q.data_ptr(), block_scale.data_ptr(), weight_q.data_ptr(), weight_block_scale.data_ptr(), alpha.data_ptr(),
@@ -860,7 +883,8 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
     """The weighted sum of a token's rows: out[t] = sum_j weights[t, j] *
     y[slots[t, j]] + add[t], in fp32, rounded once; slots below 0 add nothing.
     y (R, H) is bf16, fp16 or fp32; ``out`` (M, H) of y's type, or of any of the
-    three where y is fp32; ``add`` of out's type (``out`` itself, too)."""
+    three where y is fp32; ``add`` of out's type (``out`` itself, too).  Matrices
+    may have more rows than the call needs, or be flat; not other columns."""
     try:
         dev = y.get_device()
         R, H = y.shape
@@ -870,8 +894,9 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
         ok = (dev >= 0 and dev == _current_device() and y.is_contiguous() and out.dtype in _OUT_TYPE
               and (out.dtype is y.dtype or y.dtype is _F32) and _OUT_TYPE[out.dtype] < 3 and _OUT_TYPE.get(y.dtype, 3) < 3
               and _ints_ok(dev, slots, M * k) and _floats_ok(dev, weights, M * k)
+              and (weights.shape == slots.shape or _matrix_ok(weights, M, k))
               and out.is_contiguous() and out.numel() >= M * H and out.get_device() == dev
-              and (add is None or (add.dtype is out.dtype and add.is_contiguous() and add.numel() >= M * H
+              and (add is None or (add.dtype is out.dtype and add.is_contiguous() and _matrix_ok(add, M, H)
                                    and add.get_device() == dev)))
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -886,10 +911,10 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
             out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, **kw)
         if not isinstance(out, torch.Tensor) or _OUT_TYPE.get(out.dtype, 3) > 2:
             raise ValueError("the output must be bf16, fp16 or fp32")
-        _need(weights, "weights", 4 * M * k, (_F32,))
+        _need_matrix(weights, "weights", M, k, (_F32,))
         _need(out, "out", M * H * out.element_size(), (out.dtype,) if y.dtype is _F32 else (y.dtype,))
         if add is not None:
-            _need(add, "add", M * H * out.element_size(), (out.dtype,))
+            _need_matrix(add, "add", M, H, (out.dtype,))
         dev = _place((y, slots, weights, add, out))
     st = (_lib or load()).gnq_expert_combine(
         y.data_ptr(), slots.data_ptr(), weights.data_ptr(), None if add is None else add.data_ptr(), out.data_ptr(),
