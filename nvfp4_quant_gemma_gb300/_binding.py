@@ -585,7 +585,9 @@ def nvfp4_linear(q, block_scale, weight_q, weight_block_scale, alpha, bias=None,
 
 
 # Rows in expert order: expert e owns rows offsets[e] .. offsets[e + 1] - 1
-# (include/gemma_nq.h states the layout of their block scales).
+# (include/gemma_nq.h states the layout of their block scales).  Buffers may hold
+# more rows than a call needs or be flat, but a matrix's columns are the call's:
+# the kernels' row strides are.
 _I32 = torch.int32
 
 
@@ -613,6 +615,19 @@ def _need_matrix(t, name: str, rows: int, cols: int, dtypes) -> None:
     size = t.element_size() if isinstance(t, torch.Tensor) else 0
     _need(t, name, rows * cols * size, dtypes)
     if not _matrix_ok(t, rows, cols):
+        raise ValueError(f"{name} must be ({rows}, {cols}), got {tuple(t.shape)}")
+
+
+def _result_ok(t, rows: int, cols: int) -> bool:
+    """Whether a (rows, cols) result written to the contiguous `t` is where its
+    shape says: in rows of that width, or the first of a flat buffer."""
+    return t.numel() >= rows * cols and (t.dim() < 2 or t.shape[-1] == cols)
+
+
+def _need_result(t, name: str, rows: int, cols: int, dtypes) -> None:
+    size = t.element_size() if isinstance(t, torch.Tensor) else 0
+    _need(t, name, rows * cols * size, dtypes)
+    if not _result_ok(t, rows, cols):
         raise ValueError(f"{name} must be ({rows}, {cols}), got {tuple(t.shape)}")
 
 
@@ -665,7 +680,8 @@ def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
     k = int(k)
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be 1 .. {min(E, 32)}")
-    if out is None:
+    given = out is not None
+    if not given:
         kw = {"device": logits.device} if logits.is_cuda else {"pin_memory": True}
         out = (torch.empty((M, k), dtype=_I32, **kw), torch.empty((M, k), dtype=_F32, **kw),
                torch.empty(E + 1, dtype=_I32, **kw), torch.empty((M, k), dtype=_I32, **kw))
@@ -673,13 +689,15 @@ def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
     dev, n = logits.get_device(), M * k
     try:
         ok = (dev >= 0 and dev == _current_device() and _ints_ok(dev, experts, n) and _floats_ok(dev, weights, n)
-              and _ints_ok(dev, offsets, E + 1) and _ints_ok(dev, slots, n))
+              and _ints_ok(dev, offsets, E + 1) and _ints_ok(dev, slots, n)
+              and (not given or (_result_ok(experts, M, k) and _result_ok(weights, M, k) and _result_ok(slots, M, k))))
     except AttributeError:
         ok = False
     if not ok:
-        for t, name, size in ((experts, "experts", n), (offsets, "offsets", E + 1), (slots, "slots", n)):
-            _need(t, name, 4 * size, (_I32,))
-        _need(weights, "weights", 4 * n, (_F32,))
+        _need_result(experts, "experts", M, k, (_I32,))
+        _need_result(weights, "weights", M, k, (_F32,))
+        _need(offsets, "offsets", 4 * (E + 1), (_I32,))
+        _need_result(slots, "slots", M, k, (_I32,))
         dev = _place((logits, experts, weights, offsets, slots))
     st = (_lib or load()).gnq_expert_route(
         logits.data_ptr(), stride, _OUT_TYPE[logits.dtype], M, E, k, 1 if renormalize else 0, float(scale),
@@ -733,7 +751,7 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
                                      and slots.get_device() == dev and experts.shape == slots.shape
                                      and experts.dtype is _I32 and experts.is_contiguous()
                                      and experts.get_device() == dev))
-              and q.dtype is _U8 and q.is_contiguous() and q.nbytes >= R * H // 2 and q.get_device() == dev
+              and q.dtype is _U8 and q.is_contiguous() and _result_ok(q, R, H // 2) and q.get_device() == dev
               and bs.dtype in (_E4M3, _U8) and bs.is_contiguous() and bs.nbytes >= rows * (H // 16)
               and bs.get_device() == dev)
     except (AttributeError, TypeError, ValueError, IndexError):
@@ -748,7 +766,7 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
         rows = expert_scale_rows(R, E)
         q, bs = out if out is not None else _expert_buffers(R, rows, H, x)
         per_expert = _expert_values(scale, "scale", E)
-        _need(q, "q", R * H // 2, (_U8,))
+        _need_result(q, "q", R, H // 2, (_U8,))
         _need(bs, "block_scale", rows * (H // 16), (_E4M3, _U8))
         dev = _place((x, offsets, scale, slots, experts, q, bs))
     st = (_lib or load()).gnq_expert_quantize(
@@ -793,7 +811,7 @@ def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None,
               and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
               and (scale is None or (scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev))
               and _expert_packed_ok(dev, E, q, block_scale) and out.dtype in _OUT_TYPE
-              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.numel() >= R * K
+              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and _result_ok(out, R, K)
               and out.get_device() == dev)
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -804,7 +822,7 @@ def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None,
             out = torch.empty((R, K), dtype=dtype or torch.bfloat16, pin_memory=True)
         if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPE or (dtype is not None and out.dtype != dtype):
             raise ValueError("the output must be bf16, fp16, fp32 or float8_e4m3fn (and of the given dtype)")
-        _need(out, "out", R * K * out.element_size(), (out.dtype,))
+        _need_result(out, "out", R, K, (out.dtype,))
         per_expert = 0 if scale is None else _expert_values(scale, "scale", E)
         dev = _place((q, block_scale, offsets, scale, out))
     st = (_lib or load()).gnq_expert_dequantize(
@@ -841,7 +859,7 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
               and weight_block_scale.dtype in (_E4M3, _U8) and weight_block_scale.is_contiguous()
               and _weight_scales_ok(weight_block_scale, E, (N + 127) // 128 * 128, half // 8)
               and weight_block_scale.get_device() == dev and (g == E or g == 1) and _floats_ok(dev, alpha, 1)
-              and out.is_contiguous() and out.numel() >= R * N and out.get_device() == dev
+              and out.is_contiguous() and _result_ok(out, R, N) and out.get_device() == dev
               and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous()
                                     and _matrix_ok(bias, E, N) and bias.get_device() == dev)))
         per_expert = 1 if g == E else 0
@@ -866,7 +884,7 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
         ot = _OUT_TYPE.get(out.dtype, 3) if isinstance(out, torch.Tensor) else 3
         if ot == 3 or (dtype is not None and out.dtype != dtype):
             raise ValueError("the output must be bf16, fp16 or fp32 (and of the given dtype)")
-        _need(out, "out", R * N * out.element_size(), (out.dtype,))
+        _need_result(out, "out", R, N, (out.dtype,))
         if bias is not None:
             _need_matrix(bias, "bias", E, N, (out.dtype,) if ot < 2 else (torch.bfloat16, torch.float16))
         dev = _place((q, block_scale, weight_q, weight_block_scale, alpha, offsets, bias, out), pinned=False)
@@ -895,7 +913,7 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
               and (out.dtype is y.dtype or y.dtype is _F32) and _OUT_TYPE[out.dtype] < 3 and _OUT_TYPE.get(y.dtype, 3) < 3
               and _ints_ok(dev, slots, M * k) and _floats_ok(dev, weights, M * k)
               and (weights.shape == slots.shape or _matrix_ok(weights, M, k))
-              and out.is_contiguous() and out.numel() >= M * H and out.get_device() == dev
+              and out.is_contiguous() and _result_ok(out, M, H) and out.get_device() == dev
               and (add is None or (add.dtype is out.dtype and add.is_contiguous() and _matrix_ok(add, M, H)
                                    and add.get_device() == dev)))
     except (AttributeError, TypeError, ValueError):
@@ -912,7 +930,7 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
         if not isinstance(out, torch.Tensor) or _OUT_TYPE.get(out.dtype, 3) > 2:
             raise ValueError("the output must be bf16, fp16 or fp32")
         _need_matrix(weights, "weights", M, k, (_F32,))
-        _need(out, "out", M * H * out.element_size(), (out.dtype,) if y.dtype is _F32 else (y.dtype,))
+        _need_result(out, "out", M, H, (out.dtype,) if y.dtype is _F32 else (y.dtype,))
         if add is not None:
             _need_matrix(add, "add", M, H, (out.dtype,))
         dev = _place((y, slots, weights, add, out))

@@ -53,6 +53,15 @@ def calls(t):
         ("linear: weight scales of more columns", lambda g: linear(g, wsf=t(2, 128, 8, dtype=U8)),
          r"block scales must be \(2, 128, 4\)"),
         ("linear: flat weight scales, too many", lambda g: linear(g, wsf=t(512, 4, dtype=U8)), r"block scales must be \(2, 128, 4\)"),
+        # results
+        ("route: wider experts", lambda g: route(g, experts=t(4, 3)), r"experts must be \(4, 2\)"),
+        ("route: wider weights", lambda g: route(g, weights=t(4, 3, dtype=F32)), r"weights must be \(4, 2\)"),
+        ("route: wider slots", lambda g: route(g, slots=t(4, 3)), r"slots must be \(4, 2\)"),
+        ("quantize: wider codes", lambda g: quantize(g, q=t(4, 64, dtype=U8)), r"q must be \(4, 32\)"),
+        ("quantize: wider codes of a fan-out", lambda g: quantize(g, fan=True, q=t(8, 64, dtype=U8)), r"q must be \(8, 32\)"),
+        ("dequantize: a wider result", lambda g: dequantize(g, out=t(4, 96, dtype=BF)), r"out must be \(4, 64\)"),
+        ("linear: a wider result", lambda g: linear(g, out=t(4, 16, dtype=BF)), r"out must be \(4, 8\)"),
+        ("combine: a wider result", lambda g: combine(g, out=t(4, 72, dtype=BF)), r"out must be \(4, 64\)"),
         # types, counts and sizes
         ("route: rows that are not dense", lambda g: route(g, logits=t(4, 16, dtype=F32)[:, ::2]), "contiguous rows"),
         ("route: logits' type", lambda g: route(g, logits=t(4, 8, dtype=I32)), "logits must be"),
