@@ -284,10 +284,13 @@ int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
  * expert's last row are not written and influence nothing.
  * 1 <= E <= 1024 and 1 <= k <= 32.  scale_stride (alpha_stride) is 1 for one
  * fp32 per expert, 0 for one that all share (GNQ_ERR_MODE otherwise).
- * Offsets that do not ascend within 0 .. R, and slots that are not a row of
- * their expert, are found on the device: bit 2 of the device error word is set
- * (gnq_read_device_error), what they name is left out (nvfp4_expert_linear
- * writes nothing at all), and nothing outside the buffers is touched.
+ * Offsets that do not ascend from 0 to at most R, and slots that are not a row
+ * of their expert, are found on the device by each call that has rows: bit 2 of
+ * the device error word is set (gnq_read_device_error) and nothing outside the
+ * buffers is touched.  Of such offsets nvfp4_expert_linear writes nothing at
+ * all; the quantization and the way back leave out rows that no expert's bounds
+ * hold and slots that are no row of their expert, and give each other row to an
+ * expert whose bounds hold it.
  */
 
 /*

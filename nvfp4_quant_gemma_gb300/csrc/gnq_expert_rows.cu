@@ -39,19 +39,28 @@ struct ExpertRows {
     unsigned int *err;
 };
 
-// The expert of row `m`, one past the last where it has none (reported unless
-// the row lies behind the last used one); `e` is a lower bound of it.
+// The expert of row `m`, one past the last where it has none; `e` is a lower
+// bound of it.
 __device__ __forceinline__ int expert_from(const ExpertRows &x, int e, int m, int &o) {
     while (e < x.E && ld_i32(x.offsets + e + 1) <= m) ++e;
     o = 0;
     if (e < x.E) {
         o = row_bound(x.offsets, e, x.R);
-        if (o > m) {
-            atomicOr(x.err, (unsigned)DEVERR_BAD_ROW);
-            e = x.E;
-        }
+        if (o > m) e = x.E;  // (check_offsets reports such offsets)
     }
     return e;
+}
+
+// Reports offsets that do not start at 0, fall or end behind the R rows.  A row
+// looks only at its own expert's bounds, so a CTA of its own, the last of the
+// grid, looks at all of them: no other waits for it.
+__device__ __forceinline__ void check_offsets(const ExpertRows &x) {
+    bool bad = false;
+    for (int e = threadIdx.x; e <= x.E; e += NT) {
+        const int o = ld_i32(x.offsets + e);
+        bad |= o > x.R || (e == 0 ? o != 0 : o < ld_i32(x.offsets + e - 1));
+    }
+    if (bad) atomicOr(x.err, (unsigned)DEVERR_BAD_ROW);
 }
 
 // ---------------------------------------------------------------------------
@@ -114,6 +123,12 @@ __device__ __forceinline__ void nvfp4_block(const float (&v)[16], float sixth, f
 template <typename T, int ACT, bool FAN, bool V8, int B>
 __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant__ ExpertQuantParams p) {
     __shared__ float2 tab[128];
+    if (blockIdx.x + 1 == gridDim.x) {
+        pdl_wait();
+        pdl_trigger();
+        check_offsets(p.x);
+        return;
+    }
     const int lane = threadIdx.x & 31, upr = p.upr / B;
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
     const bool ok = at < p.units / B;
@@ -240,7 +255,7 @@ __global__ void __launch_bounds__(NT) expert_quant_kernel(const __grid_constant_
 
 template <typename T, int ACT> cudaError_t launch_expert_quant(ExpertQuantParams &p, bool v8, cudaStream_t s) {
     auto start = [&](auto fn, int blocks, bool ahead) {
-        const int64_t grid = (p.units / blocks + NT - 1) / NT;
+        const int64_t grid = (p.units / blocks + NT - 1) / NT + 1;  // (the last for check_offsets)
         if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
         p.wave = one_wave_ctas(reinterpret_cast<const void *>(fn), NT);
         const int upr = p.upr / blocks;
@@ -276,6 +291,12 @@ struct ExpertDequantParams {
 // one 44, which is the instructions of the search and the addresses), else one.
 template <int OUT, bool V8, int P>
 __global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
+    if (blockIdx.x + 1 == gridDim.x) {
+        pdl_wait();
+        pdl_trigger();
+        check_offsets(p.x);
+        return;
+    }
     const int lane = threadIdx.x & 31, ppr = p.ppr / P;
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
     const bool ok = at < p.pairs / P;
@@ -298,7 +319,7 @@ __global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constan
 
 template <int OUT> cudaError_t launch_expert_dequant(const ExpertDequantParams &p, cudaStream_t s) {
     constexpr int P = OUT == OUT_E4M3 ? 2 : 1;
-    const int64_t grid = (p.pairs / P + NT - 1) / NT;
+    const int64_t grid = (p.pairs / P + NT - 1) / NT + 1;  // (the last for check_offsets)
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     if (aligned(p.out, 32)) return launch(expert_dequant_kernel<OUT, true, P>, grid, NT, 0, 1, s, p);
     return launch(expert_dequant_kernel<OUT, false, P>, grid, NT, 0, 1, s, p);

@@ -1,11 +1,14 @@
 """GPU tests of the expert operators where they could go wrong unseen: refusals
-of device tensors and shapes that the kernels index."""
+of device tensors, shapes that the kernels index, offsets in no order."""
 import pytest
 import torch
 
 import oracle
+from experts_ref import scale_rows
 from experts_refusals import calls, names
+from gnq_testutil import u8
 from test_gpu_experts import _operands, fp32, ints
+from test_gpu_operators import SENT, Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,72 @@ def test_shapes_that_hold_the_call_s_matrices(gnq):
     for scales, b in ((wsf.cuda().reshape(-1), bias.reshape(-1)), (wsf.cuda().reshape(E * 256, 8), torch.cat((bias, bias))),
                       (more, bias)):
         assert torch.equal(gnq.nvfp4_expert_linear(*args, scales, fp32([0.01]), o, bias=b), want)
+
+
+# ---------------------------------------------------------------------------
+# offsets in no order
+# ---------------------------------------------------------------------------
+def _ascending(E, R):
+    return [R * e // E for e in range(E + 1)]
+
+
+def _with(offsets, **at):
+    offsets = list(offsets)
+    for i, v in at.items():
+        offsets[int(i[1:])] = v
+    return offsets
+
+
+BAD = {
+    "falling": [0, 5, 3, 9], "negative": [0, -4, 4, 9], "far": [0, 3, 6, 1 << 30], "behind the rows": [0, 3, 6, 10],
+    "a late start": [2, 3, 6, 9], "an early start": [-5, 3, 6, 9], "far and back": [0, 1 << 30, -(1 << 30), 9],
+    "falling among many": _with(_ascending(1024, 9), i1000=3), "behind the rows among many": _with(_ascending(700, 9), i700=10),
+    "a late start among many": _with(_ascending(300, 9), i0=1),
+}
+
+
+@pytest.mark.parametrize("bad", BAD.values(), ids=BAD.keys())
+def test_offsets_in_no_order_are_reported_by_each_operator(gnq, bad):
+    """Each call sets the word by itself; rows in nobody's bounds stay as they were."""
+    E, R, H = len(bad) - 1, 9, 128
+    o, s = ints(bad), fp32([9.0])
+    x = torch.randn(R, H, device="cuda").to(torch.bfloat16)
+    held = {r for e in range(E) for r in range(max(bad[e], 0), min(bad[e + 1], R))}
+    slots = torch.arange(R, device="cuda").reshape(R, 1).int()
+    owner = [next((e for e in range(E) if max(bad[e], 0) <= r < bad[e + 1]), -1) for r in range(R)]
+    q0 = torch.zeros(R, H // 2, dtype=torch.uint8, device="cuda")
+    sf0 = torch.zeros(scale_rows(R, E), H // 16, dtype=torch.uint8, device="cuda")
+    gnq.read_device_error()
+    for call in (lambda q, sf, back: gnq.expert_quantize(x, o, s, out=(q, sf)),
+                 lambda q, sf, back: gnq.expert_quantize(torch.cat((x, x), 1), o, s, act="silu", out=(q, sf)),
+                 lambda q, sf, back: gnq.expert_quantize(x, o, s, out=(q, sf), slots=torch.where(ints(owner)[:, None] < 0, -1, slots),
+                                                         experts=ints(owner)[:, None]),
+                 lambda q, sf, back: gnq.expert_dequantize(q0, sf0, o, s, out=back),
+                 lambda q, sf, back: gnq.expert_dequantize(q0, sf0, o, s, out=back.view(torch.uint8)[:, :H].contiguous()
+                                                           .view(torch.float8_e4m3fn))):
+        G = Guarded()
+        q, sf, back = G((R, H // 2), torch.uint8), G((scale_rows(R, E), H // 16), torch.uint8), G((R, H), torch.bfloat16)
+        call(q, sf, back)
+        torch.cuda.synchronize()
+        G.check()
+        assert gnq.read_device_error() == 2
+        for buf in (q, back):
+            for r in range(R):
+                assert r in held or (u8(buf)[r] == SENT).all()
+
+
+@pytest.mark.parametrize("E", [3, 300, 700, 1024])
+def test_offsets_in_order_are_not_reported(gnq, E):
+    """Bounds of all kinds that are right: empty experts, rows of nobody."""
+    R, H = 9, 128
+    x = torch.randn(R, H, device="cuda").to(torch.bfloat16)
+    for offsets in (_ascending(E, R), [0] * E + [R], [0] + [R] * E, [0] * (E + 1), _ascending(E, 4)):
+        o, s = ints(offsets), fp32([9.0])
+        q, sf = gnq.expert_quantize(x, o, s)
+        gnq.expert_dequantize(q, sf, o, s)
+        owner = torch.searchsorted(torch.tensor(offsets[1:]), torch.arange(R), right=True)
+        owner = torch.where(owner < E, owner, -1).int().cuda()[:, None]
+        slots = torch.where(owner >= 0, torch.arange(R, device="cuda").int()[:, None], -1)
+        gnq.expert_quantize(x, o, s, slots=slots, experts=owner)
+        torch.cuda.synchronize()
+        assert gnq.read_device_error() == 0
