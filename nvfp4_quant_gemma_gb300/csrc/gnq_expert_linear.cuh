@@ -54,14 +54,14 @@ struct TileList {
 };
 
 // Builds the list with the whole CTA (warps x 32 threads), after the wait on
-// the preceding grid.  Offsets that do not ascend within the R rows are reported
+// the preceding grid.  Offsets that do not ascend from 0 within the R rows are reported
 // and give an empty list: with others the tiles fit an int and every search ends.
 __device__ __forceinline__ TileList build_tiles(const ExpertLinearParams &x, int T, int *smem, int warps) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, E = x.E, R = (int)x.p.M;
     int *const before = smem, *const row0 = smem + E + 1, *const sums = row0 + E + 1;
     const int per = (E + 32 * warps - 1) / (32 * warps), first = min(E, t * per), last = min(E, first + per);
     int mine = 0;
-    bool bad = false;
+    bool bad = t == 0 && ld_i32(x.offsets) != 0;
     int from = row_bound(x.offsets, first, R);
     for (int e = first; e < last; ++e) {
         const int to = row_bound(x.offsets, e + 1, R);

@@ -114,6 +114,27 @@ def test_offsets_in_no_order_are_reported_by_each_operator(gnq, bad):
                 assert r in held or (u8(buf)[r] == SENT).all()
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("bad", BAD.values(), ids=BAD.keys())
+def test_the_product_of_offsets_in_no_order_writes_nothing(gnq, bad, kernel):
+    E, R, N, K = len(bad) - 1, 9, 136, 128
+    q = torch.zeros(R, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.zeros(scale_rows(R, E), K // 16, dtype=torch.uint8, device="cuda")
+    wq = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    wsf = torch.zeros(E, 256, K // 16, dtype=torch.uint8, device="cuda")
+    G = Guarded()
+    y = G((R, N), torch.bfloat16)
+    gnq.read_device_error()
+    gnq.set_linear_policy(kernel)
+    try:
+        gnq.nvfp4_expert_linear(q, sf, wq, wsf, fp32([1.0]), ints(bad), out=y)
+        torch.cuda.synchronize()
+    finally:
+        gnq.set_linear_policy(0)
+    G.check()
+    assert gnq.read_device_error() == 2 and (u8(y) == SENT).all()
+
+
 @pytest.mark.parametrize("E", [3, 300, 700, 1024])
 def test_offsets_in_order_are_not_reported(gnq, E):
     """Bounds of all kinds that are right: empty experts, rows of nobody."""
