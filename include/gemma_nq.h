@@ -374,7 +374,8 @@ int nvfp4_expert_linear(const void *q, const void *block_scale, const void *w_q,
  *
  *     out[t] = type(sum_j weights[t, j] * y[slots[t, j]] + add[t])
  *
- * in fp32, in a fixed order, `add` last, rounded once.  Slots below 0 add
+ * in fp32, two neighbours at a time in the order of j, `add` last, rounded
+ * once: the same bits whatever else the batch holds.  Slots below 0 add
  * nothing; a slot of R or more is reported as above and adds nothing.
  *   y        (R, H) of y_type GNQ_BF16, GNQ_FP16 or GNQ_FP32.
  *   weights  (M, k) fp32.

@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constan
     const int32_t *const slots = p.slots + t * p.k;
     const float *const weights = p.weights + t * p.k;
     for (int j0 = 0; j0 < p.k; j0 += G) {
-        // G rows on their way at a time, added as a tree: fewer roundings of
-        // large sums than one by one, and a shorter chain.
+        // G rows on their way at a time, added pair by pair in the order of j
+        // whatever G is: a token's sum does not depend on the batch it is in.
         int row[G];
         float w[G];
         typename Row8<Y>::Raw raw[G];
@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constan
             raw[j] = typename Row8<Y>::Raw{};
             if (row[j] >= 0) raw[j] = Row8<Y>::load(p.y, (int64_t)row[j] * p.H + col);
         }
-        float s[G / 2][8];
 #pragma unroll
         for (int j = 0; j < G; j += 2) {
             float a[8], b[8];
@@ -408,16 +407,8 @@ __global__ void __launch_bounds__(NT) expert_combine_kernel(const __grid_constan
             Row8<Y>::unpack(raw[j + 1], b);
             const float wa = row[j] < 0 ? 0.f : w[j], wb = row[j + 1] < 0 ? 0.f : w[j + 1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[j / 2][i] = fmaf(wb, b[i], wa * a[i]);
+            for (int i = 0; i < 8; ++i) acc[i] += fmaf(wb, b[i], wa * a[i]);
         }
-#pragma unroll
-        for (int d = 1; d < G / 2; d *= 2)
-#pragma unroll
-            for (int j = 0; j + d < G / 2; j += 2 * d)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[j][i] += s[j + d][i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += s[0][i];
     }
     if (p.add) {
         float f[8];

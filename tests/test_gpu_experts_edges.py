@@ -1,5 +1,6 @@
 """GPU tests of the expert operators where they could go wrong unseen: refusals
-of device tensors, shapes that the kernels index, offsets in no order."""
+of device tensors, shapes that the kernels index, offsets in no order, sums that
+must not depend on the batch."""
 import pytest
 import torch
 
@@ -7,7 +8,7 @@ import oracle
 from experts_ref import scale_rows
 from experts_refusals import calls, names
 from gnq_testutil import u8
-from test_gpu_experts import _operands, fp32, ints
+from test_gpu_experts import ALL, _operands, fp32, ints
 from test_gpu_operators import SENT, Guarded
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +151,31 @@ def test_offsets_in_order_are_not_reported(gnq, E):
         gnq.expert_quantize(x, o, s, slots=slots, experts=owner)
         torch.cuda.synchronize()
         assert gnq.read_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# the combination of large batches
+# ---------------------------------------------------------------------------
+LARGE = (2500, 520)  # tokens and columns: more units than the instance of small batches takes
+
+
+def _combination(M, H, k, Y, seed):
+    g = torch.Generator().manual_seed(seed)
+    y = torch.randn(M * k, H, generator=g).to(ALL[Y])
+    slots = torch.randperm(M * k, generator=g).reshape(M, k)
+    slots[::7, k // 2] = -1
+    slots[5] = -1
+    return y, slots, torch.rand(M, k, generator=g)
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 8, 9, 32])
+@pytest.mark.parametrize("Y,O", [("bf16", "bf16"), ("fp32", "fp32")])
+def test_a_token_s_combination_does_not_depend_on_the_batch(gnq, k, Y, O):
+    M, H = LARGE
+    y, slots, w = _combination(M, H, k, Y, k)
+    add = torch.randn(M, H).to(ALL[O]).cuda()
+    y, slots, w = y.cuda(), slots.int().cuda(), w.cuda()
+    whole = gnq.expert_combine(y, slots, w, add=add)
+    for a, z in ((0, 1), (0, 40), (M - 200, M)):
+        part = gnq.expert_combine(y, slots[a:z].contiguous(), w[a:z].contiguous(), add=add[a:z].contiguous())
+        assert torch.equal(part, whole[a:z])
