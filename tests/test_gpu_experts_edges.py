@@ -1,14 +1,17 @@
 """GPU tests of the expert operators where they could go wrong unseen: refusals
 of device tensors, shapes that the kernels index, offsets in no order, sums that
-must not depend on the batch."""
+must not depend on the batch, and the instances that only large batches, other
+types, other alignments or combined options reach."""
 import pytest
 import torch
 
 import oracle
 from experts_ref import scale_rows
 from experts_refusals import calls, names
-from gnq_testutil import u8
-from test_gpu_experts import ALL, _operands, fp32, ints
+from gnq_testutil import DTYPES, u8
+from operators_ref import assert_within, rounding
+from test_gpu_experts import (ALL, COUNTS, _check_packed, _fan, _logits, _operands, _run_linear, _values, fp32, ints,
+                              offsets_of, random_rows, route64)
 from test_gpu_operators import SENT, Guarded
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +182,150 @@ def test_a_token_s_combination_does_not_depend_on_the_batch(gnq, k, Y, O):
     for a, z in ((0, 1), (0, 40), (M - 200, M)):
         part = gnq.expert_combine(y, slots[a:z].contiguous(), w[a:z].contiguous(), add=add[a:z].contiguous())
         assert torch.equal(part, whole[a:z])
+
+
+@pytest.mark.parametrize("Y,O", [("bf16", "bf16"), ("fp16", "fp16"), ("fp32", "fp32"), ("fp32", "bf16"), ("fp32", "fp16")])
+@pytest.mark.parametrize("add", ["none", "apart", "in place"])
+@pytest.mark.parametrize("k", [5, 8])
+def test_combine_large_batches(gnq, k, add, Y, O):
+    M, H = LARGE
+    y, slots, w = _combination(M, H, k, Y, 11 + k)
+    a = torch.randn(M, H, generator=torch.Generator().manual_seed(k)).to(ALL[O])
+    G = Guarded()
+    out = G((M, H), ALL[O])
+    if add == "in place":
+        out.copy_(a)
+    gnq.expert_combine(y.cuda(), slots.int().cuda(), w.cuda(), out=out, add={"none": None, "apart": a.cuda(), "in place": out}[add])
+    torch.cuda.synchronize()
+    G.check()
+    assert gnq.read_device_error() == 0
+    rows = y.double()[slots.clamp(min=0)] * (w.double() * (slots >= 0))[..., None]
+    want, mag = rows.sum(1), rows.abs().sum(1)
+    if add != "none":
+        want, mag = want + a.double(), mag + a.double().abs()
+    # a term is rounded in its product, in its pair, in the sum of the pairs and with `add`: at most k + 1 times
+    err = (k + 2) * 2.0 ** -24 * mag
+    assert_within(out, want, err + rounding(want.abs() + err, ALL[O]), "out")
+
+
+# ---------------------------------------------------------------------------
+# the router
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,E,k", [(50001, 24, 8), (40000, 300, 8), (20003, 128, 32)])
+def test_route_places_long_chunks(gnq, M, E, k, dtype):
+    """More choices a warp than it keeps in registers: places wait in the slots."""
+    v = _logits(M, E, dtype, M, ties=True)
+    v[::11] = -float("inf")
+    v[3::13, 2:] = -float("inf")
+    G = Guarded()
+    out = (G((M, k), torch.int32), G((M, k), torch.float32), G((E + 1,), torch.int32), G((M, k), torch.int32))
+    gnq.expert_route(v.cuda(), k, out=out)
+    torch.cuda.synchronize()
+    G.check()
+    top = torch.sort(v.double() + 0.0, dim=1, descending=True, stable=True)
+    experts = torch.where(top.values[:, :k] == -float("inf"), -1, top.indices[:, :k]).int()
+    flat = experts.reshape(-1)
+    order = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    used = int((flat >= 0).sum())
+    slots = torch.full((M * k,), -1, dtype=torch.int32)
+    slots[order[:used]] = torch.arange(used, dtype=torch.int32)
+    offsets = torch.cat((torch.zeros(1, dtype=torch.int64), torch.bincount(flat[flat >= 0].long(), minlength=E).cumsum(0)))
+    assert torch.equal(out[0].cpu(), experts) and torch.equal(out[2].cpu(), offsets.int())
+    assert torch.equal(out[3].cpu(), slots.reshape(M, k))
+
+
+@pytest.mark.parametrize("M", [20, 1300])
+@pytest.mark.parametrize("E", [40, 256, 1000])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_route_nan_and_infinities_of_every_type(gnq, dtype, renormalize, E, M):
+    """NaN of either sign above +inf, its index deciding among equals; a token
+    that has one, or +inf, gets NaN weights, and no other token does."""
+    k, T = 4, ALL[dtype]
+    v = _logits(M, E, dtype, E)
+    clean = gnq.expert_route(v.cuda(), k, renormalize=renormalize)
+    nan = {"bf16": (0x7FC0, -0x3F), "fp16": (0x7E01, -0x1FF), "fp32": (0x7FC00001, -0x3FFFFF)}[dtype]
+    bits = v.view(torch.int32 if dtype == "fp32" else torch.int16)
+    bits[3, 9] = nan[0]
+    bits[4, 38] = nan[1]                      # negative
+    bits[8, 30], bits[8, 31] = nan[1], nan[0]
+    v[5, 2] = float("inf")
+    v[6, 1], v[6, 2], v[6, 3] = float("inf"), float("inf"), -float("inf")
+    v[7, 20] = float("inf")
+    bits[7, 39] = nan[1]
+    v[11] = -float("inf")
+    bits[11, 6] = nan[0]
+    v[12] = -float("inf")
+    v[12, 17] = torch.finfo(T).min
+    odd = torch.zeros(M, dtype=torch.bool)
+    odd[[3, 4, 5, 6, 7, 8, 11]] = True
+    assert torch.isnan(v).any(1).sum() == 5
+    experts, weights, offsets, slots = (t.cpu() for t in gnq.expert_route(v.cuda(), k, renormalize=renormalize))
+    e64, _, o64, s64 = route64(v, k, renormalize, 1.0)
+    assert torch.equal(experts, e64) and torch.equal(offsets, o64) and torch.equal(slots, s64)
+    assert torch.equal(torch.isnan(weights), odd[:, None] & (experts >= 0))
+    assert weights[11, 1:].tolist() == [0.0] * 3 and weights[12].tolist() == [1.0, 0.0, 0.0, 0.0]
+    keep = ~odd
+    keep[12] = False
+    assert torch.equal(weights[keep], clean[1].cpu()[keep])
+
+
+# ---------------------------------------------------------------------------
+# the way back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn])
+@pytest.mark.parametrize("counts,K", [("tiles", 320), ("few", 64), ("many", 64)])
+def test_dequantize_to_16_byte_alignment(gnq, counts, K, T):
+    """A result that is 16-byte but not 32-byte aligned has the same bits."""
+    offsets = offsets_of(COUNTS[counts])
+    R = offsets[-1] + 2
+    q, sf = (v.cuda() for v in random_rows(offsets, R, K, 3))
+    G = Guarded()
+    outs = G((R, K), T), G((R, K), T, shift=16)
+    assert outs[0].data_ptr() % 32 == 0 and outs[1].data_ptr() % 32 == 16
+    for out in outs:
+        gnq.expert_dequantize(q, sf, ints(offsets), fp32([3.0]), out=out)
+    torch.cuda.synchronize()
+    G.check()
+    assert (u8(outs[0]) == u8(outs[1])).all()
+
+
+# ---------------------------------------------------------------------------
+# quantization and products
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("counts,H,k", [("few", 64, 3), ("tiles", 192, 8), ("single", 2048, 5), ("many", 64, 32)])
+def test_quantize_activated_and_fanned_out(gnq, counts, H, k, act, dtype):
+    """The gated activation of a token, with the scale of each of its experts."""
+    offsets, slots, experts = _fan(COUNTS[counts], k, 2)
+    E, (M, k) = len(offsets) - 1, slots.shape
+    x = _values(M, 2 * H, DTYPES[dtype], M).cuda()
+    for shared in (False, True):
+        scales = [168.0] * E if shared else [50.0 + 13.0 * (e % 9) for e in range(E)]
+        G = Guarded()
+        out = G((M * k, H // 2), torch.uint8), G((scale_rows(M * k, E), H // 16), torch.float8_e4m3fn)
+        q, bs = gnq.expert_quantize(x, ints(offsets), fp32(scales[:1] if shared else scales), slots=slots.int().cuda(),
+                                    experts=experts.int().cuda(), act=act, out=out)
+        v = gnq.gated_act_quant(x, None, "none", act=act)[2].cpu()
+        torch.cuda.synchronize()
+        G.check()
+        y = torch.zeros(offsets[-1], H, dtype=v.dtype)
+        t, j = (slots >= 0).nonzero(as_tuple=True)
+        y[slots[t, j]] = v[t]
+        _check_packed(q, bs, y, scales, offsets, dtype)
+    assert gnq.read_device_error() == 0
+
+
+@pytest.mark.parametrize("N", [1, 8, 24, 40, 248, 264])
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float16, torch.float32])
+def test_pairs_of_few_columns(gnq, T, N):
+    """The pair kernel where its tile of 256 columns is clipped, in tile stores
+    (16-bit rows that are a multiple of 16 bytes) and without."""
+    gnq.set_linear_policy(2)
+    try:
+        for counts in ([1], [33, 0, 300], [31, 64, 449]):
+            _run_linear(gnq, counts, N, 320, T, seed=N)
+    finally:
+        gnq.set_linear_policy(0)
