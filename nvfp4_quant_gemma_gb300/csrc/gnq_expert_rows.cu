@@ -56,6 +56,7 @@ __device__ __forceinline__ int expert_from(const ExpertRows &x, int e, int m, in
 // grid, looks at all of them: no other waits for it.
 __device__ __forceinline__ void check_offsets(const ExpertRows &x) {
     bool bad = false;
+#pragma unroll 1
     for (int e = threadIdx.x; e <= x.E; e += NT) {
         const int o = ld_i32(x.offsets + e);
         bad |= o > x.R || (e == 0 ? o != 0 : o < ld_i32(x.offsets + e - 1));
@@ -289,8 +290,11 @@ struct ExpertDequantParams {
 
 // P pairs a thread: two where the output is small (65536 x 2048 to E4M3: 35 us, with
 // one 44, which is the instructions of the search and the addresses), else one.
+// Registers for eight CTAs on an SM where the output has 16 bits and for six to E4M3
+// (65536 x 2048: 51.7 and 34.3 us; 54.4 and 36.6 with the six and five that the
+// compiler's own choice leaves).
 template <int OUT, bool V8, int P>
-__global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
+__global__ void __launch_bounds__(NT, OUT == OUT_E4M3 ? 6 : OUT == OUT_FP32 ? 1 : 8) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
     if (blockIdx.x + 1 == gridDim.x) {
         pdl_wait();
         pdl_trigger();
