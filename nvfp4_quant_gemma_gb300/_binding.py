@@ -604,6 +604,12 @@ def _floats_ok(dev: int, t, n: int) -> bool:
     return t.dtype is _F32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
 
 
+def _is(dev: int, t, dtype, shape) -> bool:
+    """A tensor of the very shape: what the one-expression checks take of a
+    matrix, the step-by-step ones also what _matrix_ok and _result_ok admit."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
 def _matrix_ok(t, rows: int, cols: int) -> bool:
     """Whether the kernels, which index it with a row stride of `cols`, find a
     (rows, cols) matrix in the contiguous `t`: in rows of that width, or flat."""
@@ -680,17 +686,15 @@ def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
     k = int(k)
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be 1 .. {min(E, 32)}")
-    given = out is not None
-    if not given:
+    if out is None:
         kw = {"device": logits.device} if logits.is_cuda else {"pin_memory": True}
         out = (torch.empty((M, k), dtype=_I32, **kw), torch.empty((M, k), dtype=_F32, **kw),
                torch.empty(E + 1, dtype=_I32, **kw), torch.empty((M, k), dtype=_I32, **kw))
     experts, weights, offsets, slots = out
-    dev, n = logits.get_device(), M * k
+    dev, size = logits.get_device(), (M, k)
     try:
-        ok = (dev >= 0 and dev == _current_device() and _ints_ok(dev, experts, n) and _floats_ok(dev, weights, n)
-              and _ints_ok(dev, offsets, E + 1) and _ints_ok(dev, slots, n)
-              and (not given or (_result_ok(experts, M, k) and _result_ok(weights, M, k) and _result_ok(slots, M, k))))
+        ok = (dev >= 0 and dev == _current_device() and _is(dev, experts, _I32, size) and _is(dev, weights, _F32, size)
+              and _ints_ok(dev, offsets, E + 1) and _is(dev, slots, _I32, size))
     except AttributeError:
         ok = False
     if not ok:
@@ -751,7 +755,7 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
                                      and slots.get_device() == dev and experts.shape == slots.shape
                                      and experts.dtype is _I32 and experts.is_contiguous()
                                      and experts.get_device() == dev))
-              and q.dtype is _U8 and q.is_contiguous() and _result_ok(q, R, H // 2) and q.get_device() == dev
+              and q.dtype is _U8 and q.is_contiguous() and q.shape == (R, H // 2) and q.get_device() == dev
               and bs.dtype in (_E4M3, _U8) and bs.is_contiguous() and bs.nbytes >= rows * (H // 16)
               and bs.get_device() == dev)
     except (AttributeError, TypeError, ValueError, IndexError):
@@ -811,7 +815,7 @@ def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None,
               and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
               and (scale is None or (scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev))
               and _expert_packed_ok(dev, E, q, block_scale) and out.dtype in _OUT_TYPE
-              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and _result_ok(out, R, K)
+              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.shape == (R, K)
               and out.get_device() == dev)
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -857,11 +861,11 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
               and offsets.dim() == 1 and offsets.numel() == E + 1 and _ints_ok(dev, offsets, E + 1)
               and weight_q.dtype is _U8 and weight_q.is_contiguous() and weight_q.get_device() == dev
               and weight_block_scale.dtype in (_E4M3, _U8) and weight_block_scale.is_contiguous()
-              and _weight_scales_ok(weight_block_scale, E, (N + 127) // 128 * 128, half // 8)
+              and weight_block_scale.nbytes == E * ((N + 127) // 128) * 16 * half
               and weight_block_scale.get_device() == dev and (g == E or g == 1) and _floats_ok(dev, alpha, 1)
-              and out.is_contiguous() and _result_ok(out, R, N) and out.get_device() == dev
+              and out.is_contiguous() and out.shape == (R, N) and out.get_device() == dev
               and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous()
-                                    and _matrix_ok(bias, E, N) and bias.get_device() == dev)))
+                                    and bias.shape == (E, N) and bias.get_device() == dev)))
         per_expert = 1 if g == E else 0
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -911,11 +915,9 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
             out = torch.empty((M, H), dtype=y.dtype if add is None else add.dtype, device=y.device)
         ok = (dev >= 0 and dev == _current_device() and y.is_contiguous() and out.dtype in _OUT_TYPE
               and (out.dtype is y.dtype or y.dtype is _F32) and _OUT_TYPE[out.dtype] < 3 and _OUT_TYPE.get(y.dtype, 3) < 3
-              and _ints_ok(dev, slots, M * k) and _floats_ok(dev, weights, M * k)
-              and (weights.shape == slots.shape or _matrix_ok(weights, M, k))
-              and out.is_contiguous() and _result_ok(out, M, H) and out.get_device() == dev
-              and (add is None or (add.dtype is out.dtype and add.is_contiguous() and _matrix_ok(add, M, H)
-                                   and add.get_device() == dev)))
+              and slots.dtype is _I32 and slots.is_contiguous() and slots.get_device() == dev
+              and _is(dev, weights, _F32, (M, k)) and out.is_contiguous() and out.shape == (M, H)
+              and out.get_device() == dev and (add is None or _is(dev, add, out.dtype, (M, H))))
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
