@@ -277,7 +277,8 @@ int nvfp4_linear(const void *q, const void *block_scale, const void *w_q,
  * by expert: expert e owns rows offsets[e] .. offsets[e + 1] - 1 of the R rows
  * that a buffer holds; offsets are E + 1 int32 on the device, ascending from 0
  * to at most R, and are never read on the host.  Rows from offsets[E] on belong
- * to nobody: they are not read, and what is written leaves them as they were.
+ * to nobody: what they hold influences nothing, and what is written leaves them
+ * as they were.
  * Block scales keep the 128x4 layout, each expert's rows starting a 128-row
  * tile of their own, tile offsets[e] / 128 + e (rounded down): a buffer of
  * R / 128 + E tiles of 128 rows holds any split.  Bytes of a tile beyond an

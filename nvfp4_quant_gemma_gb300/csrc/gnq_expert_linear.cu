@@ -18,9 +18,9 @@
 //
 // What bounds it: the bytes of the weights that have rows, each read once.  64
 // tokens to 8 of 128 experts, N = 4096, K = 2048: 77 us of 73.7 at the copy rate (105
-// experts have rows); one token, N = 2048, K = 4096: 10.4 us of 5.6, launch, offsets,
-// first copy and last store; 301 tokens to 4 of 60, 1000 x 1088: 11.5 of 5.8, 480
-// tiles on 304 CTAs.
+// experts have rows), to fp32 78 of 75; one token, N = 2048, K = 4096: 10.4 us of 5.6,
+// launch, offsets, first copy and last store; 301 tokens to 4 of 60, 1000 x 1088: 11.5
+// of 5.8, 480 tiles on 304 CTAs.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -272,7 +272,9 @@ cudaError_t launch_expert_linear(const CUtensorMap &mw, const CUtensorMap &mx, c
 // to 1000 rows each, N of 512 to 8192, K of 512 to 4096) the choice loses 0.4 % on
 // average against the faster one, and more than 10 % on 3 (2 experts of 380 rows,
 // N = K = 4096: 17.4 us on single CTAs, 15.8 on pairs; 16 of 200 rows, N = 1024,
-// K = 2048: 11.3 and 12.4).
+// K = 2048: 11.3 and 12.4).  R, the rows that the buffers have room for, stands for
+// the rows that there are, which the host does not know: in all shapes timed the two
+// were the same, and a batch most of whose slots are -1 is taken for a full one.
 bool pairs_take(int64_t E, int64_t R, int64_t N, int64_t K) {
     if (K < 768) return false;
     const int64_t tiles = (N + 255) / 256 * std::max(E, R / 224);

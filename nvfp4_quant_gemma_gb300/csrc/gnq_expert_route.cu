@@ -19,11 +19,12 @@
 // chunk places its choices as above.  (Where that makes fewer chunks than SMs,
 // the counting is a step of its own.)
 //
-// What bounds it: picking is instruction issue (420 warp instructions a token of 256
-// fp32 logits), placing latency.  16384 tokens: 256 fp32 logits, 8 choices 20 us, 128
-// bf16 logits 17, 64 and 2 choices 13.9; 65536 of the first 56 us (1.2 TB/s of logits);
-// one token 2.4 us.  One CTA or cluster that places all 131072 choices took 22 us by
-// itself, the chunks' two steps take 9.
+// What bounds it: picking is the integer pipes (420 warp instructions a token of 256
+// fp32 logits, 5.7 us for 16384 tokens at every issue slot, take 10: 58 % of the slots,
+// and a full pipe is what warps wait for most), placing latency.  16384 tokens: 256 fp32
+// logits, 8 choices 20 us, 128 bf16 logits 17, 64 and 2 choices 13.9; 65536 of the first
+// 56 us (1.2 TB/s of logits); one token 2.4 us.  One CTA or cluster that places all
+// 131072 choices took 22 us by itself, the chunks' two steps take 9.
 #include <algorithm>
 
 #include "gemma_nq.h"
@@ -152,7 +153,7 @@ __device__ __noinline__ int pick_exact(const uint32_t (&key)[NV], int e0, int de
 // fp32 ones lose their low 8 bits (10 from 512 experts on): if two neighbours
 // in the order, down to the first that is not chosen, are equal in what is
 // left, the token is picked again from exact keys (16384 x 256 fp32 logits:
-// 15.5 us with exact keys throughout, all instruction issue).  So is one with a
+// 15.5 us with exact keys throughout).  So is one with a
 // NaN, whose key the first look does not make (their sum is one, too).
 // `b` holds the lane's logits.  Up to eight a lane are put in falling order (Batcher's merge
 // exchange), so that a choice is a maximum over the lanes' first ones and a

@@ -15,10 +15,13 @@
 //
 // A token that goes to k experts is read once and written k times, each time
 // with the codes of that expert's scale.  Measured: bf16 8192 x 4096 to 8 experts
-// each 50 us (32 at the copy rate: 75 instructions per block and expert, 70 % of
-// the issue slots), 49 with one scale for all; SiLU of 65536 x 2048 104 us (100),
-// tanh-GELU 108, no activation 52 (51); back to bf16 51 us (51), fp32 114 (90), E4M3
-// 35 (31); combination of 8192 tokens' 8 rows x 4096 102 us (99): HBM.
+// each 50.5 us (32 at the copy rate), and 48.6 with one scale for all, which encodes a
+// block once in place of eight times: not the instructions (62 and 47 % of the issue
+// slots) but the stores, whose path out of the SM is the busiest part in both, at two
+// thirds: a store of scales fills a sector with four bytes, 134 MB leave the SMs for
+// 75 MB of 4096 tokens.  SiLU of 65536 x 2048 104 us (100), tanh-GELU 109, no
+// activation 52 (51); back to bf16 52 us (51), fp32 114 (90), E4M3 34 (31);
+// combination of 8192 tokens' 8 rows x 4096 102 us (99), of fp32 rows 195 (197): HBM.
 #include "gemma_nq.h"
 #include "gnq_elementwise.cuh"
 #include "gnq_expert.cuh"
