@@ -596,20 +596,6 @@ def expert_scale_rows(R: int, E: int) -> int:
     return (R // 128 + E) * 128
 
 
-def _ints_ok(dev: int, t, n: int) -> bool:
-    return t.dtype is _I32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
-
-
-def _floats_ok(dev: int, t, n: int) -> bool:
-    return t.dtype is _F32 and t.is_contiguous() and t.numel() >= n and t.get_device() == dev
-
-
-def _is(dev: int, t, dtype, shape) -> bool:
-    """A tensor of the very shape: what the one-expression checks take of a
-    matrix, the step-by-step ones also what _matrix_ok and _result_ok admit."""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
-
-
 def _matrix_ok(t, rows: int, cols: int) -> bool:
     """Whether the kernels, which index it with a row stride of `cols`, find a
     (rows, cols) matrix in the contiguous `t`: in rows of that width, or flat."""
@@ -691,10 +677,15 @@ def expert_route(logits, k, renormalize=True, scale=1.0, out=None, stream=None):
         out = (torch.empty((M, k), dtype=_I32, **kw), torch.empty((M, k), dtype=_F32, **kw),
                torch.empty(E + 1, dtype=_I32, **kw), torch.empty((M, k), dtype=_I32, **kw))
     experts, weights, offsets, slots = out
-    dev, size = logits.get_device(), (M, k)
+    dev = logits.get_device()
     try:
-        ok = (dev >= 0 and dev == _current_device() and _is(dev, experts, _I32, size) and _is(dev, weights, _F32, size)
-              and _ints_ok(dev, offsets, E + 1) and _is(dev, slots, _I32, size))
+        ok = (dev >= 0 and dev == _current_device()
+              and experts.dtype is _I32 and experts.is_contiguous() and experts.get_device() == dev
+              and weights.dtype is _F32 and weights.is_contiguous() and weights.get_device() == dev
+              and slots.dtype is _I32 and slots.is_contiguous() and slots.get_device() == dev
+              and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev
+              and offsets.numel() > E and (experts.shape == weights.shape == slots.shape == (M, k)
+                                           or all(_result_ok(t, M, k) for t in (experts, weights, slots))))
     except AttributeError:
         ok = False
     if not ok:
@@ -739,8 +730,9 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
     k, R = 0, M
     try:
         E = offsets.numel() - 1
+        tokens = M
         if slots is not None:
-            k = slots.shape[1]
+            tokens, k = slots.shape
             R = M * k
         rows = (R // 128 + E) * 128
         if out is None and dev >= 0:
@@ -751,13 +743,13 @@ def expert_quantize(x, offsets, scale, slots=None, experts=None, act=None, out=N
         ok = (dev >= 0 and dev == _current_device() and E > 0 and (g == E or g == 1)
               and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
               and scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev
-              and (slots is None or (slots.shape == (M, k) and slots.dtype is _I32 and slots.is_contiguous()
+              and (slots is None or (tokens == M and slots.dtype is _I32 and slots.is_contiguous()
                                      and slots.get_device() == dev and experts.shape == slots.shape
                                      and experts.dtype is _I32 and experts.is_contiguous()
                                      and experts.get_device() == dev))
-              and q.dtype is _U8 and q.is_contiguous() and q.shape == (R, H // 2) and q.get_device() == dev
-              and bs.dtype in (_E4M3, _U8) and bs.is_contiguous() and bs.nbytes >= rows * (H // 16)
-              and bs.get_device() == dev)
+              and q.dtype is _U8 and q.is_contiguous() and q.get_device() == dev
+              and (q.shape == (R, H // 2) or _result_ok(q, R, H // 2)) and bs.dtype in (_E4M3, _U8)
+              and bs.is_contiguous() and bs.nbytes >= rows * (H // 16) and bs.get_device() == dev)
     except (AttributeError, TypeError, ValueError, IndexError):
         ok = False
     if not ok:
@@ -793,8 +785,7 @@ def _expert_packed(q, block_scale, E: int):
     return R, 2 * half
 
 
-def _expert_packed_ok(dev: int, E: int, q, sf) -> bool:
-    R, half = q.shape
+def _expert_packed_ok(dev: int, E: int, R: int, half: int, q, sf) -> bool:
     return (q.dtype is _U8 and q.is_contiguous() and q.get_device() == dev and sf.dtype in (_E4M3, _U8)
             and sf.is_contiguous() and sf.nbytes >= (R // 128 + E) * 16 * half and sf.get_device() == dev)
 
@@ -814,9 +805,9 @@ def expert_dequantize(q, block_scale, offsets, scale=None, dtype=None, out=None,
         ok = (dev >= 0 and dev == _current_device() and E > 0 and (g == E or g == 1)
               and offsets.dtype is _I32 and offsets.is_contiguous() and offsets.get_device() == dev and offsets.dim() == 1
               and (scale is None or (scale.dtype is _F32 and scale.is_contiguous() and scale.get_device() == dev))
-              and _expert_packed_ok(dev, E, q, block_scale) and out.dtype in _OUT_TYPE
-              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.shape == (R, K)
-              and out.get_device() == dev)
+              and _expert_packed_ok(dev, E, R, half, q, block_scale) and out.dtype in _OUT_TYPE
+              and (dtype is None or out.dtype is dtype) and out.is_contiguous() and out.get_device() == dev
+              and (out.shape == (R, K) or _result_ok(out, R, K)))
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
@@ -851,21 +842,25 @@ def nvfp4_expert_linear(q, block_scale, weight_q, weight_block_scale, alpha, off
     try:
         dev = q.get_device()
         E, N, half = weight_q.shape
-        R, K = q.shape[0], 2 * half
+        R, wide = q.shape
+        K = 2 * half
         if out is None and dev >= 0:
             out = torch.empty((R, N), dtype=dtype or torch.bfloat16, device=q.device)
         ot = _OUT_TYPE.get(out.dtype, 3)
         g = alpha.numel()
-        ok = (ot < 3 and q.shape[1] == half and dev >= 0 and dev == _current_device()
-              and (dtype is None or out.dtype is dtype) and _expert_packed_ok(dev, E, q, block_scale)
-              and offsets.dim() == 1 and offsets.numel() == E + 1 and _ints_ok(dev, offsets, E + 1)
+        ok = (ot < 3 and wide == half and dev >= 0 and dev == _current_device()
+              and (dtype is None or out.dtype is dtype) and _expert_packed_ok(dev, E, R, half, q, block_scale)
+              and offsets.dim() == 1 and offsets.numel() == E + 1 and offsets.dtype is _I32
+              and offsets.is_contiguous() and offsets.get_device() == dev
               and weight_q.dtype is _U8 and weight_q.is_contiguous() and weight_q.get_device() == dev
               and weight_block_scale.dtype in (_E4M3, _U8) and weight_block_scale.is_contiguous()
-              and weight_block_scale.nbytes == E * ((N + 127) // 128) * 16 * half
-              and weight_block_scale.get_device() == dev and (g == E or g == 1) and _floats_ok(dev, alpha, 1)
-              and out.is_contiguous() and out.shape == (R, N) and out.get_device() == dev
+              and (weight_block_scale.nbytes == E * ((N + 127) // 128) * 16 * half
+                   or _weight_scales_ok(weight_block_scale, E, (N + 127) // 128 * 128, half // 8))
+              and weight_block_scale.get_device() == dev and (g == E or g == 1)
+              and alpha.dtype is _F32 and alpha.is_contiguous() and alpha.get_device() == dev
+              and out.is_contiguous() and out.get_device() == dev and (out.shape == (R, N) or _result_ok(out, R, N))
               and (bias is None or (ot < 2 and bias.dtype is out.dtype and bias.is_contiguous()
-                                    and bias.shape == (E, N) and bias.get_device() == dev)))
+                                    and bias.get_device() == dev and (bias.shape == (E, N) or _matrix_ok(bias, E, N)))))
         per_expert = 1 if g == E else 0
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -916,8 +911,11 @@ def expert_combine(y, slots, weights, add=None, out=None, stream=None):
         ok = (dev >= 0 and dev == _current_device() and y.is_contiguous() and out.dtype in _OUT_TYPE
               and (out.dtype is y.dtype or y.dtype is _F32) and _OUT_TYPE[out.dtype] < 3 and _OUT_TYPE.get(y.dtype, 3) < 3
               and slots.dtype is _I32 and slots.is_contiguous() and slots.get_device() == dev
-              and _is(dev, weights, _F32, (M, k)) and out.is_contiguous() and out.shape == (M, H)
-              and out.get_device() == dev and (add is None or _is(dev, add, out.dtype, (M, H))))
+              and weights.dtype is _F32 and weights.is_contiguous() and weights.get_device() == dev
+              and (weights.shape == slots.shape or _matrix_ok(weights, M, k))
+              and out.is_contiguous() and out.get_device() == dev and (out.shape == (M, H) or _result_ok(out, M, H))
+              and (add is None or (add.dtype is out.dtype and add.is_contiguous() and add.get_device() == dev
+                                   and (add.shape == (M, H) or _matrix_ok(add, M, H)))))
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
