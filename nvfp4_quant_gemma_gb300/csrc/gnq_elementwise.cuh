@@ -109,16 +109,20 @@ enum { OUT_BF16 = 0, OUT_FP16 = 1, OUT_FP32 = 2, OUT_E4M3 = 3 };
 // Two neighbouring blocks (16 bytes of codes, two scale bytes) to values from
 // element `at` of `out`, in whole 32-byte sectors (V8) or 16-byte stores.  A
 // block's factor is one IEEE quotient of its scale and the global one; value =
-// RN(code * factor), then one rounding to the output type.
-template <int OUT, bool V8>
+// RN(code * factor), then one rounding to the output type.  EARLY: both quotients
+// before a code is unpacked, so that no values wait in registers meanwhile.
+template <int OUT, bool V8, bool EARLY = false>
 __device__ __forceinline__ void nvfp4_pair_out(void *out, int64_t at, const uint4 &code, uint32_t sf, float g) {
     uint4 e4m3[2];  // E4M3: both blocks leave together
+    auto quotient = [&](int h) { return __fdiv_rn(e4m3_value(sf >> (8 * h) & 0xFF), g); };
+    [[maybe_unused]] float factor[2];
+    if constexpr (EARLY) factor[0] = quotient(0), factor[1] = quotient(1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float f[16];
         e2m1_values8(h ? code.z : code.x, &f[0]);
         e2m1_values8(h ? code.w : code.y, &f[8]);
-        mul_arr_s<16>(f, __fdiv_rn(e4m3_value(sf >> (8 * h) & 0xFF), g));
+        mul_arr_s<16>(f, EARLY ? factor[h] : quotient(h));
         uint4 w[4];
         constexpr int N = OUT == OUT_FP32 ? 4 : OUT == OUT_E4M3 ? 1 : 2;  // 16-byte words of a block
         if constexpr (OUT == OUT_FP32) {

@@ -20,7 +20,7 @@
 // slots) but the stores, whose path out of the SM is the busiest part in both, at two
 // thirds: a store of scales fills a sector with four bytes, 134 MB leave the SMs for
 // 75 MB of 4096 tokens.  SiLU of 65536 x 2048 104 us (100), tanh-GELU 109, no
-// activation 52 (51); back to bf16 52 us (51), fp32 114 (90), E4M3 34 (31);
+// activation 52 (51); back to bf16 51 us (51), fp32 114 (90), E4M3 32 (31);
 // combination of 8192 tokens' 8 rows x 4096 102 us (99), of fp32 rows 195 (197): HBM.
 #include "gemma_nq.h"
 #include "gnq_elementwise.cuh"
@@ -291,13 +291,13 @@ struct ExpertDequantParams {
     int ppr, Kp4;   // of a row; scale tiles per 128 rows
 };
 
-// P pairs a thread: two where the output is small (65536 x 2048 to E4M3: 35 us, with
-// one 44, which is the instructions of the search and the addresses), else one.
-// Registers for eight CTAs on an SM where the output has 16 bits and for six to E4M3
-// (65536 x 2048: 51.7 and 34.3 us; 54.4 and 36.6 with the six and five that the
-// compiler's own choice leaves).
+// P pairs a thread: two where the output is small (65536 x 2048 to E4M3: 32 us, with
+// one 40, which is the instructions of the search and the addresses), else one.
+// Both of a pair's quotients come first (EARLY): 32 registers then hold it, where
+// values that wait for the second one take 37, and 44 to E4M3 (65536 x 2048: bf16 51.1
+// us, with six CTAs on an SM in place of eight 54.4; E4M3 32.4 and 36.6).
 template <int OUT, bool V8, int P>
-__global__ void __launch_bounds__(NT, OUT == OUT_E4M3 ? 6 : OUT == OUT_FP32 ? 1 : 8) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
+__global__ void __launch_bounds__(NT) expert_dequant_kernel(const __grid_constant__ ExpertDequantParams p) {
     if (blockIdx.x + 1 == gridDim.x) {
         pdl_wait();
         pdl_trigger();
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NT, OUT == OUT_E4M3 ? 6 : OUT == OUT_FP32 ? 1 
     const uint32_t sf = P == 2 ? (uint32_t)ld_i32(reinterpret_cast<const int32_t *>(scales)) : ld_u16(scales);
     const float g = p.x.scale ? ld_f32(p.x.scale + e * p.x.scale_stride) : 1.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) nvfp4_pair_out<OUT, V8>(p.out, (P * at + i) * 32, code[i], sf >> 16 * i, g);
+    for (int i = 0; i < P; ++i) nvfp4_pair_out<OUT, V8, true>(p.out, (P * at + i) * 32, code[i], sf >> 16 * i, g);
 }
 
 template <int OUT> cudaError_t launch_expert_dequant(const ExpertDequantParams &p, cudaStream_t s) {
